@@ -32,6 +32,7 @@
  *    U_b is U[(b*block + i)*block + j]; a row vector x_b of block b is rotated as (x_b U_b) H_B, with
  *    H_B the natural-order Sylvester Hadamard matrix scaled by 1/sqrt(block).
  *    Packed int4: uint8 [rows][K/2], two's-complement nibbles, low nibble = even k.
+ *    The single-token calls at the end also take W4A4_BF16 where they say so.
  *    Scales are fp32. Y and residual are IEEE binary16 bit patterns, row-major with strides ldy/ldr.
  *  - block must be a power of two in [1, 256] dividing K, and K must be even.
  *  - Return value: W4A4_OK or one of the W4A4_ERR_* codes; w4a4_last_error() then describes the
@@ -60,7 +61,7 @@ enum w4a4_status {
     W4A4_ERR_HIP = 7          /* a HIP runtime call or kernel launch failed */
 };
 
-enum w4a4_dtype { W4A4_F16 = 0, W4A4_F32 = 1 };
+enum w4a4_dtype { W4A4_F16 = 0, W4A4_F32 = 1, W4A4_BF16 = 2 };
 
 enum w4a4_epilogue {
     W4A4_EPI_NONE = 0,     /* Y = fp16(dequant) */
@@ -375,6 +376,36 @@ int w4a4_pack_weights_gptq(const void *W, int w_dtype, int N, int K, int64_t ldw
                            const int32_t *perm, const float *U, const double *Hf,
                            const uint8_t *dead, uint8_t *wq, float *w_scale, void *rot, void *ws,
                            size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Linears with group-scaled 4-bit weights and unquantized activations, for the language backbone's
+ * single tokens: a pass over one or a few tokens reads every weight once and is bound by the weight
+ * bytes, so quantizing the activations would buy nothing [vnrobo.com "Vi sao W4A4 kho hon W4A16?":
+ * weight-only 4-bit is the easier setting].
+ *   y[m][n] = sum_g s[g][n] * sum_{k in group g} x[m][k] c[n][k],  codes c in [-8, 7],
+ * groups of `group` consecutive k (32, 64, 128 or 256, else W4A4_ERR_UNSUPPORTED; K % group == 0,
+ * else W4A4_ERR_SHAPE), s IEEE binary16 stored group-major [K/group][N]. Products are exact, sums are
+ * fp32, one rounding at the end.
+ *  - Weight operand wt (w4a4_w4g_operand_bytes(N, K) bytes, 16-byte aligned): tiles of 16 rows x 128
+ *    k, 1 KB each, tile (n/16, k/128) at ((n/16) * ceil(K/128) + k/128) * 1024. In a tile the run of
+ *    eight codes k = 32 j + 8 g + 0..7 of row r is the dword at (g * 16 + r) * 16 + 4 j; nibble i of
+ *    it (bits 4i..4i+3) holds code + 8 of run element 2 i for i < 4 and 2 (i - 4) + 1 for i >= 4.
+ *    Rows past N and k past K hold code 0.
+ *  - w4a4_pack_weights_w4g: round to nearest per group of W (fp16, fp32 or bf16): s = fp16(fp32(max
+ *    |w| / 7)), 1 for a group of zeros, and held inside fp16's range (2^-24 below, 65504 above);
+ *    c = clamp(rint(fp32(w / s)), -8, 7). W must be finite.
+ *  - w4a4_codes_to_w4g: packed int4 codes [N][K/2] of any other solver -> wt (K % 32 == 0).
+ *  - w4a4_gemv_w4g: the product, for any M (M == 0 is a valid empty call). X fp16, fp32 or bf16 with
+ *    any row stride; Y and residual fp16, for bf16 X bf16. Epilogues as in w4a4_gemm (residual is
+ *    added to the fp32 sum; it may be Y itself). No workspace.
+ * ------------------------------------------------------------------------------------------- */
+size_t w4a4_w4g_operand_bytes(int N, int K);
+int w4a4_pack_weights_w4g(const void *W, int w_dtype, int N, int K, int64_t ldw, int group,
+                          uint8_t *wt, uint16_t *w_scale, hipStream_t stream);
+int w4a4_codes_to_w4g(const uint8_t *codes, int N, int K, uint8_t *wt, hipStream_t stream);
+int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
+                  const uint16_t *w_scale, int group, int N, uint16_t *Y, int64_t ldy, int epilogue,
+                  const uint16_t *residual, int64_t ldr, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Diagnostics (host only).

@@ -12,7 +12,7 @@ LIB_PATH = os.path.join(PKG, "libw4a4.so")
 
 W4A4_OK, W4A4_ERR_ARG, W4A4_ERR_SHAPE, W4A4_ERR_STEP_RANGE = 0, 1, 2, 3
 W4A4_ERR_UNSUPPORTED, W4A4_ERR_ALIGN, W4A4_ERR_WORKSPACE, W4A4_ERR_HIP = 4, 5, 6, 7
-W4A4_F16, W4A4_F32 = 0, 1
+W4A4_F16, W4A4_F32, W4A4_BF16 = 0, 1, 2
 EPI_NONE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -72,6 +72,10 @@ SIGNATURES = {
     "w4a4_pack_gptq_workspace_bytes": (_sz, [_i, _i, _i]),
     "w4a4_pack_weights_gptq": (_i, [_vp, _i, _i, _i, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     _sz, _vp]),
+    "w4a4_w4g_operand_bytes": (_sz, [_i, _i]),
+    "w4a4_pack_weights_w4g": (_i, [_vp, _i, _i, _i, _i64, _i, _vp, _vp, _vp]),
+    "w4a4_codes_to_w4g": (_i, [_vp, _i, _i, _vp, _vp]),
+    "w4a4_gemv_w4g": (_i, [_vp, _i, _i, _i, _i64, _vp, _vp, _i, _i, _vp, _i64, _i, _vp, _i64, _vp]),
     "w4a4_last_error": (ctypes.c_char_p, []),
     "w4a4_status_string": (ctypes.c_char_p, [_i]),
     "w4a4_abi_version": (_i, []),
@@ -470,3 +474,108 @@ def pack_weights_gptq(W, perm, U, block: int, Hf, dead=None):
                                        _p(U), _p(Hf), _p(dead), _p(wq), _p(w_scale), _p(rot), _p(ws),
                                        nb, _stream()))
     return wq, w_scale, rot
+
+
+# ---------------------------------------------------------------------------------------------
+# Single-token path: group-scaled 4-bit linears. These calls run once per linear and token, so the
+# Python side is kept short: raw pointers as integers, and one look at the current device. They run
+# on the tensors' own device and on that device's current stream.
+# ---------------------------------------------------------------------------------------------
+
+def _code16(t) -> int:
+    """W4A4_* code of an fp16, bf16 or fp32 tensor (the calls that take bf16)."""
+    torch = _torch()
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return W4A4_BF16
+    if dt is torch.float16:
+        return W4A4_F16
+    if dt is torch.float32:
+        return W4A4_F32
+    raise TypeError(f"unsupported dtype {dt}")
+
+
+def _launch(fn, tensors, *args):
+    """fn(*args, stream) on the tensors' device and its current stream. Every tensor must be on that
+    one GPU."""
+    torch = _torch()
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"expected GPU tensors, got one on {dev}")
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(i).cuda_stream)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, torch.cuda.current_stream(i).cuda_stream)
+    if rc != W4A4_OK:
+        check(rc)
+
+
+def _ld(t) -> int:
+    """Row stride of a 2-D tensor (the row length where there is only one row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _want(cond, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def pack_weights_w4g(W, group: int):
+    """Round-to-nearest int4 codes of W [N, K] with one fp16 scale per `group` consecutive k. Returns
+    (wt uint8 [w4a4_w4g_operand_bytes], w_scale fp16 [K / group, N])."""
+    torch = _torch()
+    N, K = W.shape
+    L = lib()
+    wt = torch.empty(L.w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=W.device)
+    w_scale = torch.empty((max(K // group, 1) if group > 0 else 1, N), dtype=torch.float16, device=W.device)
+    _launch(L.w4a4_pack_weights_w4g, (W,), W.data_ptr(), _code16(W), N, K, _row_stride(W), group,
+            wt.data_ptr(), w_scale.data_ptr())
+    return wt, w_scale
+
+
+def codes_to_w4g(codes, K: int):
+    """The operand of gemv_w4g from packed int4 codes [N, K / 2] (as pack_weights_gptq's wq)."""
+    torch = _torch()
+    N = codes.shape[0]
+    _want(codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape == (N, K // 2),
+          "codes must be contiguous uint8 [N, K / 2]")
+    L = lib()
+    wt = torch.empty(L.w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=codes.device)
+    _launch(L.w4a4_codes_to_w4g, (codes,), codes.data_ptr(), N, K, wt.data_ptr())
+    return wt
+
+
+def gemv_w4g(X, wt, w_scale, Y=None, epilogue: int = EPI_NONE, residual=None):
+    """Y [M, N] = X [M, K] times the group-scaled 4-bit weights (wt, w_scale [K / group, N]), with an
+    epilogue. X fp16, fp32 or bf16; Y and residual fp16, for bf16 X bf16."""
+    torch = _torch()
+    M, K = X.shape
+    groups, N = w_scale.shape
+    dt = _code16(X)
+    ydt = torch.bfloat16 if dt == W4A4_BF16 else torch.float16
+    L = lib()
+    _want(X.stride(1) == 1 or K == 1, "X must have unit column stride")
+    _want(groups > 0 and K % groups == 0, f"K = {K} does not hold {groups} groups")
+    _want(w_scale.dtype is torch.float16 and w_scale.is_contiguous(), "w_scale must be contiguous fp16")
+    _want(wt.dtype is torch.uint8 and wt.is_contiguous()
+          and wt.numel() == ((N + 15) // 16) * ((K + 127) // 128) * 1024, "wt does not hold [N, K] weights")
+    if Y is None:
+        Y = torch.empty((M, N), dtype=ydt, device=X.device)
+    else:
+        _want(Y.dtype is ydt and Y.shape == (M, N) and Y.stride(1) == 1, f"Y must be {ydt} [M, N]")
+    if residual is None:
+        _launch(L.w4a4_gemv_w4g, (X, wt, w_scale, Y), X.data_ptr(), dt, M, K, _ld(X),
+                wt.data_ptr(), w_scale.data_ptr(), K // groups, N, Y.data_ptr(), _ld(Y),
+                epilogue, None, 0)
+    else:
+        _want(residual.dtype is ydt and residual.shape == (M, N) and residual.stride(1) == 1,
+              f"residual must be {ydt} [M, N]")
+        _launch(L.w4a4_gemv_w4g, (X, wt, w_scale, Y, residual), X.data_ptr(), dt, M, K,
+                _ld(X), wt.data_ptr(), w_scale.data_ptr(), K // groups, N, Y.data_ptr(),
+                _ld(Y), epilogue, residual.data_ptr(), _ld(residual))
+    return Y

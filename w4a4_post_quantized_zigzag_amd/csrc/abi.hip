@@ -54,13 +54,15 @@ static int ok()
 
 static bool pow2_block(int B) { return B >= 1 && B <= 256 && (B & (B - 1)) == 0; }
 
-static int check_dtype(int dt, const char *name)
+// bf16: whether the call takes W4A4_BF16 (only the single-token calls and their weight pack do)
+static int check_dtype(int dt, const char *name, bool bf16 = false)
 {
-    if (dt != W4A4_F16 && dt != W4A4_F32) return fail(W4A4_ERR_ARG, "%s dtype %d unknown", name, dt);
+    if (dt != W4A4_F16 && dt != W4A4_F32 && !(bf16 && dt == W4A4_BF16))
+        return fail(W4A4_ERR_ARG, "%s dtype %d unknown", name, dt);
     return W4A4_OK;
 }
 
-static size_t dtype_bytes(int dt) { return dt == W4A4_F16 ? 2 : 4; }
+static size_t dtype_bytes(int dt) { return dt == W4A4_F32 ? 4 : 2; }
 
 static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -76,9 +78,10 @@ static int check_kb(int K, int B)
     return W4A4_OK;
 }
 
-static int check_matrix(const void *A, int dt, int rows, int K, int64_t ld, const char *name)
+static int check_matrix(const void *A, int dt, int rows, int K, int64_t ld, const char *name,
+                        bool bf16 = false)
 {
-    int rc = check_dtype(dt, name);
+    int rc = check_dtype(dt, name, bf16);
     if (rc) return rc;
     if (rows < 0) return fail(W4A4_ERR_ARG, "%s rows = %d negative", name, rows);
     if (ld < K) return fail(W4A4_ERR_SHAPE, "%s leading dimension %lld < K = %d", name,
@@ -999,6 +1002,77 @@ int w4a4_pack_weights_gptq(const void *W, int w_dtype, int N, int K, int64_t ldw
         return rc;
     if ((rc = launch_gptq_sweep(Wr, N, K, Hf, dead, rowmax, codes, w_scale, stream))) return rc;
     if ((rc = launch_pack_codes(codes, N, K, wq, stream))) return rc;
+    return ok();
+}
+
+// ------------------------------------------------------------------ group-scaled 4-bit linears
+
+// group = 32 << *gshift, and K a positive multiple of it
+static int check_group(int N, int K, int group, int *gshift)
+{
+    if (group != 32 && group != 64 && group != 128 && group != 256)
+        return fail(W4A4_ERR_UNSUPPORTED, "group %d is not 32, 64, 128 or 256", group);
+    if (N <= 0) return fail(W4A4_ERR_ARG, "N = %d must be positive", N);
+    if (K <= 0) return fail(W4A4_ERR_ARG, "K = %d must be positive", K);
+    if (K % group) return fail(W4A4_ERR_SHAPE, "K = %d is not a multiple of the group %d", K, group);
+    if (K > (1 << 23) || N > (1 << 24))
+        return fail(W4A4_ERR_UNSUPPORTED, "N = %d, K = %d above 2^24, 2^23", N, K);
+    *gshift = group == 32 ? 0 : group == 64 ? 1 : group == 128 ? 2 : 3;
+    return W4A4_OK;
+}
+
+size_t w4a4_w4g_operand_bytes(int N, int K)
+{
+    if (N <= 0 || K <= 0) return 0;
+    return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128) * 1024;
+}
+
+int w4a4_pack_weights_w4g(const void *W, int w_dtype, int N, int K, int64_t ldw, int group,
+                          uint8_t *wt, uint16_t *w_scale, hipStream_t stream)
+{
+    int rc, gshift;
+    if ((rc = check_group(N, K, group, &gshift))) return rc;
+    if ((rc = check_matrix(W, w_dtype, N, K, ldw, "W", true))) return rc;
+    if (!wt || !w_scale) return fail(W4A4_ERR_ARG, "wt and w_scale are required");
+    if (!aligned(wt, 16) || !aligned(w_scale, 2))
+        return fail(W4A4_ERR_ALIGN, "wt must be 16-byte and w_scale 2-byte aligned");
+    if ((rc = launch_pack_w4g(W, w_dtype, N, K, ldw, gshift, wt, w_scale, stream))) return rc;
+    return ok();
+}
+
+int w4a4_codes_to_w4g(const uint8_t *codes, int N, int K, uint8_t *wt, hipStream_t stream)
+{
+    int rc, gshift;
+    if ((rc = check_group(N, K, 32, &gshift))) return rc;
+    if (!codes || !wt) return fail(W4A4_ERR_ARG, "codes and wt are required");
+    if (!aligned(wt, 16)) return fail(W4A4_ERR_ALIGN, "wt must be 16-byte aligned");
+    if ((rc = launch_codes_to_w4g(codes, N, K, wt, stream))) return rc;
+    return ok();
+}
+
+int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
+                  const uint16_t *w_scale, int group, int N, uint16_t *Y, int64_t ldy, int epilogue,
+                  const uint16_t *residual, int64_t ldr, hipStream_t stream)
+{
+    int rc, gshift;
+    if ((rc = check_group(N, K, group, &gshift))) return rc;
+    if ((rc = check_matrix(X, x_dtype, M, K, ldx, "X", true))) return rc;
+    if (!wt || !w_scale) return fail(W4A4_ERR_ARG, "wt and w_scale are required");
+    if (!aligned(wt, 16) || !aligned(w_scale, 2))
+        return fail(W4A4_ERR_ALIGN, "wt must be 16-byte and w_scale 2-byte aligned");
+    if (epilogue != W4A4_EPI_NONE && epilogue != W4A4_EPI_GELU && epilogue != W4A4_EPI_RESIDUAL)
+        return fail(W4A4_ERR_ARG, "epilogue %d unknown", epilogue);
+    if (ldy < N) return fail(W4A4_ERR_SHAPE, "ldy = %lld < N = %d", (long long)ldy, N);
+    if (epilogue == W4A4_EPI_RESIDUAL && ldr < N)
+        return fail(W4A4_ERR_SHAPE, "ldr = %lld < N = %d", (long long)ldr, N);
+    if (M > (1 << 21)) return fail(W4A4_ERR_UNSUPPORTED, "M = %d above 2^21", M);
+    if (M == 0) return ok();
+    if (!Y) return fail(W4A4_ERR_ARG, "Y is NULL");
+    if (epilogue == W4A4_EPI_RESIDUAL && !residual) return fail(W4A4_ERR_ARG, "residual is NULL");
+    if (!aligned(Y, 2) || !aligned(residual, 2)) return fail(W4A4_ERR_ALIGN, "Y / residual misaligned");
+    if ((rc = launch_gemv_w4g(X, x_dtype, M, K, ldx, wt, w_scale, gshift, N, Y, ldy, epilogue,
+                              residual, ldr, stream)))
+        return rc;
     return ok();
 }
 

@@ -219,6 +219,14 @@ size_t gemm_f6_workspace(int M, int N, int K);
 int launch_gemm_f6(const uint8_t *xf, const uint8_t *wf, int M, int N, int K,
                    const GemmEpilogue &epi, void *ws, size_t ws_bytes, hipStream_t s);
 
+// group-scaled 4-bit linears (k_w4g.hip); group = 32 << gshift
+int launch_pack_w4g(const void *W, int wdt, int N, int K, int64_t ldw, int gshift, uint8_t *wt,
+                    uint16_t *w_scale, hipStream_t s);
+int launch_codes_to_w4g(const uint8_t *codes, int N, int K, uint8_t *wt, hipStream_t s);
+int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
+                    const uint16_t *w_scale, int gshift, int N, uint16_t *Y, int64_t ldy, int epilogue,
+                    const uint16_t *residual, int64_t ldr, hipStream_t s);
+
 // calibration (k_calib.hip)
 size_t zigzag_workspace(int K);
 int launch_zigzag(const void *W, int wdt, int N, int K, int64_t ldw, int B, int32_t *perm,
