@@ -408,6 +408,56 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
                   const uint16_t *residual, int64_t ldr, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Between QKV and O for single tokens [gist.science "Metodologia": the language backbone's linears
+ * are the quantized ones; its attention stays in 16 bits]. Elements are fp16 or bf16 (`dtype`), all
+ * arithmetic is fp32 with one rounding at the end.
+ *
+ * Paged cache: keys and values in two arrays of num_pages pages, [kv_heads][page_size][head_dim] each,
+ * page p at p * page_stride elements (>= kv_heads * page_size * head_dim and a multiple of 8; bases
+ * 16-byte aligned, else W4A4_ERR_ALIGN). page_size: a power of two in [16, 4096] (else
+ * W4A4_ERR_UNSUPPORTED).
+ *
+ * w4a4_qk_norm_rope: per-head RMS norm and position rotation of queries and keys in one pass, and the
+ * append of keys and values to the cache. Rows q [M][heads][head_dim], k and v [M][kv_heads][head_dim]
+ * with row strides ldq, ldk, ldv (slices of a QKV output; heads are adjacent); head_dim a multiple of
+ * 16 up to 512.
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (weight NULL: ones; the mean square is an fp32 number)
+ * then the first rot_dim channels (a multiple of 16, 0: none) are rotated in pairs (a, b) ->
+ * (a cos t - b sin t, b cos t + a sin t), t = positions[m] * inv_freq[i]: pair i is channels
+ * (i, i + rot_dim / 2), with interleaved != 0 (2 i, 2 i + 1). inv_freq is fp64 [rot_dim / 2] and t is
+ * reduced in fp64, so positions to 2^31 and beyond keep their angle. Queries go to q_out (may be q),
+ * keys to k_out if given (may be k) and, with a cache, to slot slots[m] = page * page_size + offset,
+ * values (unchanged) likewise. A slot outside the cache is skipped (padded rows use -1). Two rows
+ * with one slot leave either's values there. Without a cache (both NULL) v and slots are ignored.
+ *
+ * w4a4_paged_attn_decode: for each sequence b and query head h (key/value head h / (heads /
+ * kv_heads)), out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q.k_j), over the visible j < lens[b]:
+ * all of them for window 0, else the last `window` and the first `sinks`. Token j is at offset j %
+ * page_size of page table[b][j / page_size]; entries of pages without a visible token are not read.
+ * lens[b] <= 0 gives zeros. The device cannot report a bad table through the return value, so a
+ * visible page outside [0, num_pages), or lens[b] > table_width * page_size, makes that sequence's
+ * output NaN and reads nothing outside the cache. max_len is the largest length the work is split for:
+ * a longer sequence is still right, only slower. head_dim 64, 96, 128, 192 or 256 (else
+ * W4A4_ERR_UNSUPPORTED); out [B][heads][head_dim] with row stride ldo. Results do not depend on
+ * timing. ws: w4a4_paged_attn_workspace_bytes(...) bytes of the same sizes, 256-byte aligned.
+ * ------------------------------------------------------------------------------------------- */
+int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
+                      int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
+                      const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
+                      int rot_dim, int interleaved, const int64_t *positions, void *q_out,
+                      int64_t ldqo, void *k_out, int64_t ldko, void *k_cache, void *v_cache,
+                      int num_pages, int page_size, int64_t page_stride, const int64_t *slots,
+                      hipStream_t stream);
+size_t w4a4_paged_attn_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_len,
+                                       int window, int sinks);
+int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim,
+                           int64_t ldq, const void *k_cache, const void *v_cache, int num_pages,
+                           int page_size, int64_t page_stride, const int32_t *table, int table_width,
+                           int64_t ldt, const int32_t *lens, int max_len, float scale, int window,
+                           int sinks, void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Diagnostics (host only).
  * ------------------------------------------------------------------------------------------- */
 const char *w4a4_last_error(void);

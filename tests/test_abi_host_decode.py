@@ -114,3 +114,168 @@ def test_binding_refuses_before_the_library():
         bd.gemv_w4g(X[:, :100], wt, torch.ones((3, 16), dtype=torch.float16))
     with pytest.raises(TypeError):
         bd.gemv_w4g(X.double(), wt, s)
+
+
+# ---- norm, rotation, append --------------------------------------------------------------------
+
+def rope(L, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, dt=bd.W4A4_F16, M=4, H=8, KV=2, D=64, ldq=512, ldk=128, ldv=128, qw=FAKE,
+             kw=FAKE, eps=1e-6, f=FAKE, rot=64, inter=0, pos=FAKE, qo=FAKE, ldqo=512, ko=NULL, ldko=0,
+             kc=FAKE, vc=FAKE, P=10, page=16, stride=2 * 16 * 64, slots=FAKE) | kw
+    return L.w4a4_qk_norm_rope(*[a[n] for n in (
+        "q", "k", "v", "dt", "M", "H", "KV", "D", "ldq", "ldk", "ldv", "qw", "kw", "eps", "f", "rot",
+        "inter", "pos", "qo", "ldqo", "ko", "ldko", "kc", "vc", "P", "page", "stride", "slots")], NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=bd.W4A4_F32), bd.W4A4_ERR_ARG),
+    (dict(M=-1), bd.W4A4_ERR_ARG),
+    (dict(H=0), bd.W4A4_ERR_ARG),
+    (dict(KV=0), bd.W4A4_ERR_ARG),
+    (dict(D=0), bd.W4A4_ERR_ARG),
+    (dict(H=5000), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(D=72, rot=0), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(D=528, rot=0), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(rot=80), bd.W4A4_ERR_SHAPE),
+    (dict(rot=8), bd.W4A4_ERR_SHAPE),
+    (dict(rot=-16), bd.W4A4_ERR_SHAPE),
+    (dict(eps=-1.0), bd.W4A4_ERR_ARG),
+    (dict(eps=float("nan")), bd.W4A4_ERR_ARG),
+    (dict(ldq=511), bd.W4A4_ERR_SHAPE),
+    (dict(ldk=127), bd.W4A4_ERR_SHAPE),
+    (dict(ldv=127), bd.W4A4_ERR_SHAPE),
+    (dict(ldqo=511), bd.W4A4_ERR_SHAPE),
+    (dict(ko=FAKE, ldko=127), bd.W4A4_ERR_SHAPE),
+    (dict(q=NULL), bd.W4A4_ERR_ARG),
+    (dict(k=NULL), bd.W4A4_ERR_ARG),
+    (dict(v=NULL), bd.W4A4_ERR_ARG),
+    (dict(qo=NULL), bd.W4A4_ERR_ARG),
+    (dict(kc=NULL), bd.W4A4_ERR_ARG),
+    (dict(vc=NULL), bd.W4A4_ERR_ARG),
+    (dict(kc=NULL, vc=NULL), bd.W4A4_ERR_ARG),           # keys would go nowhere
+    (dict(slots=NULL), bd.W4A4_ERR_ARG),
+    (dict(pos=NULL), bd.W4A4_ERR_ARG),
+    (dict(f=NULL), bd.W4A4_ERR_ARG),
+    (dict(P=0), bd.W4A4_ERR_ARG),
+    (dict(page=8), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(page=48, stride=1 << 16), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(page=8192, stride=1 << 30), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(stride=2 * 16 * 64 - 8), bd.W4A4_ERR_SHAPE),
+    (dict(stride=2 * 16 * 64 + 4), bd.W4A4_ERR_ALIGN),
+    (dict(kc=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(vc=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(q=ODD), bd.W4A4_ERR_ALIGN),
+    (dict(f=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(pos=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(slots=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(qw=ODD), bd.W4A4_ERR_ALIGN),
+])
+def test_qk_norm_rope_rejects(L, kw, code):
+    assert rope(L, **kw) == code
+    assert L.w4a4_last_error() != b""
+
+
+def test_qk_norm_rope_empty(L):
+    assert rope(L, M=0) == bd.W4A4_OK
+    assert rope(L, M=0, kc=NULL, vc=NULL, v=NULL, slots=NULL, q=NULL, k=NULL, qo=NULL) == bd.W4A4_OK
+
+
+# ---- attention over the cache ------------------------------------------------------------------
+
+def attn(L, **kw):
+    a = dict(q=FAKE, dt=bd.W4A4_BF16, B=2, H=8, KV=2, D=64, ldq=512, kc=FAKE, vc=FAKE, P=10, page=16,
+             stride=2 * 16 * 64, table=FAKE, width=4, ldt=4, lens=FAKE, max_len=64, scale=0.125, window=0,
+             sinks=0, out=FAKE, ldo=512, ws=NULL, wsb=0) | kw
+    return L.w4a4_paged_attn_decode(*[a[n] for n in (
+        "q", "dt", "B", "H", "KV", "D", "ldq", "kc", "vc", "P", "page", "stride", "table", "width", "ldt",
+        "lens", "max_len", "scale", "window", "sinks", "out", "ldo", "ws", "wsb")], NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=bd.W4A4_F32), bd.W4A4_ERR_ARG),
+    (dict(B=-1), bd.W4A4_ERR_ARG),
+    (dict(B=1 << 16), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(H=0), bd.W4A4_ERR_ARG),
+    (dict(H=9, ldq=576, ldo=576), bd.W4A4_ERR_SHAPE),      # heads not a multiple of kv_heads
+    (dict(D=80, ldq=640, ldo=640), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(D=32), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(D=512, ldq=4096, ldo=4096), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(ldq=511), bd.W4A4_ERR_SHAPE),
+    (dict(ldo=511), bd.W4A4_ERR_SHAPE),
+    (dict(q=NULL), bd.W4A4_ERR_ARG),
+    (dict(out=NULL), bd.W4A4_ERR_ARG),
+    (dict(kc=NULL), bd.W4A4_ERR_ARG),
+    (dict(vc=NULL), bd.W4A4_ERR_ARG),
+    (dict(table=NULL), bd.W4A4_ERR_ARG),
+    (dict(lens=NULL), bd.W4A4_ERR_ARG),
+    (dict(P=0), bd.W4A4_ERR_ARG),
+    (dict(P=1 << 30, page=4096, stride=1 << 20), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(page=24), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(page=1), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(stride=100), bd.W4A4_ERR_SHAPE),
+    (dict(stride=2 * 16 * 64 + 2), bd.W4A4_ERR_ALIGN),
+    (dict(kc=BY4), bd.W4A4_ERR_ALIGN),
+    (dict(width=0, ldt=0), bd.W4A4_ERR_ARG),
+    (dict(ldt=3), bd.W4A4_ERR_SHAPE),
+    (dict(width=(1 << 26) + 1, ldt=(1 << 26) + 1), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(table=ctypes.c_void_p(0x10002)), bd.W4A4_ERR_ALIGN),
+    (dict(lens=ctypes.c_void_p(0x10002)), bd.W4A4_ERR_ALIGN),
+    (dict(max_len=-1), bd.W4A4_ERR_ARG),
+    (dict(window=-1), bd.W4A4_ERR_ARG),
+    (dict(sinks=-1), bd.W4A4_ERR_ARG),
+    (dict(scale=float("inf")), bd.W4A4_ERR_ARG),
+    (dict(max_len=100000), bd.W4A4_ERR_WORKSPACE),
+    (dict(max_len=100000, ws=BY4, wsb=1 << 30), bd.W4A4_ERR_ALIGN),
+])
+def test_paged_attn_rejects(L, kw, code):
+    assert attn(L, **kw) == code
+    assert L.w4a4_last_error() != b""
+
+
+def test_paged_attn_empty_and_workspace(L):
+    assert attn(L, B=0, q=NULL, out=NULL, table=NULL, lens=NULL) == bd.W4A4_OK
+    assert L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 64, 0, 0) == 0          # one split
+    big = L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 100000, 0, 0)
+    assert big > 0
+    # a window bounds what there is to split
+    assert L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 100000, 40, 4) < big
+    assert L.w4a4_paged_attn_workspace_bytes(2, 9, 2, 64, 100000, 0, 0) == 0
+
+
+def test_binding_checks_shapes():
+    import torch
+    q = torch.zeros((2, 4, 64), dtype=torch.float16)
+    kc = torch.zeros((3, 2, 16, 64), dtype=torch.float16)
+    table, lens = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    call = bd.paged_attn_decode
+    with pytest.raises(ValueError, match="GPU"):
+        call(q, kc, kc.clone(), table, lens)
+    with pytest.raises(ValueError, match="cache"):
+        call(q, kc.bfloat16(), kc, table, lens)
+    with pytest.raises(ValueError, match="alike"):
+        call(q, kc, kc[:2], table, lens)
+    with pytest.raises(ValueError, match="dense"):
+        t = torch.zeros((3, 16, 2, 64), dtype=torch.float16).transpose(1, 2)
+        call(q, t, t, table, lens)
+    with pytest.raises(ValueError, match="table"):
+        call(q, kc, kc, table.long(), lens)
+    with pytest.raises(ValueError, match="lens"):
+        call(q, kc, kc, table, lens.long())
+    with pytest.raises(ValueError, match="adjacent"):
+        call(q[:, ::2], kc, kc, table, lens)
+    with pytest.raises(TypeError):
+        call(q.float(), kc.float(), kc.float(), table, lens)
+    k = torch.zeros((2, 2, 64), dtype=torch.float16)
+    w, f, pos = torch.ones(64), torch.ones(32, dtype=torch.float64), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        bd.qk_norm_rope(q, k, w, w, f, pos)
+    with pytest.raises(ValueError, match="inv_freq"):
+        bd.qk_norm_rope(q, k, w, w, f.float(), pos)
+    with pytest.raises(ValueError, match="positions"):
+        bd.qk_norm_rope(q, k, w, w, f, pos.int())
+    with pytest.raises(ValueError, match="q_weight"):
+        bd.qk_norm_rope(q, k, w.half(), w, f, pos)
+    with pytest.raises(ValueError, match="slots"):
+        bd.qk_norm_rope_append(q, k, k, w, w, f, pos, kc, kc.clone(), pos.int())
+    with pytest.raises(ValueError, match="required"):
+        bd.qk_norm_rope_append(q, k, None, w, w, f, pos, kc, kc, pos)

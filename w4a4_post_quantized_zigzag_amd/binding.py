@@ -76,6 +76,12 @@ SIGNATURES = {
     "w4a4_pack_weights_w4g": (_i, [_vp, _i, _i, _i, _i64, _i, _vp, _vp, _vp]),
     "w4a4_codes_to_w4g": (_i, [_vp, _i, _i, _vp, _vp]),
     "w4a4_gemv_w4g": (_i, [_vp, _i, _i, _i, _i64, _vp, _vp, _i, _i, _vp, _i64, _i, _vp, _i64, _vp]),
+    "w4a4_qk_norm_rope": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i64, _i64, _i64, _vp, _vp,
+                               ctypes.c_float, _vp, _i, _i, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i,
+                               _i64, _vp, _vp]),
+    "w4a4_paged_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "w4a4_paged_attn_decode": (_i, [_vp, _i, _i, _i, _i, _i, _i64, _vp, _vp, _i, _i, _i64, _vp, _i,
+                                    _i64, _vp, _i, ctypes.c_float, _i, _i, _vp, _i64, _vp, _sz, _vp]),
     "w4a4_last_error": (ctypes.c_char_p, []),
     "w4a4_status_string": (ctypes.c_char_p, [_i]),
     "w4a4_abi_version": (_i, []),
@@ -579,3 +585,135 @@ def gemv_w4g(X, wt, w_scale, Y=None, epilogue: int = EPI_NONE, residual=None):
                 _ld(X), wt.data_ptr(), w_scale.data_ptr(), K // groups, N, Y.data_ptr(),
                 _ld(Y), epilogue, residual.data_ptr(), _ld(residual))
     return Y
+
+
+def _code_heads(t, name: str) -> int:
+    """W4A4_* code of an fp16 or bf16 tensor [rows, heads, head_dim] whose heads are adjacent."""
+    torch = _torch()
+    _want(t.dim() == 3 and t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1),
+          f"{name} must be [rows, heads, head_dim] with adjacent heads")
+    if t.dtype is torch.bfloat16:
+        return W4A4_BF16
+    if t.dtype is torch.float16:
+        return W4A4_F16
+    raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def _ld3(t) -> int:
+    """Row stride of [rows, heads, head_dim]."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _cache_shape(k_cache, v_cache, dtype, kv_heads: int, D: int):
+    """(pages, page_size, page_stride) of the paged cache arrays [pages, kv_heads, page_size, D]."""
+    P, KV, page, d = k_cache.shape
+    st = k_cache.stride()
+    _want(KV == kv_heads and d == D and k_cache.dtype is dtype and v_cache.dtype is dtype,
+          f"cache must be {dtype} [pages, {kv_heads}, page_size, {D}]")
+    _want(v_cache.shape == k_cache.shape and v_cache.stride() == st, "k_cache and v_cache must be laid out alike")
+    _want(st[3] == 1 and st[2] == D and (st[1] == page * D or KV == 1), "a cache page must be dense")
+    return P, page, st[0] if P > 1 else KV * page * D
+
+
+def _index(t, dtype, shape, name: str):
+    _want(t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous(),
+          f"{name} must be contiguous {dtype} {list(shape)}")
+    return t.data_ptr()
+
+
+def _norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out, k_cache,
+               v_cache, slots):
+    torch = _torch()
+    M, H, D = q.shape
+    KV = k.shape[1]
+    dt = _code_heads(q, "q")
+    _want(_code_heads(k, "k") == dt and k.shape[0] == M and k.shape[2] == D, "k must be [M, kv_heads, D] of q's type")
+    if q_out is None:
+        q_out = torch.empty((M, H, D), dtype=q.dtype, device=q.device)
+    else:
+        _want(_code_heads(q_out, "q_out") == dt and q_out.shape == q.shape, "q_out must be like q")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    used = [q, k, q_out]
+    ptr = {}
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        ptr[name] = None
+        if w is not None:
+            ptr[name] = _index(w, torch.float32, (D,), name)
+            used.append(w)
+    fp = pp = None
+    if rot:
+        fp = _index(inv_freq, torch.float64, (rot // 2,), "inv_freq")
+        pp = _index(positions, torch.int64, (M,), "positions")
+        used += (inv_freq, positions)
+    kop = None
+    if k_out is not None:
+        _want(_code_heads(k_out, "k_out") == dt and k_out.shape == k.shape, "k_out must be like k")
+        kop = k_out.data_ptr()
+        used.append(k_out)
+    vp = kcp = vcp = sp = None
+    P = page = stride = ldv = 0
+    if k_cache is not None:
+        _want(_code_heads(v, "v") == dt and v.shape == k.shape, "v must be like k")
+        P, page, stride = _cache_shape(k_cache, v_cache, q.dtype, KV, D)
+        sp = _index(slots, torch.int64, (M,), "slots")
+        vp, ldv, kcp, vcp = v.data_ptr(), _ld3(v), k_cache.data_ptr(), v_cache.data_ptr()
+        used += (v, k_cache, v_cache, slots)
+    _launch(lib().w4a4_qk_norm_rope, used, q.data_ptr(), k.data_ptr(), vp, dt, M, H, KV, D, _ld3(q), _ld3(k),
+            ldv, ptr["q_weight"], ptr["k_weight"], eps, fp, rot, 1 if interleaved else 0, pp,
+            q_out.data_ptr(), _ld3(q_out), kop, _ld3(k_out) if kop else 0, kcp, vcp, P, page, stride, sp)
+    return q_out
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head RMS norm and position rotation of queries [M, heads, D] and keys [M, kv_heads, D] in one
+    pass. Weights fp32 [D] or None, inv_freq fp64 [rot / 2] or None (no rotation), positions int64 [M].
+    Returns (q_out, k_out), which may be q and k themselves."""
+    if k_out is None:
+        k_out = _torch().empty(k.shape, dtype=k.dtype, device=k.device)
+    return _norm_rope(q, k, None, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
+                      None, None, None), k_out
+
+
+def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, k_cache, v_cache, slots,
+                        eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None):
+    """qk_norm_rope with the keys and values written to slots int64 [M] (page * page_size + offset, or
+    -1) of the paged cache [pages, kv_heads, page_size, D]. Returns q_out."""
+    _want(k_cache is not None and v_cache is not None and slots is not None and v is not None,
+          "v, k_cache, v_cache and slots are required")
+    return _norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
+                      k_cache, v_cache, slots)
+
+
+def paged_attn_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, window: int = 0,
+                      sinks: int = 0, max_len: int | None = None, out=None, ws=None):
+    """Attention of one new token per sequence, q [B, heads, D], over the first lens[b] tokens of the
+    paged cache [pages, kv_heads, page_size, D] through table int32 [B, width]; lens int32 [B]. window >
+    0: only the last `window` and the first `sinks` tokens. scale defaults to D ** -0.5, max_len (what the
+    work is split for) to what the table holds."""
+    torch = _torch()
+    B, H, D = q.shape
+    KV = k_cache.shape[1]
+    dt = _code_heads(q, "q")
+    P, page, stride = _cache_shape(k_cache, v_cache, q.dtype, KV, D)
+    _want(table.dtype is torch.int32 and table.dim() == 2 and table.shape[0] == B
+          and (table.stride(1) == 1 or table.shape[1] == 1), "table must be int32 [B, width]")
+    width = table.shape[1]
+    lp = _index(lens, torch.int32, (B,), "lens")
+    if max_len is None:
+        max_len = width * page
+    if out is None:
+        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
+    else:
+        _want(_code_heads(out, "out") == dt and out.shape == q.shape, "out must be like q")
+    L = lib()
+    if ws is None:
+        nb = L.w4a4_paged_attn_workspace_bytes(B, H, KV, D, max_len, window, sinks)
+        if nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
+    used = (q, k_cache, v_cache, table, lens, out) if ws is None else (q, k_cache, v_cache, table, lens, out, ws)
+    _launch(L.w4a4_paged_attn_decode, used, q.data_ptr(), dt, B, H, KV, D, _ld3(q), k_cache.data_ptr(),
+            v_cache.data_ptr(), P, page, stride, table.data_ptr(), width, table.stride(0) if B > 1 else width,
+            lp, max_len, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ld3(out),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+    return out

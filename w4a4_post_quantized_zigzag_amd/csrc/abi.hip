@@ -1076,4 +1076,201 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
     return ok();
 }
 
+// ------------------------------------------------------------------ single-token path
+
+static int check_dtype16(int dt)
+{
+    if (dt != W4A4_F16 && dt != W4A4_BF16) return fail(W4A4_ERR_ARG, "dtype %d is not fp16 or bf16", dt);
+    return W4A4_OK;
+}
+
+static int check_heads(int heads, int kv_heads, int head_dim)
+{
+    if (heads <= 0 || kv_heads <= 0 || head_dim <= 0)
+        return fail(W4A4_ERR_ARG, "heads %d, kv_heads %d and head_dim %d must be positive", heads,
+                    kv_heads, head_dim);
+    if (heads > 4096 || kv_heads > 4096)
+        return fail(W4A4_ERR_UNSUPPORTED, "heads %d, kv_heads %d above 4096", heads, kv_heads);
+    return W4A4_OK;
+}
+
+static int check_cache(const void *k_cache, const void *v_cache, int kv_heads, int head_dim,
+                       int num_pages, int page_size, int64_t page_stride)
+{
+    if (!k_cache || !v_cache) return fail(W4A4_ERR_ARG, "k_cache and v_cache are required");
+    if (num_pages <= 0) return fail(W4A4_ERR_ARG, "num_pages = %d must be positive", num_pages);
+    if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)))
+        return fail(W4A4_ERR_UNSUPPORTED, "page_size %d is not a power of two in [16, 4096]", page_size);
+    const int64_t page = (int64_t)kv_heads * page_size * head_dim;
+    if (page > ((int64_t)1 << 30))
+        return fail(W4A4_ERR_UNSUPPORTED, "a page of %lld elements is above 2^30", (long long)page);
+    if (page_stride < page)
+        return fail(W4A4_ERR_SHAPE, "page_stride %lld < %lld", (long long)page_stride, (long long)page);
+    if ((int64_t)num_pages > (((int64_t)1 << 44) / page_stride))
+        return fail(W4A4_ERR_UNSUPPORTED, "cache above 2^44 elements");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || page_stride % 8)
+        return fail(W4A4_ERR_ALIGN, "cache pages must be 16-byte aligned");
+    return W4A4_OK;
+}
+
+static int check_rows16(const void *p, int M, int64_t ld, int64_t width, const char *name)
+{
+    if (ld < width)
+        return fail(W4A4_ERR_SHAPE, "%s row stride %lld < %lld", name, (long long)ld, (long long)width);
+    if (M > 0 && !p) return fail(W4A4_ERR_ARG, "%s is NULL", name);
+    if (!aligned(p, 2)) return fail(W4A4_ERR_ALIGN, "%s misaligned", name);
+    if ((int64_t)M * ld > ((int64_t)1 << 40))
+        return fail(W4A4_ERR_UNSUPPORTED, "%s larger than 2^40 elements", name);
+    return W4A4_OK;
+}
+
+int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
+                      int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
+                      const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
+                      int rot_dim, int interleaved, const int64_t *positions, void *q_out,
+                      int64_t ldqo, void *k_out, int64_t ldko, void *k_cache, void *v_cache,
+                      int num_pages, int page_size, int64_t page_stride, const int64_t *slots,
+                      hipStream_t stream)
+{
+    int rc;
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim))) return rc;
+    if (M < 0) return fail(W4A4_ERR_ARG, "M = %d negative", M);
+    if (head_dim % 16 || head_dim > 512)
+        return fail(W4A4_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 16 up to 512", head_dim);
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+        return fail(W4A4_ERR_SHAPE, "rot_dim %d is not a multiple of 16 in [0, %d]", rot_dim, head_dim);
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(W4A4_ERR_ARG, "eps must be finite and not negative");
+    const int64_t wq = (int64_t)heads * head_dim, wk = (int64_t)kv_heads * head_dim;
+    if ((rc = check_rows16(q, M, ldq, wq, "q")) || (rc = check_rows16(k, M, ldk, wk, "k")) ||
+        (rc = check_rows16(q_out, M, ldqo, wq, "q_out")))
+        return rc;
+    const bool cache = k_cache || v_cache;
+    if (M > 0 && !cache && !k_out) return fail(W4A4_ERR_ARG, "keys need k_out or a cache");
+    if (k_out && (rc = check_rows16(k_out, M, ldko, wk, "k_out"))) return rc;
+    if (cache) {
+        if ((rc = check_cache(k_cache, v_cache, kv_heads, head_dim, num_pages, page_size, page_stride)) ||
+            (rc = check_rows16(v, M, ldv, wk, "v")))
+            return rc;
+        if (M > 0 && !slots) return fail(W4A4_ERR_ARG, "slots is NULL");
+    }
+    if (M > 0 && rot_dim > 0 && (!inv_freq || !positions))
+        return fail(W4A4_ERR_ARG, "inv_freq and positions are required for rot_dim %d", rot_dim);
+    if (!aligned(inv_freq, 8) || !aligned(positions, 8) || !aligned(slots, 8) || !aligned(q_weight, 4) ||
+        !aligned(k_weight, 4))
+        return fail(W4A4_ERR_ALIGN, "inv_freq / positions / slots / weights misaligned");
+    if (M == 0) return ok();
+    NormRopeArgs a{};
+    a.q = (const uint16_t *)q;
+    a.k = (const uint16_t *)k;
+    a.v = cache ? (const uint16_t *)v : nullptr;
+    a.M = M;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.D = head_dim;
+    a.rot = rot_dim;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    a.q_out = (uint16_t *)q_out;
+    a.k_out = (uint16_t *)k_out;
+    a.ldqo = ldqo;
+    a.ldko = ldko;
+    a.k_cache = (uint16_t *)k_cache;
+    a.v_cache = (uint16_t *)v_cache;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_stride = page_stride;
+    a.slots = slots;
+    if ((rc = launch_norm_rope(a, dtype, interleaved != 0, stream))) return rc;
+    return ok();
+}
+
+static size_t attn_ws_bytes(const AttnPlan &p, int B, int heads, int head_dim)
+{
+    if (p.splits <= 1 || B <= 0) return 0;
+    const size_t n = (size_t)B * heads * p.splits;
+    return align_up(n * sizeof(float2), 256) + align_up(n * head_dim * sizeof(float), 256);
+}
+
+size_t w4a4_paged_attn_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_len,
+                                       int window, int sinks)
+{
+    if (B <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads || head_dim <= 0 || max_len < 0 ||
+        window < 0 || sinks < 0)
+        return 0;
+    return attn_ws_bytes(attn_plan(B, heads, kv_heads, max_len, window, sinks), B, heads, head_dim);
+}
+
+int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim,
+                           int64_t ldq, const void *k_cache, const void *v_cache, int num_pages,
+                           int page_size, int64_t page_stride, const int32_t *table, int table_width,
+                           int64_t ldt, const int32_t *lens, int max_len, float scale, int window,
+                           int sinks, void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                           hipStream_t stream)
+{
+    int rc;
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim))) return rc;
+    if (B < 0) return fail(W4A4_ERR_ARG, "B = %d negative", B);
+    if (B > 65535) return fail(W4A4_ERR_UNSUPPORTED, "B = %d above 65535", B);
+    if (heads % kv_heads)
+        return fail(W4A4_ERR_SHAPE, "heads %d is not a multiple of kv_heads %d", heads, kv_heads);
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+        return fail(W4A4_ERR_UNSUPPORTED, "head_dim %d is not 64, 96, 128, 192 or 256", head_dim);
+    const int64_t width = (int64_t)heads * head_dim;
+    if ((rc = check_rows16(q, B, ldq, width, "q")) || (rc = check_rows16(out, B, ldo, width, "out")) ||
+        (rc = check_cache(k_cache, v_cache, kv_heads, head_dim, num_pages, page_size, page_stride)))
+        return rc;
+    if (table_width <= 0) return fail(W4A4_ERR_ARG, "table_width = %d must be positive", table_width);
+    if (ldt < table_width)
+        return fail(W4A4_ERR_SHAPE, "table row stride %lld < %d", (long long)ldt, table_width);
+    if ((int64_t)table_width * page_size > ((int64_t)1 << 30))
+        return fail(W4A4_ERR_UNSUPPORTED, "a table row of more than 2^30 tokens");
+    if (B > 0 && (!table || !lens)) return fail(W4A4_ERR_ARG, "table and lens are required");
+    if (!aligned(table, 4) || !aligned(lens, 4)) return fail(W4A4_ERR_ALIGN, "table / lens misaligned");
+    if (max_len < 0 || window < 0 || sinks < 0)
+        return fail(W4A4_ERR_ARG, "max_len %d, window %d and sinks %d must not be negative", max_len,
+                    window, sinks);
+    if (!std::isfinite(scale)) return fail(W4A4_ERR_ARG, "scale must be finite");
+    const AttnPlan plan = attn_plan(B, heads, kv_heads, max_len, window, sinks);
+    const size_t need = attn_ws_bytes(plan, B, heads, head_dim);
+    if ((rc = check_ws(ws, ws_bytes, need))) return rc;
+    if (B == 0) return ok();
+    AttnArgs a{};
+    a.q = (const uint16_t *)q;
+    a.k_cache = (const uint16_t *)k_cache;
+    a.v_cache = (const uint16_t *)v_cache;
+    a.out = (uint16_t *)out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.page_stride = page_stride;
+    a.ldt = ldt;
+    a.table = table;
+    a.lens = lens;
+    a.B = B;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_shift = __builtin_ctz((unsigned)page_size);
+    a.table_width = table_width;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.splits = plan.splits;
+    a.tiles_per_split = plan.tiles_per_split;
+    if (need) {
+        a.stat = reinterpret_cast<float2 *>(ws);
+        a.part = reinterpret_cast<float *>(
+            reinterpret_cast<char *>(ws) +
+            align_up((size_t)B * heads * plan.splits * sizeof(float2), 256));
+    }
+    if ((rc = launch_paged_attn(a, dtype, head_dim, stream))) return rc;
+    return ok();
+}
+
 }  // extern "C"

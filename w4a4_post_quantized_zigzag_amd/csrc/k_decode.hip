@@ -1,0 +1,558 @@
+// The single-token path between two linears: per-head RMS norm and position rotation of queries and
+// keys with the append to the paged key-value cache, and the attention of one new token per sequence
+// over that cache.
+#include <algorithm>
+
+#include "w4a4_internal.h"
+
+namespace w4a4 {
+
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef float f2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+
+// two fp32 values rounded to the 16-bit type, low value first, and back
+template <int DT> __device__ __forceinline__ uint32_t pack16(float a, float b)
+{
+    if constexpr (DT == W4A4_BF16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, b2_t));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, h2_t));
+}
+
+template <int DT> __device__ __forceinline__ f2_t unpack16(uint32_t w)
+{
+    if constexpr (DT == W4A4_BF16)
+        return f2_t{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
+    else
+        return __builtin_convertvector(__builtin_bit_cast(h2_t, w), f2_t);
+}
+
+// Eight consecutive 16-bit elements; rows that are not 16-byte aligned go element by element.
+template <bool VEC> __device__ __forceinline__ u4_t load8(const uint16_t *__restrict__ p)
+{
+    if (VEC) return *reinterpret_cast<const u4_t *>(p);
+    u4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+    return r;
+}
+
+template <bool VEC> __device__ __forceinline__ void store8(uint16_t *p, const u4_t &v)
+{
+    if (VEC) {
+        *reinterpret_cast<u4_t *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p[2 * i] = (uint16_t)v[i];
+        p[2 * i + 1] = (uint16_t)(v[i] >> 16);
+    }
+}
+
+// ================================================================================================
+// Norm, rotation, append. Per head x of D channels: y = x / sqrt(mean(x^2) + eps) * w, then the first
+// rot channels in pairs (a, b) -> (a cos t - b sin t, b cos t + a sin t), t = position * inv_freq.
+//
+// Bound by the bytes: every element is read once and written once, in one launch for queries, keys
+// and values. A head is LH lanes of eight channels (one 16-byte load each), a wave works on 64 / LH
+// heads at a time and walks its token's heads, so the rotation's sines and cosines are computed once
+// per token (one lane per frequency, shared through LDS) and kept in registers over its heads. The
+// angle is reduced to a fraction of a turn in fp64, so far positions lose nothing.
+// ================================================================================================
+template <int DT, int LH, bool VEC, bool PAIRS>
+__global__ __launch_bounds__(256) void k_norm_rope(const NormRopeArgs a)
+{
+    extern __shared__ float2 turns[];  // [tokens of the workgroup][rot / 2] (cos, sin)
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int half = a.rot >> 1;
+    const int wpt = a.waves_per_token, tpw = 4 / wpt;  // waves on one token, tokens per workgroup
+    const int slot_t = wave / wpt;
+    const int64_t m = (int64_t)blockIdx.x * tpw + slot_t;
+    float2 *cs = turns + slot_t * half;
+    if (m < a.M && half > 0) {
+        const double pos = (double)a.positions[m] * 0.15915494309189533577;  // 1 / (2 pi)
+        for (int f = (wave % wpt) * 64 + lane; f < half; f += wpt * 64) {
+            double t = pos * a.inv_freq[f];
+            t -= rint(t);
+            float s, c;
+            sincospif(2.0f * (float)t, &s, &c);
+            cs[f] = make_float2(c, s);
+        }
+    }
+    __syncthreads();
+    if (m >= a.M) return;
+
+    constexpr int HP = 64 / LH;  // heads at a time
+    const int c = lane % LH, d = c * 8;
+    const bool on = d < a.D;
+    const bool rotated = d < a.rot, first = PAIRS || d < half;
+    float co[8], si[8];  // per channel (PAIRS: per pair, in the first four)
+    int partner = lane;
+    if (rotated) {
+        if (PAIRS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 t = cs[d / 2 + i];
+                co[i] = t.x;
+                si[i] = t.y;
+            }
+        } else {
+            partner = first ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 t = cs[(first ? d : d - half) + i];
+                co[i] = t.x;
+                si[i] = first ? -t.y : t.y;
+            }
+        }
+    }
+    float wq[8], wk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        wq[i] = (a.q_weight && on) ? a.q_weight[d + i] : 1.0f;
+        wk[i] = (a.k_weight && on) ? a.k_weight[d + i] : 1.0f;
+    }
+    int64_t row = -1;  // cache row offset of this token (elements), -1: not kept
+    if (a.k_cache) {
+        const int64_t s = a.slots[m];
+        if (s >= 0 && s < (int64_t)a.num_pages * a.page_size)
+            row = (s / a.page_size) * a.page_stride + (s % a.page_size) * a.D;
+    }
+    const int nq = a.heads, nk = a.kv_heads, total = nq + nk + (a.k_cache ? nk : 0);
+    const float inv_d = 1.0f / (float)a.D;
+
+    for (int h0 = (wave % wpt) * HP; h0 < total; h0 += wpt * HP) {
+        const int h = h0 + lane / LH;
+        const bool is_q = h < nq, is_v = h >= nq + nk;
+        const int hk = is_q ? 0 : is_v ? h - nq - nk : h - nq;
+        const bool live = on && h < total;
+        u4_t raw = {0, 0, 0, 0};
+        if (live)
+            raw = load8<VEC>(is_q   ? a.q + m * a.ldq + (int64_t)h * a.D + d
+                             : is_v ? a.v + m * a.ldv + (int64_t)hk * a.D + d
+                                    : a.k + m * a.ldk + (int64_t)hk * a.D + d);
+        float x[8], sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f2_t f = unpack16<DT>(raw[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+            sq = fmaf(f.x, f.x, sq);
+            sq = fmaf(f.y, f.y, sq);
+        }
+#pragma unroll
+        for (int off = 1; off < LH; off <<= 1) sq += __shfl_xor(sq, off, 64);
+        const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
+        if (PAIRS) {
+            if (rotated) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = y[2 * i], q = y[2 * i + 1];
+                    y[2 * i] = p * co[i] - q * si[i];
+                    y[2 * i + 1] = q * co[i] + p * si[i];
+                }
+            }
+        } else if (half > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = __shfl(y[i], partner, 64);
+                if (rotated) y[i] = y[i] * co[i] + o * si[i];
+            }
+        }
+        u4_t out;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = is_v ? raw[i] : pack16<DT>(y[2 * i], y[2 * i + 1]);
+        if (!live) continue;
+        if (is_q) {
+            store8<VEC>(a.q_out + m * a.ldqo + (int64_t)h * a.D + d, out);
+        } else {
+            if (!is_v && a.k_out) store8<VEC>(a.k_out + m * a.ldko + (int64_t)hk * a.D + d, out);
+            if (row >= 0)
+                store8<true>((is_v ? a.v_cache : a.k_cache) + row + (int64_t)hk * a.page_size * a.D + d, out);
+        }
+    }
+}
+
+template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool vec, bool pairs, hipStream_t s)
+{
+    const int tpw = 4 / a.waves_per_token;
+    const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(256);
+    const size_t lds = (size_t)tpw * (a.rot / 2) * sizeof(float2);
+    if (vec && pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, true>), grid, block, lds, s, a);
+    else if (vec) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, false>), grid, block, lds, s, a);
+    else if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, false, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false, false>), grid, block, lds, s, a);
+    return check_launch("qk_norm_rope");
+}
+
+template <int DT> static int pick_head(const NormRopeArgs &a, bool vec, bool pairs, hipStream_t s)
+{
+    if (a.D <= 32) return run_norm_rope<DT, 4>(a, vec, pairs, s);
+    if (a.D <= 64) return run_norm_rope<DT, 8>(a, vec, pairs, s);
+    if (a.D <= 128) return run_norm_rope<DT, 16>(a, vec, pairs, s);
+    if (a.D <= 256) return run_norm_rope<DT, 32>(a, vec, pairs, s);
+    return run_norm_rope<DT, 64>(a, vec, pairs, s);
+}
+
+int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
+{
+    auto rows16 = [](const void *p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0); };
+    const bool vec = rows16(a.q, a.ldq) && rows16(a.k, a.ldk) && rows16(a.v, a.ldv) &&
+                     rows16(a.q_out, a.ldqo) && rows16(a.k_out, a.ldko);
+    // few tokens: all four waves on one; many: a wave each, so that its sines serve all heads
+    a.waves_per_token = a.M < 1024 ? 4 : 1;
+    return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, vec, interleaved, s)
+                              : pick_head<W4A4_F16>(a, vec, interleaved, s);
+}
+
+// ================================================================================================
+// Attention of one new token over the paged cache.
+//
+// Bound by the cache bytes: every visible key and value is read once for all the query heads that
+// share it. A wave takes tiles of 32 keys:
+//  - scores^T (16 keys x 16 heads, twice) = K (A operand, rows straight from the cache) . q^T;
+//  - a lane then holds 8 keys of one head. Running maximum and sum as usual, the sum per lane;
+//  - out^T (16 channels x 16 heads per product) += V^T (A operand) . p (B operand). The scores'
+//    result layout already is the B operand of a 32-key product if key 4 g + e (e < 4) of the first
+//    and of the second half of the tile are its k = 8 g + e and 8 g + 4 + e. For the A operand a lane
+//    loads D / 16 neighbouring channels of those eight keys and pairs them up with byte permutes;
+//    nothing passes through LDS and no cross-lane step is needed but the maximum's.
+//  - p is split in two 16-bit parts (p = hi + lo to 2^-16 or better), two products per tile.
+// Tiles of one sequence go round-robin to the four waves of a workgroup and, above that, in equal
+// runs to `splits` workgroups, joined in LDS and by k_attn_join in a fixed order.
+// ================================================================================================
+
+// Tiles of 32 keys that hold something visible: tiles [0, ns) and from w0 on, T in all.
+struct AttnTiles {
+    int ns, w0, T;
+    bool over;  // longer than the table can say: poisoned, one logical tile
+};
+
+__device__ __forceinline__ AttnTiles attn_tiles(int n, const AttnArgs &a)
+{
+    AttnTiles t{0, 0, 0, false};
+    if (n <= 0) return t;
+    if ((int64_t)n > (int64_t)a.table_width * a.page_size) {
+        t.over = true;
+        t.T = 1;
+        return t;
+    }
+    const int all = (int)(((int64_t)n + 31) >> 5);
+    if (a.window > 0 && (int64_t)n > (int64_t)a.window + a.sinks) {
+        t.ns = (a.sinks + 31) >> 5;
+        t.w0 = max((n - a.window) >> 5, t.ns);
+    }
+    t.T = t.ns + all - t.w0;
+    return t;
+}
+
+template <int DT> __device__ __forceinline__ f4_t mma32(const u4_t &a, const u4_t &b, const f4_t &c)
+{
+    if constexpr (DT == W4A4_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a),
+                                                      __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a),
+                                                       __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
+}
+
+// combine the four 16-lane groups of a wave: every lane gets the result over lanes l, l^16, l^32, l^48
+template <typename F> __device__ __forceinline__ float across_groups(float x, F f)
+{
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    x = f(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+    u = __builtin_bit_cast(uint32_t, x);
+    auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+
+constexpr int ATTN_WAVES = 4;
+
+// N dwords from a 4-byte aligned address
+template <int N> struct __attribute__((aligned(4))) DwordRun {
+    uint32_t v[N];
+};
+
+template <int DT, int D>
+__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a)
+{
+    constexpr int KJ = D / 32, VE = D / 16, DW = VE / 2;
+    // p is held times 2^14 in fp16, so that what the two parts drop is 2^-38 of the largest
+    constexpr float OFF = DT == W4A4_F16 ? 14.0f : 0.0f;
+    extern __shared__ float sm[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int b = blockIdx.z, split = blockIdx.x;
+    const int kvh = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
+    const int group = a.heads / a.kv_heads, G = min(16, group - ht * 16), h0 = kvh * group + ht * 16;
+    const int n = a.lens[b];
+    const AttnTiles tl = attn_tiles(n, a);
+    const int t0 = split * a.tiles_per_split;
+    const int t1 = split + 1 == a.splits ? tl.T : min(tl.T, t0 + a.tiles_per_split);
+    uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h0 * D;
+    if (tl.T == 0) {  // nothing visible: zeros
+        if (split == 0)
+            for (int e = threadIdx.x; e < G * D; e += 64 * ATTN_WAVES) out[e] = 0;
+        return;
+    }
+    if (t0 >= t1) return;
+
+    u4_t q[KJ];
+    {
+        const uint16_t *qp = a.q + (int64_t)b * a.ldq + (int64_t)(h0 + r) * D + 8 * g;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+            q[j] = r < G ? (a.q_vec ? load8<true>(qp + 32 * j) : load8<false>(qp + 32 * j)) : u4_t{0, 0, 0, 0};
+    }
+    f4_t acc[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) acc[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float mx = -INFINITY, sum = 0.0f;
+    bool bad = tl.over;
+    const int *table = a.table + (int64_t)b * a.ldt;
+    const int first_in_window = a.window > 0 ? n - a.window : 0;
+    auto seen = [&](int key) {
+        return key < n && (key >= first_in_window || key < a.sinks);
+    };
+    // element offset of a key's row in the caches; a page that does not exist reads page 0 and poisons
+    auto row_of = [&](int key) {
+        int pid = table[key >> a.page_shift];
+        if ((unsigned)pid >= (unsigned)a.num_pages) {
+            bad = true;
+            pid = 0;
+        }
+        return (int64_t)pid * a.page_stride + (int64_t)(kvh * a.page_size + (key & (a.page_size - 1))) * D;
+    };
+
+    for (int t = tl.over ? t1 : t0 + wave; t < t1; t += ATTN_WAVES) {
+        const int key0 = (t < tl.ns ? t : tl.w0 + t - tl.ns) * 32;
+        const bool whole = key0 <= n - 32 && (key0 >= first_in_window || key0 + 32 <= a.sinks);
+        u4_t k[2][KJ];
+        DwordRun<DW> v[8];
+        if (whole) {
+            // 16 keys that start at a multiple of 16 lie in one page: one uniform lookup each
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int64_t at = row_of(key0 + 16 * hf);
+                const uint16_t *kp = a.k_cache + at + r * D + 8 * g;
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) k[hf][j] = *reinterpret_cast<const u4_t *>(kp + 32 * j);
+                const uint16_t *vp = a.v_cache + at + 4 * g * D + VE * r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[4 * hf + e] = *reinterpret_cast<const DwordRun<DW> *>(vp + e * D);
+            }
+        } else {
+            // keys that are not visible read the last one, which is
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int key = key0 + 16 * hf + r;
+                const uint16_t *kp = a.k_cache + row_of(seen(key) ? key : n - 1) + 8 * g;
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) k[hf][j] = *reinterpret_cast<const u4_t *>(kp + 32 * j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int vk = key0 + 16 * hf + 4 * g + e;
+                    const bool ok = seen(vk);
+                    v[4 * hf + e] = *reinterpret_cast<const DwordRun<DW> *>(
+                        a.v_cache + row_of(ok ? vk : n - 1) + VE * r);
+#pragma unroll
+                    for (int i = 0; i < DW; ++i) v[4 * hf + e].v[i] = ok ? v[4 * hf + e].v[i] : 0u;
+                }
+            }
+        }
+        float p[8];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            f4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) s = mma32<DT>(k[hf][j], q[j], s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[4 * hf + e] = (whole || seen(key0 + 16 * hf + 4 * g + e)) ? s[e] * a.scale_log2 : -INFINITY;
+        }
+        float top = p[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
+        top = across_groups(top, [](float x, float y) { return fmaxf(x, y); });
+        if (__any(top > mx)) {
+            const float to = fmaxf(mx, top), f = to > mx ? __builtin_amdgcn_exp2f(mx - to) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) acc[i] *= f;
+            sum *= f;
+            mx = to;
+        }
+        const float from = (mx == -INFINITY ? 0.0f : mx) - OFF;
+        u4_t hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float x = __builtin_amdgcn_exp2f(p[e] - from), y = __builtin_amdgcn_exp2f(p[e + 1] - from);
+            sum += x + y;
+            hi[e / 2] = pack16<DT>(x, y);
+            const f2_t h = unpack16<DT>(hi[e / 2]);
+            lo[e / 2] = pack16<DT>(x - h.x, y - h.y);
+        }
+#pragma unroll
+        for (int i = 0; i < DW; ++i) {
+            u4_t even, odd;  // channels VE r + 2 i and + 2 i + 1 of the eight keys
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                even[e] = __builtin_amdgcn_perm(v[2 * e + 1].v[i], v[2 * e].v[i], 0x05040100u);
+                odd[e] = __builtin_amdgcn_perm(v[2 * e + 1].v[i], v[2 * e].v[i], 0x07060302u);
+            }
+            acc[2 * i] = mma32<DT>(even, lo, acc[2 * i]);
+            acc[2 * i + 1] = mma32<DT>(odd, lo, acc[2 * i + 1]);
+            acc[2 * i] = mma32<DT>(even, hi, acc[2 * i]);
+            acc[2 * i + 1] = mma32<DT>(odd, hi, acc[2 * i + 1]);
+        }
+    }
+    sum = across_groups(sum, [](float x, float y) { return x + y; });
+    if (__any(bad)) sum = NAN;
+
+    // ---- join the waves: sm = max [W][16], sum [W][16], channels [W][G][D] ----
+    float *wm = sm, *ws = sm + ATTN_WAVES * 16, *wa = sm + ATTN_WAVES * 32;
+    if (g == 0) {
+        wm[wave * 16 + r] = mx;
+        ws[wave * 16 + r] = sum;
+    }
+    if (r < G) {
+        float *dst = wa + ((size_t)wave * G + r) * D;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int i = 0; i < VE; ++i) dst[VE * (4 * g + x) + i] = acc[i][x];
+    }
+    __syncthreads();
+    const bool alone = a.splits == 1 || tl.T <= a.tiles_per_split;
+    for (int e = threadIdx.x; e < G * D; e += 64 * ATTN_WAVES) {
+        const int h = e / D, d = e % D;
+        float top = wm[h];
+#pragma unroll
+        for (int w = 1; w < ATTN_WAVES; ++w) top = fmaxf(top, wm[w * 16 + h]);
+        const float from = top == -INFINITY ? 0.0f : top;
+        float o = 0.0f, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < ATTN_WAVES; ++w) {
+            const float f = __builtin_amdgcn_exp2f(wm[w * 16 + h] - from);
+            o += f * wa[((size_t)w * G + h) * D + d];
+            l += f * ws[w * 16 + h];
+        }
+        if (alone) {
+            out[e] = (uint16_t)pack16<DT>(o / l, 0.0f);
+        } else {
+            const int64_t at = ((int64_t)b * a.heads + h0 + h) * a.splits + split;
+            a.part[at * D + d] = o;
+            if (d == 0) a.stat[at] = make_float2(top, l);
+        }
+    }
+}
+
+// out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the splits that had tiles.
+template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a)
+{
+    constexpr int TC = D / 4, ROWS = 256 / TC;  // threads over the channels, splits at a time
+    __shared__ float4 red[ROWS][TC];
+    __shared__ float tot[ROWS];
+    const int b = blockIdx.y, h = blockIdx.x;
+    const AttnTiles tl = attn_tiles(a.lens[b], a);
+    if (tl.T <= a.tiles_per_split) return;  // written by its only workgroup
+    const int used = min(a.splits, (tl.T + a.tiles_per_split - 1) / a.tiles_per_split);
+    const int64_t at = ((int64_t)b * a.heads + h) * a.splits;
+    float top = -INFINITY;
+    for (int s = 0; s < used; ++s) top = fmaxf(top, a.stat[at + s].x);
+    const float from = top == -INFINITY ? 0.0f : top;
+    const int c = threadIdx.x % TC, row = threadIdx.x / TC;
+    float4 o = make_float4(0, 0, 0, 0);
+    float l = 0.0f;
+    if (row < ROWS)
+        for (int s = row; s < used; s += ROWS) {
+            const float2 st = a.stat[at + s];
+            const float f = __builtin_amdgcn_exp2f(st.x - from);
+            const float4 v = reinterpret_cast<const float4 *>(a.part + (at + s) * D)[c];
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+            l += f * st.y;
+        }
+    if (row < ROWS) {
+        red[row][c] = o;
+        if (c == 0) tot[row] = l;
+    }
+    __syncthreads();
+    if (row == 0) {
+        for (int s = 1; s < ROWS; ++s) {
+            const float4 v = red[s][c];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+            l += tot[s];
+        }
+        uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h * D + 4 * c;
+        const uint32_t x = pack16<DT>(o.x / l, o.y / l), y = pack16<DT>(o.z / l, o.w / l);
+        out[0] = (uint16_t)x;
+        out[1] = (uint16_t)(x >> 16);
+        out[2] = (uint16_t)y;
+        out[3] = (uint16_t)(y >> 16);
+    }
+}
+
+AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks)
+{
+    const int head_tiles = (heads / kv_heads + 15) / 16;
+    int64_t tiles = ((int64_t)max_len + 31) / 32;
+    if (window > 0)  // a run of w keys touches at most w / 32 + 2 tiles
+        tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
+    tiles = std::max<int64_t>(tiles, 1);
+    const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
+    // about 2048 workgroups, each with at least one tile per wave
+    const int64_t want = std::min<int64_t>(std::max<int64_t>(2048 / rows, 1), 256);
+    AttnPlan p;
+    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, ATTN_WAVES);
+    p.splits = (int)((tiles + p.tiles_per_split - 1) / p.tiles_per_split);
+    return p;
+}
+
+template <int DT, int D> static int run_attn(const AttnArgs &a, hipStream_t s)
+{
+    const int G = std::min(16, a.heads / a.kv_heads);
+    const size_t lds = (size_t)(ATTN_WAVES * 32 + ATTN_WAVES * G * D) * sizeof(float);
+    int rc;
+    if ((rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_split<DT, D>), lds, "paged_attn")))
+        return rc;
+    hipLaunchKernelGGL((k_attn_split<DT, D>), dim3(a.splits, a.kv_heads * a.head_tiles, a.B),
+                       dim3(64 * ATTN_WAVES), lds, s, a);
+    if ((rc = check_launch("paged_attn_decode")) || a.splits == 1) return rc;
+    hipLaunchKernelGGL((k_attn_join<DT, D>), dim3(a.heads, a.B), dim3(256), 0, s, a);
+    return check_launch("paged_attn_decode join");
+}
+
+template <int DT> static int pick_dim(const AttnArgs &a, int D, hipStream_t s)
+{
+    switch (D) {
+    case 64: return run_attn<DT, 64>(a, s);
+    case 96: return run_attn<DT, 96>(a, s);
+    case 128: return run_attn<DT, 128>(a, s);
+    case 192: return run_attn<DT, 192>(a, s);
+    default: return run_attn<DT, 256>(a, s);
+    }
+}
+
+int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s)
+{
+    a.head_tiles = (a.heads / a.kv_heads + 15) / 16;
+    a.q_vec = (uintptr_t)a.q % 16 == 0 && a.ldq % 8 == 0;
+    return dtype == W4A4_BF16 ? pick_dim<W4A4_BF16>(a, D, s) : pick_dim<W4A4_F16>(a, D, s);
+}
+
+}  // namespace w4a4

@@ -227,6 +227,44 @@ int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const
                     const uint16_t *w_scale, int gshift, int N, uint16_t *Y, int64_t ldy, int epilogue,
                     const uint16_t *residual, int64_t ldr, hipStream_t s);
 
+// single-token path between two linears (k_decode.hip); 16-bit elements, strides in elements
+struct NormRopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t M, ldq, ldk, ldv;
+    int heads, kv_heads, D, rot;
+    const float *q_weight, *k_weight;  // [D] or nullptr: ones
+    float eps;
+    const double *inv_freq;    // [rot / 2]
+    const int64_t *positions;  // [M]
+    uint16_t *q_out, *k_out;   // k_out may be nullptr
+    int64_t ldqo, ldko;
+    uint16_t *k_cache, *v_cache;  // both or neither
+    int num_pages, page_size;
+    int64_t page_stride;
+    const int64_t *slots;  // [M]
+    int waves_per_token;   // set by the launcher
+};
+int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s);
+
+struct AttnArgs {
+    const uint16_t *q, *k_cache, *v_cache;
+    uint16_t *out;
+    int64_t ldq, ldo, page_stride, ldt;
+    const int32_t *table, *lens;
+    int B, heads, kv_heads, num_pages, page_size, page_shift, table_width, window, sinks;
+    float scale_log2;  // scale * log2(e)
+    int splits, tiles_per_split;
+    float2 *stat;  // [B][heads][splits] (maximum, sum)
+    float *part;   // [B][heads][splits][D]
+    int head_tiles;  // set by the launcher, as is q_vec
+    bool q_vec;
+};
+struct AttnPlan {
+    int splits, tiles_per_split;
+};
+AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks);
+int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s);
+
 // calibration (k_calib.hip)
 size_t zigzag_workspace(int K);
 int launch_zigzag(const void *W, int wdt, int N, int K, int64_t ldw, int B, int32_t *perm,
