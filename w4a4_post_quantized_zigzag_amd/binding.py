@@ -1,7 +1,8 @@
 """Thin ctypes binding of libw4a4.so (include/w4a4.h). Argument marshalling only: shapes and
 pointers are taken from torch tensors that live on the GPU, workspaces are torch allocations, and
 every call is enqueued on torch's current stream. All arithmetic runs in the library's HIP kernels;
-there is no fallback: if the library is missing, ``lib()`` raises."""
+there is no fallback: if the library is missing, ``lib()`` raises. The single-token calls at the end
+are marshalled by a compiled module instead of ctypes."""
 from __future__ import annotations
 
 import ctypes
@@ -483,52 +484,36 @@ def pack_weights_gptq(W, perm, U, block: int, Hf, dead=None):
 
 
 # ---------------------------------------------------------------------------------------------
-# Single-token path: group-scaled 4-bit linears. These calls run once per linear and token, so the
-# Python side is kept short: raw pointers as integers, and one look at the current device. They run
-# on the tensors' own device and on that device's current stream.
+# Single-token path: group-scaled 4-bit linears, norm + rotation + cache append, attention over the
+# paged cache. These calls run once per layer and token and take a few microseconds on the GPU, so
+# their marshalling is compiled (csrc/py_decode.cpp, module _decode beside the library). They run on
+# the tensors' own device and on that device's current stream; a wrong layout is a ValueError, a wrong
+# dtype a TypeError, anything the library refuses a W4A4Error.
 # ---------------------------------------------------------------------------------------------
 
+_native = None
+
+
+def _decode():
+    """The compiled marshalling of the single-token calls (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        import importlib
+        _torch()
+        lib()
+        try:
+            mod = importlib.import_module("._decode", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"{PKG}/_decode.so is missing or does not load ({e}): build it with "
+                               "`python -m w4a4_post_quantized_zigzag_amd.build`") from e
+        mod.init(W4A4Error)
+        _native = mod
+    return _native
+
+
 def _code16(t) -> int:
-    """W4A4_* code of an fp16, bf16 or fp32 tensor (the calls that take bf16)."""
-    torch = _torch()
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return W4A4_BF16
-    if dt is torch.float16:
-        return W4A4_F16
-    if dt is torch.float32:
-        return W4A4_F32
-    raise TypeError(f"unsupported dtype {dt}")
-
-
-def _launch(fn, tensors, *args):
-    """fn(*args, stream) on the tensors' device and its current stream. Every tensor must be on that
-    one GPU."""
-    torch = _torch()
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise ValueError(f"expected GPU tensors, got one on {dev}")
-    i = dev.index
-    if i == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(i).cuda_stream)
-    else:
-        with torch.cuda.device(i):
-            rc = fn(*args, torch.cuda.current_stream(i).cuda_stream)
-    if rc != W4A4_OK:
-        check(rc)
-
-
-def _ld(t) -> int:
-    """Row stride of a 2-D tensor (the row length where there is only one row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _want(cond, what: str):
-    if not cond:
-        raise ValueError(what)
+    """W4A4_* code of an fp16, fp32 or bf16 tensor (the calls that take bf16)."""
+    return W4A4_BF16 if t.dtype == _torch().bfloat16 else _dtype_code(t)
 
 
 def pack_weights_w4g(W, group: int):
@@ -536,11 +521,11 @@ def pack_weights_w4g(W, group: int):
     (wt uint8 [w4a4_w4g_operand_bytes], w_scale fp16 [K / group, N])."""
     torch = _torch()
     N, K = W.shape
-    L = lib()
-    wt = torch.empty(L.w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=W.device)
-    w_scale = torch.empty((max(K // group, 1) if group > 0 else 1, N), dtype=torch.float16, device=W.device)
-    _launch(L.w4a4_pack_weights_w4g, (W,), W.data_ptr(), _code16(W), N, K, _row_stride(W), group,
-            wt.data_ptr(), w_scale.data_ptr())
+    wt = torch.empty(lib().w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=W.device)
+    w_scale = torch.empty((max(K // max(group, 1), 1), N), dtype=torch.float16, device=W.device)
+    with torch.cuda.device(W.device):
+        check(lib().w4a4_pack_weights_w4g(_p(W), _code16(W), N, K, _row_stride(W), group, _p(wt),
+                                          _p(w_scale), _stream()))
     return wt, w_scale
 
 
@@ -548,120 +533,18 @@ def codes_to_w4g(codes, K: int):
     """The operand of gemv_w4g from packed int4 codes [N, K / 2] (as pack_weights_gptq's wq)."""
     torch = _torch()
     N = codes.shape[0]
-    _want(codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape == (N, K // 2),
-          "codes must be contiguous uint8 [N, K / 2]")
-    L = lib()
-    wt = torch.empty(L.w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=codes.device)
-    _launch(L.w4a4_codes_to_w4g, (codes,), codes.data_ptr(), N, K, wt.data_ptr())
+    if codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.shape != (N, K // 2):
+        raise ValueError("codes must be contiguous uint8 [N, K / 2]")
+    wt = torch.empty(lib().w4a4_w4g_operand_bytes(N, K), dtype=torch.uint8, device=codes.device)
+    with torch.cuda.device(codes.device):
+        check(lib().w4a4_codes_to_w4g(_p(codes), N, K, _p(wt), _stream()))
     return wt
 
 
 def gemv_w4g(X, wt, w_scale, Y=None, epilogue: int = EPI_NONE, residual=None):
     """Y [M, N] = X [M, K] times the group-scaled 4-bit weights (wt, w_scale [K / group, N]), with an
-    epilogue. X fp16, fp32 or bf16; Y and residual fp16, for bf16 X bf16."""
-    torch = _torch()
-    M, K = X.shape
-    groups, N = w_scale.shape
-    dt = _code16(X)
-    ydt = torch.bfloat16 if dt == W4A4_BF16 else torch.float16
-    L = lib()
-    _want(X.stride(1) == 1 or K == 1, "X must have unit column stride")
-    _want(groups > 0 and K % groups == 0, f"K = {K} does not hold {groups} groups")
-    _want(w_scale.dtype is torch.float16 and w_scale.is_contiguous(), "w_scale must be contiguous fp16")
-    _want(wt.dtype is torch.uint8 and wt.is_contiguous()
-          and wt.numel() == ((N + 15) // 16) * ((K + 127) // 128) * 1024, "wt does not hold [N, K] weights")
-    if Y is None:
-        Y = torch.empty((M, N), dtype=ydt, device=X.device)
-    else:
-        _want(Y.dtype is ydt and Y.shape == (M, N) and Y.stride(1) == 1, f"Y must be {ydt} [M, N]")
-    if residual is None:
-        _launch(L.w4a4_gemv_w4g, (X, wt, w_scale, Y), X.data_ptr(), dt, M, K, _ld(X),
-                wt.data_ptr(), w_scale.data_ptr(), K // groups, N, Y.data_ptr(), _ld(Y),
-                epilogue, None, 0)
-    else:
-        _want(residual.dtype is ydt and residual.shape == (M, N) and residual.stride(1) == 1,
-              f"residual must be {ydt} [M, N]")
-        _launch(L.w4a4_gemv_w4g, (X, wt, w_scale, Y, residual), X.data_ptr(), dt, M, K,
-                _ld(X), wt.data_ptr(), w_scale.data_ptr(), K // groups, N, Y.data_ptr(),
-                _ld(Y), epilogue, residual.data_ptr(), _ld(residual))
-    return Y
-
-
-def _code_heads(t, name: str) -> int:
-    """W4A4_* code of an fp16 or bf16 tensor [rows, heads, head_dim] whose heads are adjacent."""
-    torch = _torch()
-    _want(t.dim() == 3 and t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1),
-          f"{name} must be [rows, heads, head_dim] with adjacent heads")
-    if t.dtype is torch.bfloat16:
-        return W4A4_BF16
-    if t.dtype is torch.float16:
-        return W4A4_F16
-    raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-
-
-def _ld3(t) -> int:
-    """Row stride of [rows, heads, head_dim]."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _cache_shape(k_cache, v_cache, dtype, kv_heads: int, D: int):
-    """(pages, page_size, page_stride) of the paged cache arrays [pages, kv_heads, page_size, D]."""
-    P, KV, page, d = k_cache.shape
-    st = k_cache.stride()
-    _want(KV == kv_heads and d == D and k_cache.dtype is dtype and v_cache.dtype is dtype,
-          f"cache must be {dtype} [pages, {kv_heads}, page_size, {D}]")
-    _want(v_cache.shape == k_cache.shape and v_cache.stride() == st, "k_cache and v_cache must be laid out alike")
-    _want(st[3] == 1 and st[2] == D and (st[1] == page * D or KV == 1), "a cache page must be dense")
-    return P, page, st[0] if P > 1 else KV * page * D
-
-
-def _index(t, dtype, shape, name: str):
-    _want(t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous(),
-          f"{name} must be contiguous {dtype} {list(shape)}")
-    return t.data_ptr()
-
-
-def _norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out, k_cache,
-               v_cache, slots):
-    torch = _torch()
-    M, H, D = q.shape
-    KV = k.shape[1]
-    dt = _code_heads(q, "q")
-    _want(_code_heads(k, "k") == dt and k.shape[0] == M and k.shape[2] == D, "k must be [M, kv_heads, D] of q's type")
-    if q_out is None:
-        q_out = torch.empty((M, H, D), dtype=q.dtype, device=q.device)
-    else:
-        _want(_code_heads(q_out, "q_out") == dt and q_out.shape == q.shape, "q_out must be like q")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    used = [q, k, q_out]
-    ptr = {}
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        ptr[name] = None
-        if w is not None:
-            ptr[name] = _index(w, torch.float32, (D,), name)
-            used.append(w)
-    fp = pp = None
-    if rot:
-        fp = _index(inv_freq, torch.float64, (rot // 2,), "inv_freq")
-        pp = _index(positions, torch.int64, (M,), "positions")
-        used += (inv_freq, positions)
-    kop = None
-    if k_out is not None:
-        _want(_code_heads(k_out, "k_out") == dt and k_out.shape == k.shape, "k_out must be like k")
-        kop = k_out.data_ptr()
-        used.append(k_out)
-    vp = kcp = vcp = sp = None
-    P = page = stride = ldv = 0
-    if k_cache is not None:
-        _want(_code_heads(v, "v") == dt and v.shape == k.shape, "v must be like k")
-        P, page, stride = _cache_shape(k_cache, v_cache, q.dtype, KV, D)
-        sp = _index(slots, torch.int64, (M,), "slots")
-        vp, ldv, kcp, vcp = v.data_ptr(), _ld3(v), k_cache.data_ptr(), v_cache.data_ptr()
-        used += (v, k_cache, v_cache, slots)
-    _launch(lib().w4a4_qk_norm_rope, used, q.data_ptr(), k.data_ptr(), vp, dt, M, H, KV, D, _ld3(q), _ld3(k),
-            ldv, ptr["q_weight"], ptr["k_weight"], eps, fp, rot, 1 if interleaved else 0, pp,
-            q_out.data_ptr(), _ld3(q_out), kop, _ld3(k_out) if kop else 0, kcp, vcp, P, page, stride, sp)
-    return q_out
+    epilogue. X fp16, fp32 or bf16; Y and residual fp16, for bf16 X bf16. Y may be the residual."""
+    return (_native or _decode()).gemv(X, wt, w_scale, Y, epilogue, residual)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps: float = 1e-6,
@@ -670,19 +553,20 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps: float = 1e-
     pass. Weights fp32 [D] or None, inv_freq fp64 [rot / 2] or None (no rotation), positions int64 [M].
     Returns (q_out, k_out), which may be q and k themselves."""
     if k_out is None:
-        k_out = _torch().empty(k.shape, dtype=k.dtype, device=k.device)
-    return _norm_rope(q, k, None, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
-                      None, None, None), k_out
+        torch = _torch()
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    return (_native or _decode()).norm_rope(q, k, None, q_weight, k_weight, inv_freq, positions, eps,
+                                            interleaved, q_out, k_out, None, None, None), k_out
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, k_cache, v_cache, slots,
                         eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None):
     """qk_norm_rope with the keys and values written to slots int64 [M] (page * page_size + offset, or
     -1) of the paged cache [pages, kv_heads, page_size, D]. Returns q_out."""
-    _want(k_cache is not None and v_cache is not None and slots is not None and v is not None,
-          "v, k_cache, v_cache and slots are required")
-    return _norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
-                      k_cache, v_cache, slots)
+    if k_cache is None or v_cache is None:
+        raise ValueError("v, k_cache, v_cache and slots are required")
+    return (_native or _decode()).norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps,
+                                            interleaved, q_out, k_out, k_cache, v_cache, slots)
 
 
 def paged_attn_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, window: int = 0,
@@ -690,30 +574,6 @@ def paged_attn_decode(q, k_cache, v_cache, table, lens, scale: float | None = No
     """Attention of one new token per sequence, q [B, heads, D], over the first lens[b] tokens of the
     paged cache [pages, kv_heads, page_size, D] through table int32 [B, width]; lens int32 [B]. window >
     0: only the last `window` and the first `sinks` tokens. scale defaults to D ** -0.5, max_len (what the
-    work is split for) to what the table holds."""
-    torch = _torch()
-    B, H, D = q.shape
-    KV = k_cache.shape[1]
-    dt = _code_heads(q, "q")
-    P, page, stride = _cache_shape(k_cache, v_cache, q.dtype, KV, D)
-    _want(table.dtype is torch.int32 and table.dim() == 2 and table.shape[0] == B
-          and (table.stride(1) == 1 or table.shape[1] == 1), "table must be int32 [B, width]")
-    width = table.shape[1]
-    lp = _index(lens, torch.int32, (B,), "lens")
-    if max_len is None:
-        max_len = width * page
-    if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
-    else:
-        _want(_code_heads(out, "out") == dt and out.shape == q.shape, "out must be like q")
-    L = lib()
-    if ws is None:
-        nb = L.w4a4_paged_attn_workspace_bytes(B, H, KV, D, max_len, window, sinks)
-        if nb:
-            ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
-    used = (q, k_cache, v_cache, table, lens, out) if ws is None else (q, k_cache, v_cache, table, lens, out, ws)
-    _launch(L.w4a4_paged_attn_decode, used, q.data_ptr(), dt, B, H, KV, D, _ld3(q), k_cache.data_ptr(),
-            v_cache.data_ptr(), P, page, stride, table.data_ptr(), width, table.stride(0) if B > 1 else width,
-            lp, max_len, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ld3(out),
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
-    return out
+    work is split for) to what the table holds. ws: a workspace of w4a4_paged_attn_workspace_bytes."""
+    return (_native or _decode()).paged_attn(q, k_cache, v_cache, table, lens, scale, window, sinks, max_len,
+                                             out, ws)

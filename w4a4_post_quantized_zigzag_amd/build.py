@@ -1,10 +1,12 @@
-"""Build libw4a4.so in-tree with hipcc for gfx950 (python -m w4a4_post_quantized_zigzag_amd.build)."""
+"""Build libw4a4.so in-tree with hipcc for gfx950, and the torch-facing marshalling of the single-token
+calls beside it (python -m w4a4_post_quantized_zigzag_amd.build)."""
 from __future__ import annotations
 
 import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,18 +35,41 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_marshalling() -> str:
+    """_decode.so: host code against torch's headers and the library just linked beside it."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    out = os.path.join(PKG, "_decode.so")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__=1",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"]]
+    for p in include_paths():
+        cmd += ["-isystem", p]
+    cmd += [os.path.join(CSRC, "py_decode.cpp"), "-o", out + ".tmp", LIB,
+            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"marshalling build failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
+    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-soname,libw4a4.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    mod = _build_marshalling()
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {mod}")
     return LIB
 
 
