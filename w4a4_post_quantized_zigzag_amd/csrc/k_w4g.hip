@@ -12,7 +12,7 @@
 //    group scale per lane is folded in (fp32 FMA) after each group's exact-product partial sum.
 //  - The waves of a workgroup share one tile of 16 channels and split K; their partial sums meet in
 //    LDS in a fixed order, so results do not depend on timing.
-#include <type_traits>
+#include <algorithm>
 
 #include "w4a4_internal.h"
 
@@ -155,28 +155,42 @@ template <int DT> __device__ __forceinline__ uint16_t store_y(float v)
     else return __half_as_ushort(__float2half_rn(v));
 }
 
+// Orders one wave's LDS writes and reads of other lanes' data (the hardware keeps a wave's LDS accesses
+// in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void turn_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // One workgroup: 16 output channels (blockIdx.x) of 16 MT rows (blockIdx.y), its waves splitting the
 // 128-k stages round-robin. GS groups per stage (1 for group >= 128). U stages are in flight per
 // wave: all their loads are issued before the first is used.
-template <int DT, int MT, int GS, bool VEC, int U, int MAXW>
+//
+// The matrix operand wants neighbouring lanes in neighbouring rows; loading the activations that way
+// touches 64 cache lines per instruction. A wave therefore loads each row's 256 bytes of a stage with
+// 16 neighbouring lanes and turns the 16 x 128 tile in its own corner of LDS (no barrier), where run c
+// of row r sits in slot c ^ r so that both sides are free of bank conflicts.
+// Q: quads of rows that a tile has at most (1 for M <= 4, so that its loads need no registers for more).
+template <int DT, int MT, int Q, int GS, bool VEC, int U, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 {
     typedef typename ActOf<DT>::raw raw;
     constexpr int P = ActOf<DT>::PARTS;
-    extern __shared__ float red[];  // [waves][MT][4][64]
+    // per wave: the tile in turn [P][16][16 slots] of 16 bytes; afterwards [waves][MT][4][64] floats
+    extern __shared__ u4_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int nt = blockIdx.x, m0 = blockIdx.y * (16 * MT);
     const int stages = (a.K + 127) >> 7, ngroups = a.K >> (5 + a.gshift);
-    const int n = nt * 16 + r, ns = min(n, a.N - 1);
+    const int ns = min(nt * 16 + r, a.N - 1);
+    u4_t *turn = lds + wave * (P * 256);
 
     const uint8_t *wp = a.wt + ((int64_t)nt * stages * 64 + lane) * 16;
     const uint16_t *sp = a.w_scale + ns;
-    const raw *xp[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)  // rows past M repeat the last one; their results are not stored
-        xp[t] = reinterpret_cast<const raw *>(a.X) +
-                (int64_t)min(m0 + 16 * t + r, a.M - 1) * a.ldx + 8 * g;
+    // as loader: lane (g, r) holds run r of rows 4 q + g
+    const raw *xp = reinterpret_cast<const raw *>(a.X) + (int64_t)(m0 + g) * a.ldx + 8 * r;
+    const int rows = a.M - m0 - g;  // row 16 t + 4 q + g exists if 16 t + 4 q < rows
 
     f4_t acc[MT];
 #pragma unroll
@@ -185,7 +199,7 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     for (int s0 = wave; s0 < stages; s0 += waves * U) {
         u4_t w[U];
         uint16_t sc[U][GS];
-        ActRun<DT> x[U][4][MT];
+        ActRun<DT> x[U][MT][Q];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = min(s0 + u * waves, stages - 1);
@@ -195,45 +209,54 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
                 const int grp = GS == 1 ? (s * 4) >> a.gshift : s * GS + q;
                 sc[u][q] = sp[(int64_t)min(grp, ngroups - 1) * a.N];
             }
+            const bool in = s * 128 + 8 * r < a.K;  // runs past K (the last stage) are not used
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // a run past K (the last stage of K % 128 != 0) reads the row's start instead
-                const int k = s * 128 + 32 * j;
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int t = 0; t < MT; ++t) x[u][j][t] = load_run<DT, VEC>(xp[t] + (k < a.K ? k : 0));
-            }
+                for (int q = 0; q < Q; ++q)
+                    if (in && 16 * t + 4 * q < rows)
+                        x[u][t][q] = load_run<DT, VEC>(xp + (int64_t)(16 * t + 4 * q) * a.ldx + s * 128);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * waves;
             if (u > 0 && s >= stages) break;
-            f4_t part[MT];
+            u4_t b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (s * 128 + 32 * j >= a.K) break;  // codes past K are zeros; x there is not x
-                const u4_t b = DT == W4A4_F16 ? widen_f16(w[u][j]) : widen_bf16(w[u][j]);
+            for (int j = 0; j < 4; ++j) b[j] = DT == W4A4_F16 ? widen_f16(w[u][j]) : widen_bf16(w[u][j]);
+            float f[GS];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
+            for (int q = 0; q < GS; ++q)
+                f[q] = __half2float(__ushort_as_half(sc[u][q])) * (DT == W4A4_F16 ? 1.0f : 16.0f);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                // rows past M leave what the slot held: their results are not stored
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
                     u4_t p[P];
-                    act_parts<DT>(x[u][j][t], p);
-                    if (j % (4 / GS) == 0) part[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    act_parts<DT>(x[u][t][q], p);
 #pragma unroll
-                    for (int q = P - 1; q >= 0; --q) part[t] = mma<DT>(p[q], b, part[t]);
-                    if (GS > 1 && (j + 1) % (4 / GS) == 0) {
-                        const float f = __half2float(__ushort_as_half(sc[u][j * GS / 4])) *
-                                        (DT == W4A4_F16 ? 1.0f : 16.0f);
-                        acc[t] += part[t] * f;
-                    }
+                    for (int i = 0; i < P; ++i) turn[(i * 16 + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
                 }
-            }
-            if (GS == 1) {
-                const float f = __half2float(__ushort_as_half(sc[u][0])) * (DT == W4A4_F16 ? 1.0f : 16.0f);
+                turn_fence();
+                f4_t part;
 #pragma unroll
-                for (int t = 0; t < MT; ++t) acc[t] += part[t] * f;
+                for (int j = 0; j < 4; ++j) {
+                    if (s * 128 + 32 * j >= a.K) break;  // nothing there
+                    if (j % (4 / GS) == 0) part = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = P - 1; i >= 0; --i)
+                        part = mma<DT>(turn[(i * 16 + r) * 16 + ((4 * j + g) ^ r)], b[j], part);
+                    if (GS > 1 && (j + 1) % (4 / GS) == 0) acc[t] += part * f[j * GS / 4];
+                }
+                turn_fence();
+                if (GS == 1) acc[t] += part * f[0];
             }
         }
     }
 
+    float *red = reinterpret_cast<float *>(lds);
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -251,35 +274,38 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     }
 }
 
-template <int DT, int MT, int GS, bool VEC>
+template <int DT, int MT, int Q, int GS, bool VEC>
 static int run_gemv(const W4gArgs &a, hipStream_t s)
 {
-    constexpr int U = (MT == 1 && DT != W4A4_F32) ? 4 : (MT <= 2 && DT != W4A4_F32) ? 2 : 1;
-    constexpr int MAXW = MT == 1 ? 16 : 8;
+    constexpr int U = DT == W4A4_F32 ? (Q == 1 ? 2 : 1) : Q == 1 ? 4 : MT == 1 ? 2 : 1;
+    constexpr int MAXW = MT == 1 && DT != W4A4_F32 ? 16 : 8;  // at most 96 KB of LDS
     const int tiles = (a.N + 15) / 16, rows = (a.M + 16 * MT - 1) / (16 * MT);
     const int stages = (a.K + 127) / 128;
     int waves = 1;
     while (waves < MAXW && waves * 2 <= stages && (waves < 4 || (int64_t)tiles * rows * waves < 4096)) waves *= 2;
-    hipLaunchKernelGGL((k_gemv_w4g<DT, MT, GS, VEC, U, MAXW>), dim3(tiles, rows), dim3(64 * waves),
-                       (size_t)waves * MT * 1024, s, a);
+    const size_t lds = (size_t)waves * 1024 * std::max(4 * ActOf<DT>::PARTS, MT);
+    const auto kernel = k_gemv_w4g<DT, MT, Q, GS, VEC, U, MAXW>;
+    if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, "gemv_w4g")) return rc;
+    hipLaunchKernelGGL(kernel, dim3(tiles, rows), dim3(64 * waves), lds, s, a);
     return check_launch("gemv_w4g");
 }
 
-template <int DT, int MT>
+template <int DT, int MT, int Q>
 static int pick_group(const W4gArgs &a, hipStream_t s)
 {
     const size_t eb = sizeof(typename ActOf<DT>::raw);
     const bool vec = (uintptr_t)a.X % 16 == 0 && (a.ldx * eb) % 16 == 0;
-    if (a.gshift == 0) return vec ? run_gemv<DT, MT, 4, true>(a, s) : run_gemv<DT, MT, 4, false>(a, s);
-    if (a.gshift == 1) return vec ? run_gemv<DT, MT, 2, true>(a, s) : run_gemv<DT, MT, 2, false>(a, s);
-    return vec ? run_gemv<DT, MT, 1, true>(a, s) : run_gemv<DT, MT, 1, false>(a, s);
+    if (a.gshift == 0) return vec ? run_gemv<DT, MT, Q, 4, true>(a, s) : run_gemv<DT, MT, Q, 4, false>(a, s);
+    if (a.gshift == 1) return vec ? run_gemv<DT, MT, Q, 2, true>(a, s) : run_gemv<DT, MT, Q, 2, false>(a, s);
+    return vec ? run_gemv<DT, MT, Q, 1, true>(a, s) : run_gemv<DT, MT, Q, 1, false>(a, s);
 }
 
 template <int DT> static int pick_rows(const W4gArgs &a, hipStream_t s)
 {
-    if (a.M <= 16) return pick_group<DT, 1>(a, s);
-    if (a.M <= 32) return pick_group<DT, 2>(a, s);
-    return pick_group<DT, 4>(a, s);
+    if (a.M <= 4) return pick_group<DT, 1, 1>(a, s);
+    if (a.M <= 16) return pick_group<DT, 1, 4>(a, s);
+    if (a.M <= 32) return pick_group<DT, 2, 4>(a, s);
+    return pick_group<DT, 4, 4>(a, s);
 }
 
 int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
