@@ -30,16 +30,20 @@ typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 // Nibble position p < 4 holds k = 2p of its run and p >= 4 holds k = 2 (p - 4) + 1, so that the two
 // halves of (w >> 4 i) & 0x000F000F are neighbours in k.
 
-// fp16: 0x6400 | u is 1024 + u exactly; subtracting 1032 leaves the code u - 8.
+// fp16: with u in the low four bits of the mantissa, 0x6400 | u is 1024 + u; in the next four, 0x5400 |
+// 16 u is 64 + u, which saves the shift. Subtracting 1032 or 72 leaves the code u - 8, all exactly. The
+// or-mask is kept in a register: v_and_or_b32 takes one scalar constant only.
 __device__ __forceinline__ u4_t widen_f16(uint32_t w)
 {
+    uint32_t m0 = 0x64006400u, m1 = 0x54005400u;
+    asm("" : "+v"(m0), "+v"(m1));
+    const h2_t b0 = {(_Float16)1032.0f, (_Float16)1032.0f}, b1 = {(_Float16)72.0f, (_Float16)72.0f};
+    const uint32_t v = w >> 8;
     u4_t r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t t = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-        const h2_t h = __builtin_bit_cast(h2_t, t) - h2_t{(_Float16)1032.0f, (_Float16)1032.0f};
-        r[i] = __builtin_bit_cast(uint32_t, h);
-    }
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, (w & 0x000F000Fu) | m0) - b0);
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, (w & 0x00F000F0u) | m1) - b1);
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, (v & 0x000F000Fu) | m0) - b0);
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, (v & 0x00F000F0u) | m1) - b1);
     return r;
 }
 
@@ -53,12 +57,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 __device__ __forceinline__ u4_t widen_bf16(uint32_t w)
 {
     const uint32_t a = w ^ 0x88888888u, b = a >> 4;
-    auto c = [](uint32_t v) { return __builtin_amdgcn_cvt_off_f32_i4((int)v); };
+    // byte extracts fold into the conversions' operand selection
+    auto c = [](uint32_t v, int byte) {
+        return __builtin_amdgcn_cvt_off_f32_i4((int)(byte == 0 ? v : (v >> (8 * byte)) & 0xFFu));
+    };
     u4_t r;
-    r[0] = pack_bf16(c(a), c(a >> 16));
-    r[1] = pack_bf16(c(b), c(b >> 16));
-    r[2] = pack_bf16(c(a >> 8), c(a >> 24));
-    r[3] = pack_bf16(c(b >> 8), c(b >> 24));
+    r[0] = pack_bf16(c(a, 0), c(a, 2));
+    r[1] = pack_bf16(c(b, 0), c(b, 2));
+    r[2] = pack_bf16(c(a, 1), c(a, 3));
+    r[3] = pack_bf16(c(b, 1), c(b, 3));
     return r;
 }
 
@@ -74,21 +81,15 @@ template <int DT> struct ActRun {
     u4_t v[DT == W4A4_F32 ? 2 : 1];
 };
 
-template <int DT, bool VEC>
+// Rows start anywhere an element may: the hardware's vector loads take any address.
+template <int DT>
 __device__ __forceinline__ ActRun<DT> load_run(const typename ActOf<DT>::raw *__restrict__ p)
 {
+    typedef uint32_t run_t __attribute__((ext_vector_type(4), aligned(2)));
+    const run_t *q = reinterpret_cast<const run_t *>(p);
     ActRun<DT> r;
-    if (VEC) {
-        const u4_t *q = reinterpret_cast<const u4_t *>(p);
-        r.v[0] = q[0];
-        if constexpr (DT == W4A4_F32) r.v[1] = q[1];
-    } else if constexpr (DT == W4A4_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i / 4][i % 4] = p[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.v[0][i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-    }
+    r.v[0] = q[0];
+    if constexpr (DT == W4A4_F32) r.v[1] = q[1];
     return r;
 }
 
@@ -128,6 +129,12 @@ template <int DT> __device__ __forceinline__ f4_t mma(const u4_t &a, const u4_t 
                                                        __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
 }
 
+#ifndef W4G_F4_TILES
+#define W4G_F4_TILES 64
+#define W4G_F2_TILES 128
+#define W4G_TN4 1024
+#define W4G_TN2 512
+#endif
 struct W4gArgs {
     const void *X;
     int64_t ldx;
@@ -163,149 +170,238 @@ __device__ __forceinline__ void turn_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// One workgroup: 16 output channels (blockIdx.x) of 16 MT rows (blockIdx.y), its waves splitting the
-// 128-k stages round-robin. GS groups per stage (1 for group >= 128). U stages are in flight per
-// wave: all their loads are issued before the first is used.
+// One workgroup: TN tiles of C = 16 / F output channels (blockIdx.x) for 16 MT rows (blockIdx.y), its
+// waves splitting K. A wave turns the activations of U steps into matrix operands once and keeps them in
+// registers over its TN tiles. All loads of the next steps are in flight while it works on these. GS groups
+// per 128-k stage (1 for group >= 128).
+//
+// F (1, 2, 4; MT = 1): few activation rows leave most of the 16 x 16 results of a product unused, and few
+// output channels leave CUs without work. With F > 1 a product takes F stages at once: row and column
+// f C + i of the operands hold row i of the activations and channel i of stage f, so that its F diagonal
+// blocks are partial sums of the same C x C results. One step is then F stages, a workgroup has C channels
+// and the grid F times as many workgroups. Needs M <= C.
 //
 // The matrix operand wants neighbouring lanes in neighbouring rows; loading the activations that way
 // touches 64 cache lines per instruction. A wave therefore loads each row's 256 bytes of a stage with
 // 16 neighbouring lanes and turns the 16 x 128 tile in its own corner of LDS (no barrier), where run c
 // of row r sits in slot c ^ r so that both sides are free of bank conflicts.
-// Q: quads of rows that a tile has at most (1 for M <= 4, so that its loads need no registers for more).
-template <int DT, int MT, int Q, int GS, bool VEC, int U, int MAXW>
+// Q: quads of operand rows that hold activations at most (1 for M <= 4 with F = 1, else 4).
+template <int DT, int F, int MT, int Q, int GS, int U, int TN> struct GemvStep {
+    u4_t w[U][TN];
+    uint16_t sc[U][TN][GS];
+    ActRun<DT> x[U][MT][Q];
+};
+
+template <int DT, int F, int MT, int Q, int GS, int U, int TN, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 {
     typedef typename ActOf<DT>::raw raw;
-    constexpr int P = ActOf<DT>::PARTS;
-    // per wave: the tile in turn [P][16][16 slots] of 16 bytes; afterwards [waves][MT][4][64] floats
+    constexpr int P = ActOf<DT>::PARTS, C = 16 / F;
+    constexpr int TILE = P * 4 * Q * 16;  // 16-byte slots of a tile in turn
+    // per wave: one step's tiles in turn [U][MT][P][4 Q][16]; afterwards [waves][TN][MT][4][64] floats
     extern __shared__ u4_t lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int nt = blockIdx.x, m0 = blockIdx.y * (16 * MT);
-    const int stages = (a.K + 127) >> 7, ngroups = a.K >> (5 + a.gshift);
-    const int ns = min(nt * 16 + r, a.N - 1);
-    u4_t *turn = lds + wave * (P * 256);
+    const int c0 = blockIdx.x * (TN * C), m0 = blockIdx.y * (16 * MT);
+    const int stages = (a.K + 127) >> 7, steps = (stages + F - 1) / F, ngroups = a.K >> (5 + a.gshift);
+    u4_t *turn = lds + wave * (U * MT * TILE);
 
-    const uint8_t *wp = a.wt + ((int64_t)nt * stages * 64 + lane) * 16;
-    const uint16_t *sp = a.w_scale + ns;
-    // as loader: lane (g, r) holds run r of rows 4 q + g
-    const raw *xp = reinterpret_cast<const raw *>(a.X) + (int64_t)(m0 + g) * a.ldx + 8 * r;
-    const int rows = a.M - m0 - g;  // row 16 t + 4 q + g exists if 16 t + 4 q < rows
-
-    f4_t acc[MT];
+    // as holder of the weight operand: channel c0 + t C + r % C of stage F step + r / C
+    const int wfold = r / C, last_tile = (a.N - 1) >> 4;
+    const uint8_t *wp[TN];
+    const uint16_t *sp[TN];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < TN; ++t) {
+        const int col = c0 + t * C + r % C;  // a tile past N reads the last one; nothing of it is stored
+        wp[t] = a.wt + ((int64_t)min(col >> 4, last_tile) * stages * 64 + g * 16 + (col & 15)) * 16;
+        sp[t] = a.w_scale + min(col, a.N - 1);
+    }
+    // as loader: lane (g, r) holds run r of operand rows 4 q + g, row (4 q + g) % C of stage (4 q + g) / C
+    const raw *xp = reinterpret_cast<const raw *>(a.X) + (int64_t)(m0 + g) * a.ldx + 8 * r;
+    const int rows = a.M - m0 - g, kleft = a.K - 8 * r;
 
-    for (int s0 = wave; s0 < stages; s0 += waves * U) {
-        u4_t w[U];
-        uint16_t sc[U][GS];
-        ActRun<DT> x[U][MT][Q];
+    f4_t acc[TN][MT];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    typedef GemvStep<DT, F, MT, Q, GS, U, TN> Step;
+    // activations first: they are needed first, and the weights can then be used as they arrive
+    auto load = [&](int s0, Step &d) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int s = min(s0 + u * waves, stages - 1);
-            w[u] = __builtin_nontemporal_load(reinterpret_cast<const u4_t *>(wp + (int64_t)s * 1024));
+            const int step = s0 + u * waves;
 #pragma unroll
-            for (int q = 0; q < GS; ++q) {
-                const int grp = GS == 1 ? (s * 4) >> a.gshift : s * GS + q;
-                sc[u][q] = sp[(int64_t)min(grp, ngroups - 1) * a.N];
-            }
-            const bool in = s * 128 + 8 * r < a.K;  // runs past K (the last stage) are not used
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int q = 0; q < Q; ++q)
-                    if (in && 16 * t + 4 * q < rows)
-                        x[u][t][q] = load_run<DT, VEC>(xp + (int64_t)(16 * t + 4 * q) * a.ldx + s * 128);
+                for (int q = 0; q < Q; ++q) {
+                    // rows past M and runs past K (whole stages too) are zeros
+                    const int row = F == 1 ? 16 * m + 4 * q : (4 * q) % C, k = (step * F + 4 * q / C) * 128;
+                    d.x[u][m][q] = ActRun<DT>{};
+                    if (row < rows && k < kleft)
+                        d.x[u][m][q] = load_run<DT>(xp + (int64_t)row * a.ldx + k);
+                }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * waves;
-            if (u > 0 && s >= stages) break;
-            u4_t b[4];
+            const int step = s0 + u * waves;
+            if (u > 0 && step >= steps) break;
+            const int s = F == 1 ? step : min(step * F + wfold, stages - 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = DT == W4A4_F16 ? widen_f16(w[u][j]) : widen_bf16(w[u][j]);
-            float f[GS];
+            for (int t = 0; t < TN; ++t)
 #pragma unroll
-            for (int q = 0; q < GS; ++q)
-                f[q] = __half2float(__ushort_as_half(sc[u][q])) * (DT == W4A4_F16 ? 1.0f : 16.0f);
+                for (int q = 0; q < GS; ++q) {
+                    const int grp = GS == 1 ? (s * 4) >> a.gshift : min(s * GS + q, ngroups - 1);
+                    d.sc[u][t][q] = sp[t][(int64_t)grp * a.N];
+                }
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                // rows past M leave what the slot held: their results are not stored
+            for (int t = 0; t < TN; ++t)
+                d.w[u][t] = *reinterpret_cast<const u4_t *>(wp[t] + (int64_t)s * 1024);
+        }
+    };
+    u4_t x[U][MT][P][4];
+    auto turn_rows = [&](const Step &d) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     u4_t p[P];
-                    act_parts<DT>(x[u][t][q], p);
+                    act_parts<DT>(d.x[u][m][q], p);
 #pragma unroll
-                    for (int i = 0; i < P; ++i) turn[(i * 16 + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
+                    for (int i = 0; i < P; ++i)
+                        turn[(u * MT + m) * TILE + (i * 4 * Q + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
                 }
-                turn_fence();
-                f4_t part;
+        turn_fence();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // with one quad of rows the operand's other rows repeat them
+                        x[u][m][i][j] = turn[(u * MT + m) * TILE + (i * 4 * Q + r % (4 * Q)) * 16 +
+                                             ((4 * j + g) ^ (r % (4 * Q)))];
+        turn_fence();
+    };
+    auto multiply = [&](int s0, const Step &d) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u > 0 && s0 + u * waves >= steps) break;
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                f4_t part[MT];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (s * 128 + 32 * j >= a.K) break;  // nothing there
-                    if (j % (4 / GS) == 0) part = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    const u4_t b = DT == W4A4_F16 ? widen_f16(d.w[u][t][j]) : widen_bf16(d.w[u][t][j]);
 #pragma unroll
-                    for (int i = P - 1; i >= 0; --i)
-                        part = mma<DT>(turn[(i * 16 + r) * 16 + ((4 * j + g) ^ r)], b[j], part);
-                    if (GS > 1 && (j + 1) % (4 / GS) == 0) acc[t] += part * f[j * GS / 4];
+                    for (int m = 0; m < MT; ++m) {
+                        if (j % (4 / GS) == 0) part[m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int i = P - 1; i >= 0; --i) part[m] = mma<DT>(x[u][m][i][j], b, part[m]);
+                    }
+                    if ((j + 1) % (4 / GS) == 0) {
+                        const float f = __half2float(__ushort_as_half(d.sc[u][t][j * GS / 4])) *
+                                        (DT == W4A4_F16 ? 1.0f : 16.0f);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) acc[t][m] += part[m] * f;
+                    }
                 }
-                turn_fence();
-                if (GS == 1) acc[t] += part * f[0];
             }
         }
+    };
+
+    Step cur;
+    load(wave, cur);  // there are no more waves than steps
+    int s0 = wave;
+    for (; s0 + waves * U < steps; s0 += waves * U) {
+        turn_rows(cur);
+        Step next;
+        load(s0 + waves * U, next);
+        multiply(s0, cur);
+        cur = next;
     }
+    turn_rows(cur);
+    multiply(s0, cur);
 
     float *red = reinterpret_cast<float *>(lds);
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < TN; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[((wave * MT + t) * 4 + i) * 64 + lane] = acc[t][i];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[(((wave * TN + t) * MT + m) * 4 + i) * 64 + lane] = acc[t][m][i];
     __syncthreads();
-    for (int e = tid; e < MT * 256; e += blockDim.x) {
-        const int l = e & 63, i = (e >> 6) & 3, t = e >> 8;
-        const int m = m0 + 16 * t + 4 * (l >> 4) + i, col = nt * 16 + (l & 15);
-        if (m >= a.M || col >= a.N) continue;
+    // result (m, c) of a tile: operand row f C + m (lanes of group row / 4, register row % 4), column f C + c
+    const int live = min(a.M - m0, F == 1 ? 16 * MT : C);
+    for (int e = tid; e < TN * C * live; e += blockDim.x) {
+        const int c = e % C, t = e / C % TN, m = e / (C * TN);
+        const int col = c0 + t * C + c;
+        if (col >= a.N) continue;
         float y = 0.0f;
-        for (int v = 0; v < waves; ++v) y += red[v * (MT * 256) + e];
+        for (int v = 0; v < waves; ++v)
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int row = f * C + m;
+                y += red[(((v * TN + t) * MT + row / 16) * 4 + row % 4) * 64 + (row % 16) / 4 * 16 + f * C + c];
+            }
         if (a.epilogue == W4A4_EPI_GELU) y = gelu_f32(y);
-        else if (a.epilogue == W4A4_EPI_RESIDUAL) y += load_y<DT>(a.residual[(int64_t)m * a.ldr + col]);
-        a.Y[(int64_t)m * a.ldy + col] = store_y<DT>(y);
+        else if (a.epilogue == W4A4_EPI_RESIDUAL) y += load_y<DT>(a.residual[(m0 + m) * a.ldr + col]);
+        a.Y[(m0 + m) * a.ldy + col] = store_y<DT>(y);
     }
 }
 
-template <int DT, int MT, int Q, int GS, bool VEC>
+template <int DT, int F, int MT, int Q, int GS, int TN>
 static int run_gemv(const W4gArgs &a, hipStream_t s)
 {
-    constexpr int U = DT == W4A4_F32 ? (Q == 1 ? 2 : 1) : Q == 1 ? 4 : MT == 1 ? 2 : 1;
-    constexpr int MAXW = MT == 1 && DT != W4A4_F32 ? 16 : 8;  // at most 96 KB of LDS
-    const int tiles = (a.N + 15) / 16, rows = (a.M + 16 * MT - 1) / (16 * MT);
-    const int stages = (a.K + 127) / 128;
+    constexpr int P = ActOf<DT>::PARTS;
+    constexpr int U = P == 1 && Q == 1 && TN <= 2 ? 2 : 1;
+    constexpr int MAXW = MT * P >= 6 ? 4 : MT == 1 && P == 1 ? 16 : 8;
+    constexpr int C = 16 / F;
+    const int tiles = (a.N + TN * C - 1) / (TN * C), rows = (a.M + 16 * MT - 1) / (16 * MT);
+    const int steps = ((a.K + 127) / 128 + F - 1) / F;
     int waves = 1;
-    while (waves < MAXW && waves * 2 <= stages && (waves < 4 || (int64_t)tiles * rows * waves < 4096)) waves *= 2;
-    const size_t lds = (size_t)waves * 1024 * std::max(4 * ActOf<DT>::PARTS, MT);
-    const auto kernel = k_gemv_w4g<DT, MT, Q, GS, VEC, U, MAXW>;
+    while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * rows * waves < 4096)) waves *= 2;
+    const size_t lds = (size_t)waves * 1024 * std::max(U * MT * P * Q, TN * MT);
+    const auto kernel = k_gemv_w4g<DT, F, MT, Q, GS, U, TN, MAXW>;
     if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, "gemv_w4g")) return rc;
     hipLaunchKernelGGL(kernel, dim3(tiles, rows), dim3(64 * waves), lds, s, a);
     return check_launch("gemv_w4g");
 }
 
-template <int DT, int MT, int Q>
+template <int DT, int F, int MT, int Q, int TN>
 static int pick_group(const W4gArgs &a, hipStream_t s)
 {
-    const size_t eb = sizeof(typename ActOf<DT>::raw);
-    const bool vec = (uintptr_t)a.X % 16 == 0 && (a.ldx * eb) % 16 == 0;
-    if (a.gshift == 0) return vec ? run_gemv<DT, MT, Q, 4, true>(a, s) : run_gemv<DT, MT, Q, 4, false>(a, s);
-    if (a.gshift == 1) return vec ? run_gemv<DT, MT, Q, 2, true>(a, s) : run_gemv<DT, MT, Q, 2, false>(a, s);
-    return vec ? run_gemv<DT, MT, Q, 1, true>(a, s) : run_gemv<DT, MT, Q, 1, false>(a, s);
+    if (a.gshift == 0) return run_gemv<DT, F, MT, Q, 4, TN>(a, s);
+    if (a.gshift == 1) return run_gemv<DT, F, MT, Q, 2, TN>(a, s);
+    return run_gemv<DT, F, MT, Q, 1, TN>(a, s);
 }
 
+template <int DT, int MT, int Q> static int pick_tiles(const W4gArgs &a, hipStream_t s)
+{
+    const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.M + 16 * MT - 1) / (16 * MT));
+    if (MT == 1 && wgs >= W4G_TN4) return pick_group<DT, 1, MT, Q, MT == 1 ? 4 : 1>(a, s);
+    if (MT * ActOf<DT>::PARTS < 4 && wgs >= W4G_TN2) return pick_group<DT, 1, MT, Q, MT * ActOf<DT>::PARTS < 4 ? 2 : 1>(a, s);
+    return pick_group<DT, 1, MT, Q, 1>(a, s);
+}
+
+// F stages per product while that gives the CUs workgroups they lack.
 template <int DT> static int pick_rows(const W4gArgs &a, hipStream_t s)
 {
-    if (a.M <= 4) return pick_group<DT, 1, 1>(a, s);
-    if (a.M <= 16) return pick_group<DT, 1, 4>(a, s);
-    if (a.M <= 32) return pick_group<DT, 2, 4>(a, s);
-    return pick_group<DT, 4, 4>(a, s);
+    const int tiles = (a.N + 15) / 16;
+    if (a.M <= 4 && a.K > 256 && tiles <= W4G_F4_TILES) return pick_group<DT, 4, 1, 4, 1>(a, s);
+    if (a.M <= 8 && a.K > 128 && tiles <= W4G_F2_TILES) return pick_group<DT, 2, 1, 4, 1>(a, s);
+    if (a.M <= 4) return pick_tiles<DT, 1, 1>(a, s);
+    if (a.M <= 16) return pick_tiles<DT, 1, 4>(a, s);
+    // fp32 activations take three operand registers for one
+    if (a.M <= 32 || DT == W4A4_F32) return pick_tiles<DT, 2, 4>(a, s);
+    return pick_tiles<DT, DT == W4A4_F32 ? 2 : 4, 4>(a, s);
 }
 
 int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
