@@ -1066,6 +1066,7 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
     if (epilogue == W4A4_EPI_RESIDUAL && ldr < N)
         return fail(W4A4_ERR_SHAPE, "ldr = %lld < N = %d", (long long)ldr, N);
     if (M > (1 << 21)) return fail(W4A4_ERR_UNSUPPORTED, "M = %d above 2^21", M);
+    if (ldx > (1 << 24)) return fail(W4A4_ERR_UNSUPPORTED, "ldx = %lld above 2^24", (long long)ldx);
     if (M == 0) return ok();
     if (!Y) return fail(W4A4_ERR_ARG, "Y is NULL");
     if (epilogue == W4A4_EPI_RESIDUAL && !residual) return fail(W4A4_ERR_ARG, "residual is NULL");

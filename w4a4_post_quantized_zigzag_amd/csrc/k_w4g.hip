@@ -13,6 +13,7 @@
 //  - The waves of a workgroup share one tile of 16 channels and split K; their partial sums meet in
 //    LDS in a fixed order, so results do not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "w4a4_internal.h"
 
@@ -53,7 +54,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 }
 
 // bf16: v_cvt_off_f32_i4 turns a two's-complement nibble into code / 16, exact in bf16 as well; the
-// factor 16 is folded into the group scale.
+// factor 16 is put back at the end.
 __device__ __forceinline__ u4_t widen_bf16(uint32_t w)
 {
     const uint32_t a = w ^ 0x88888888u, b = a >> 4;
@@ -198,28 +199,44 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     typedef typename ActOf<DT>::raw raw;
     constexpr int P = ActOf<DT>::PARTS, C = 16 / F;
     constexpr int TILE = P * 4 * Q * 16;  // 16-byte slots of a tile in turn
-    // per wave: one step's tiles in turn [U][MT][P][4 Q][16]; afterwards [waves][TN][MT][4][64] floats
+    // per wave: one tile in turn [P][4 Q][16]; afterwards [waves][TN][MT][4][64] floats
     extern __shared__ u4_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int c0 = blockIdx.x * (TN * C), m0 = blockIdx.y * (16 * MT);
     const int stages = (a.K + 127) >> 7, steps = (stages + F - 1) / F, ngroups = a.K >> (5 + a.gshift);
-    u4_t *turn = lds + wave * (U * MT * TILE);
+    u4_t *turn = lds + wave * TILE;
 
-    // as holder of the weight operand: channel c0 + t C + r % C of stage F step + r / C
+    // as holder of the weight operand: channel c0 + t C + r % C of stage F step + r / C. With F = 1 the
+    // addresses are a uniform base and a lane's fixed offset.
     const int wfold = r / C, last_tile = (a.N - 1) >> 4;
-    const uint8_t *wp[TN];
-    const uint16_t *sp[TN];
+    auto weights = [&](int t, int s) {  // a tile past N reads the last one; nothing of it is stored
+        const int col = c0 + t * C;
+        if constexpr (F == 1) {
+            const uint8_t *p = a.wt + ((int64_t)min(col >> 4, last_tile) * stages + s) * 1024;
+            return reinterpret_cast<const u4_t *>(p + lane * 16u);
+        } else {
+            const int row = col % 16 + r % C;
+            return reinterpret_cast<const u4_t *>(
+                a.wt + (((int64_t)min(col >> 4, last_tile) * stages + s) * 64 + g * 16 + row) * 16);
+        }
+    };
+    uint32_t soff[TN];
 #pragma unroll
-    for (int t = 0; t < TN; ++t) {
-        const int col = c0 + t * C + r % C;  // a tile past N reads the last one; nothing of it is stored
-        wp[t] = a.wt + ((int64_t)min(col >> 4, last_tile) * stages * 64 + g * 16 + (col & 15)) * 16;
-        sp[t] = a.w_scale + min(col, a.N - 1);
-    }
-    // as loader: lane (g, r) holds run r of operand rows 4 q + g, row (4 q + g) % C of stage (4 q + g) / C
-    const raw *xp = reinterpret_cast<const raw *>(a.X) + (int64_t)(m0 + g) * a.ldx + 8 * r;
-    const int rows = a.M - m0 - g, kleft = a.K - 8 * r;
+    for (int t = 0; t < TN; ++t) soff[t] = (uint32_t)min(c0 + t * C + r % C, a.N - 1);
+    auto scale = [&](int t, int grp) { return (a.w_scale + (int64_t)grp * a.N)[soff[t]]; };
+    // as loader: lane (g, r) holds run r of operand rows 4 q + g, row (4 q + g) % C of stage (4 q + g) / C.
+    // Rows past M repeat the last one; their results are not stored. 64 rows stay inside 32-bit offsets.
+    uint32_t xoff[MT][Q];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            xoff[m][q] = (uint32_t)min(16 * m + (4 * q) % C + g, a.M - m0 - 1) * (uint32_t)a.ldx;
+    const raw *xbase = reinterpret_cast<const raw *>(a.X) + (int64_t)m0 * a.ldx;
+    // start of the stage that operand row 4 q is from
+    auto stage_k = [&](int step, int q) { return (step * F + 4 * q / C) * 128; };
 
     f4_t acc[TN][MT];
 #pragma unroll
@@ -237,11 +254,9 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    // rows past M and runs past K (whole stages too) are zeros
-                    const int row = F == 1 ? 16 * m + 4 * q : (4 * q) % C, k = (step * F + 4 * q / C) * 128;
-                    d.x[u][m][q] = ActRun<DT>{};
-                    if (row < rows && k < kleft)
-                        d.x[u][m][q] = load_run<DT>(xp + (int64_t)row * a.ldx + k);
+                    const int k0 = stage_k(step, q), k = k0 < a.K ? k0 : 0;
+                    // runs past K read the last one; turn_rows makes them zeros
+                    d.x[u][m][q] = load_run<DT>(xbase + k + (xoff[m][q] + (uint32_t)min(8 * r, a.K - 8 - k)));
                 }
         }
 #pragma unroll
@@ -254,39 +269,36 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 #pragma unroll
                 for (int q = 0; q < GS; ++q) {
                     const int grp = GS == 1 ? (s * 4) >> a.gshift : min(s * GS + q, ngroups - 1);
-                    d.sc[u][t][q] = sp[t][(int64_t)grp * a.N];
+                    d.sc[u][t][q] = scale(t, grp);
                 }
 #pragma unroll
             for (int t = 0; t < TN; ++t)
-                d.w[u][t] = *reinterpret_cast<const u4_t *>(wp[t] + (int64_t)s * 1024);
+                d.w[u][t] = *weights(t, s);
         }
     };
     u4_t x[U][MT][P][4];
-    auto turn_rows = [&](const Step &d) {
+    auto turn_rows = [&](int s0, Step &d, auto last) {  // only a wave's last steps can reach past K
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
+                    if (last.value && stage_k(s0 + u * waves, q) + 8 * r >= a.K) d.x[u][m][q] = ActRun<DT>{};
                     u4_t p[P];
                     act_parts<DT>(d.x[u][m][q], p);
 #pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        turn[(u * MT + m) * TILE + (i * 4 * Q + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
+                    for (int i = 0; i < P; ++i) turn[(i * 4 * Q + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
                 }
-        turn_fence();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
+                turn_fence();
 #pragma unroll
                 for (int i = 0; i < P; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // with one quad of rows the operand's other rows repeat them
-                        x[u][m][i][j] = turn[(u * MT + m) * TILE + (i * 4 * Q + r % (4 * Q)) * 16 +
-                                             ((4 * j + g) ^ (r % (4 * Q)))];
-        turn_fence();
+                        x[u][m][i][j] =
+                            turn[(i * 4 * Q + r % (4 * Q)) * 16 + ((4 * j + g) ^ (r % (4 * Q)))];
+                turn_fence();
+            }
     };
     auto multiply = [&](int s0, const Step &d) {
 #pragma unroll
@@ -305,8 +317,7 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
                         for (int i = P - 1; i >= 0; --i) part[m] = mma<DT>(x[u][m][i][j], b, part[m]);
                     }
                     if ((j + 1) % (4 / GS) == 0) {
-                        const float f = __half2float(__ushort_as_half(d.sc[u][t][j * GS / 4])) *
-                                        (DT == W4A4_F16 ? 1.0f : 16.0f);
+                        const float f = __half2float(__ushort_as_half(d.sc[u][t][j * GS / 4]));
 #pragma unroll
                         for (int m = 0; m < MT; ++m) acc[t][m] += part[m] * f;
                     }
@@ -319,13 +330,13 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     load(wave, cur);  // there are no more waves than steps
     int s0 = wave;
     for (; s0 + waves * U < steps; s0 += waves * U) {
-        turn_rows(cur);
+        turn_rows(s0, cur, std::false_type());
         Step next;
         load(s0 + waves * U, next);
         multiply(s0, cur);
         cur = next;
     }
-    turn_rows(cur);
+    turn_rows(s0, cur, std::true_type());
     multiply(s0, cur);
 
     float *red = reinterpret_cast<float *>(lds);
@@ -351,6 +362,7 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
                 const int row = f * C + m;
                 y += red[(((v * TN + t) * MT + row / 16) * 4 + row % 4) * 64 + (row % 16) / 4 * 16 + f * C + c];
             }
+        if (DT != W4A4_F16) y *= 16.0f;  // the codes were sixteenths
         if (a.epilogue == W4A4_EPI_GELU) y = gelu_f32(y);
         else if (a.epilogue == W4A4_EPI_RESIDUAL) y += load_y<DT>(a.residual[(m0 + m) * a.ldr + col]);
         a.Y[(m0 + m) * a.ldy + col] = store_y<DT>(y);
@@ -368,7 +380,7 @@ static int run_gemv(const W4gArgs &a, hipStream_t s)
     const int steps = ((a.K + 127) / 128 + F - 1) / F;
     int waves = 1;
     while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * rows * waves < 4096)) waves *= 2;
-    const size_t lds = (size_t)waves * 1024 * std::max(U * MT * P * Q, TN * MT);
+    const size_t lds = (size_t)waves * 1024 * std::max(P * Q, TN * MT);
     const auto kernel = k_gemv_w4g<DT, F, MT, Q, GS, U, TN, MAXW>;
     if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, "gemv_w4g")) return rc;
     hipLaunchKernelGGL(kernel, dim3(tiles, rows), dim3(64 * waves), lds, s, a);
