@@ -1264,6 +1264,7 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.splits = plan.splits;
     a.tiles_per_split = plan.tiles_per_split;
+    a.waves = plan.waves;
     if (need) {
         a.stat = reinterpret_cast<float2 *>(ws);
         a.part = reinterpret_cast<float *>(

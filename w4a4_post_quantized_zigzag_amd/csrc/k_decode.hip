@@ -14,6 +14,7 @@ typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 
 // two fp32 values rounded to the 16-bit type, low value first, and back
 template <int DT> __device__ __forceinline__ uint32_t pack16(float a, float b)
@@ -32,28 +33,12 @@ template <int DT> __device__ __forceinline__ f2_t unpack16(uint32_t w)
         return __builtin_convertvector(__builtin_bit_cast(h2_t, w), f2_t);
 }
 
-// Eight consecutive 16-bit elements; rows that are not 16-byte aligned go element by element.
-template <bool VEC> __device__ __forceinline__ u4_t load8(const uint16_t *__restrict__ p)
-{
-    if (VEC) return *reinterpret_cast<const u4_t *>(p);
-    u4_t r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-    return r;
-}
-
-template <bool VEC> __device__ __forceinline__ void store8(uint16_t *p, const u4_t &v)
-{
-    if (VEC) {
-        *reinterpret_cast<u4_t *>(p) = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        p[2 * i] = (uint16_t)v[i];
-        p[2 * i + 1] = (uint16_t)(v[i] >> 16);
-    }
-}
+// Eight consecutive 16-bit elements from and to any element's address: the hardware's vector accesses
+// take them all.
+typedef uint32_t any4_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t any2_t __attribute__((ext_vector_type(2), aligned(2)));
+__device__ __forceinline__ u4_t load8_any(const uint16_t *p) { return *reinterpret_cast<const any4_t *>(p); }
+__device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinterpret_cast<any4_t *>(p) = v; }
 
 // ================================================================================================
 // Norm, rotation, append. Per head x of D channels: y = x / sqrt(mean(x^2) + eps) * w, then the first
@@ -65,7 +50,7 @@ template <bool VEC> __device__ __forceinline__ void store8(uint16_t *p, const u4
 // per token (one lane per frequency, shared through LDS) and kept in registers over its heads. The
 // angle is reduced to a fraction of a turn in fp64, so far positions lose nothing.
 // ================================================================================================
-template <int DT, int LH, bool VEC, bool PAIRS>
+template <int DT, int LH, bool PAIRS>
 __global__ __launch_bounds__(256) void k_norm_rope(const NormRopeArgs a)
 {
     extern __shared__ float2 turns[];  // [tokens of the workgroup][rot / 2] (cos, sin)
@@ -134,7 +119,7 @@ __global__ __launch_bounds__(256) void k_norm_rope(const NormRopeArgs a)
         const bool live = on && h < total;
         u4_t raw = {0, 0, 0, 0};
         if (live)
-            raw = load8<VEC>(is_q   ? a.q + m * a.ldq + (int64_t)h * a.D + d
+            raw = load8_any(is_q   ? a.q + m * a.ldq + (int64_t)h * a.D + d
                              : is_v ? a.v + m * a.ldv + (int64_t)hk * a.D + d
                                     : a.k + m * a.ldk + (int64_t)hk * a.D + d);
         float x[8], sq = 0.0f;
@@ -173,45 +158,40 @@ __global__ __launch_bounds__(256) void k_norm_rope(const NormRopeArgs a)
         for (int i = 0; i < 4; ++i) out[i] = is_v ? raw[i] : pack16<DT>(y[2 * i], y[2 * i + 1]);
         if (!live) continue;
         if (is_q) {
-            store8<VEC>(a.q_out + m * a.ldqo + (int64_t)h * a.D + d, out);
+            store8_any(a.q_out + m * a.ldqo + (int64_t)h * a.D + d, out);
         } else {
-            if (!is_v && a.k_out) store8<VEC>(a.k_out + m * a.ldko + (int64_t)hk * a.D + d, out);
+            if (!is_v && a.k_out) store8_any(a.k_out + m * a.ldko + (int64_t)hk * a.D + d, out);
             if (row >= 0)
-                store8<true>((is_v ? a.v_cache : a.k_cache) + row + (int64_t)hk * a.page_size * a.D + d, out);
+                store8_any((is_v ? a.v_cache : a.k_cache) + row + (int64_t)hk * a.page_size * a.D + d, out);
         }
     }
 }
 
-template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool vec, bool pairs, hipStream_t s)
+template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool pairs, hipStream_t s)
 {
     const int tpw = 4 / a.waves_per_token;
     const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(256);
     const size_t lds = (size_t)tpw * (a.rot / 2) * sizeof(float2);
-    if (vec && pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, true>), grid, block, lds, s, a);
-    else if (vec) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, false>), grid, block, lds, s, a);
-    else if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, false, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false, false>), grid, block, lds, s, a);
+    if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false>), grid, block, lds, s, a);
     return check_launch("qk_norm_rope");
 }
 
-template <int DT> static int pick_head(const NormRopeArgs &a, bool vec, bool pairs, hipStream_t s)
+template <int DT> static int pick_head(const NormRopeArgs &a, bool pairs, hipStream_t s)
 {
-    if (a.D <= 32) return run_norm_rope<DT, 4>(a, vec, pairs, s);
-    if (a.D <= 64) return run_norm_rope<DT, 8>(a, vec, pairs, s);
-    if (a.D <= 128) return run_norm_rope<DT, 16>(a, vec, pairs, s);
-    if (a.D <= 256) return run_norm_rope<DT, 32>(a, vec, pairs, s);
-    return run_norm_rope<DT, 64>(a, vec, pairs, s);
+    if (a.D <= 32) return run_norm_rope<DT, 4>(a, pairs, s);
+    if (a.D <= 64) return run_norm_rope<DT, 8>(a, pairs, s);
+    if (a.D <= 128) return run_norm_rope<DT, 16>(a, pairs, s);
+    if (a.D <= 256) return run_norm_rope<DT, 32>(a, pairs, s);
+    return run_norm_rope<DT, 64>(a, pairs, s);
 }
 
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 {
-    auto rows16 = [](const void *p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0); };
-    const bool vec = rows16(a.q, a.ldq) && rows16(a.k, a.ldk) && rows16(a.v, a.ldv) &&
-                     rows16(a.q_out, a.ldqo) && rows16(a.k_out, a.ldko);
     // few tokens: all four waves on one; many: a wave each, so that its sines serve all heads
     a.waves_per_token = a.M < 1024 ? 4 : 1;
-    return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, vec, interleaved, s)
-                              : pick_head<W4A4_F16>(a, vec, interleaved, s);
+    return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, interleaved, s)
+                              : pick_head<W4A4_F16>(a, interleaved, s);
 }
 
 // ================================================================================================
@@ -276,7 +256,8 @@ template <typename F> __device__ __forceinline__ float across_groups(float x, F 
     return f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
 }
 
-constexpr int ATTN_WAVES = 4;
+constexpr int ATTN_WAVES = 4;   // waves of a workgroup, or one where there is little to do
+constexpr int ATTN_PAD = 4;     // floats between the heads' rows in LDS, against bank conflicts
 
 // N dwords from a 4-byte aligned address
 template <int N> struct __attribute__((aligned(4))) DwordRun {
@@ -290,9 +271,16 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     // p is held times 2^14 in fp16, so that what the two parts drop is 2^-38 of the largest
     constexpr float OFF = DT == W4A4_F16 ? 14.0f : 0.0f;
     extern __shared__ float sm[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int b = blockIdx.z, split = blockIdx.x;
-    const int kvh = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    // Consecutive workgroups go to different XCDs. All heads of one (sequence, split) run on the same XCD,
+    // which then walks each page once, and the sequences move on by one XCD from split to split: the late
+    // splits, which only the longest sequences have, are spread over all of them.
+    const int hts = a.kv_heads * a.head_tiles;
+    const int unit = blockIdx.x / (8 * hts) * 8 + blockIdx.x % 8, head = blockIdx.x / 8 % hts;
+    const int split = unit / a.B, b = (unit + split) % a.B;
+    const int kvh = head / a.head_tiles, ht = head % a.head_tiles;
+    if (split >= a.splits) return;
     const int group = a.heads / a.kv_heads, G = min(16, group - ht * 16), h0 = kvh * group + ht * 16;
     const int n = a.lens[b];
     const AttnTiles tl = attn_tiles(n, a);
@@ -301,75 +289,80 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h0 * D;
     if (tl.T == 0) {  // nothing visible: zeros
         if (split == 0)
-            for (int e = threadIdx.x; e < G * D; e += 64 * ATTN_WAVES) out[e] = 0;
+            for (int e = threadIdx.x; e < G * D; e += blockDim.x) out[e] = 0;
         return;
     }
     if (t0 >= t1) return;
 
     u4_t q[KJ];
     {
-        const uint16_t *qp = a.q + (int64_t)b * a.ldq + (int64_t)(h0 + r) * D + 8 * g;
+        // operand rows past the group repeat its last head; their results are not used
+        const uint16_t *qp = a.q + (int64_t)b * a.ldq + (int64_t)(h0 + min(r, G - 1)) * D + 8 * g;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j)
-            q[j] = r < G ? (a.q_vec ? load8<true>(qp + 32 * j) : load8<false>(qp + 32 * j)) : u4_t{0, 0, 0, 0};
+        for (int j = 0; j < KJ; ++j) q[j] = load8_any(qp + 32 * j);
     }
     f4_t acc[VE];
 #pragma unroll
     for (int i = 0; i < VE; ++i) acc[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float mx = -INFINITY, sum = 0.0f;
     bool bad = tl.over;
-    const int *table = a.table + (int64_t)b * a.ldt;
+    const int32_t *table = a.table + (int64_t)b * a.ldt;
     const int first_in_window = a.window > 0 ? n - a.window : 0;
-    auto seen = [&](int key) {
-        return key < n && (key >= first_in_window || key < a.sinks);
-    };
-    // element offset of a key's row in the caches; a page that does not exist reads page 0 and poisons
-    auto row_of = [&](int key) {
-        int pid = table[key >> a.page_shift];
-        if ((unsigned)pid >= (unsigned)a.num_pages) {
-            bad = true;
-            pid = 0;
-        }
-        return (int64_t)pid * a.page_stride + (int64_t)(kvh * a.page_size + (key & (a.page_size - 1))) * D;
-    };
+    auto seen = [&](int key) { return key < n && (key >= first_in_window || key < a.sinks); };
 
-    for (int t = tl.over ? t1 : t0 + wave; t < t1; t += ATTN_WAVES) {
-        const int key0 = (t < tl.ns ? t : tl.w0 + t - tl.ns) * 32;
+    // A tile's two halves of 16 keys lie in one page each. A half without a visible key may have no page
+    // any more and reads the other half's; a page with one is there as a whole. A page that does not
+    // exist reads page 0 and poisons the result.
+    struct Pages {
+        int key0, at[2];  // first key; first row of each half inside its page
+        int64_t page[2];
+    };
+    auto look_up = [&](int t) {
+        Pages p;
+        p.key0 = (t < tl.ns ? t : tl.w0 + t - tl.ns) * 32;
+        bool any[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int lo = p.key0 + 16 * hf;
+            any[hf] = lo < n && (min(lo + 15, n - 1) >= first_in_window || lo < a.sinks);
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int lo = p.key0 + 16 * (any[hf] ? hf : 1 - hf);
+            int pid = __builtin_amdgcn_readfirstlane(table[lo >> a.page_shift]);
+            if ((unsigned)pid >= (unsigned)a.num_pages) {
+                bad = true;
+                pid = 0;
+            }
+            p.page[hf] = (int64_t)pid * a.page_stride;
+            p.at[hf] = (kvh * a.page_size + (lo & (a.page_size - 1))) * D;
+        }
+        return p;
+    };
+    const uint32_t koff = r * D + 8 * g, voff = 4 * g * D + VE * r;
+
+    int t = tl.over ? t1 : t0 + wave;
+    Pages pg;
+    if (t < t1) pg = look_up(t);
+    for (; t < t1; t += waves) {
+        const int key0 = pg.key0;
         const bool whole = key0 <= n - 32 && (key0 >= first_in_window || key0 + 32 <= a.sinks);
         u4_t k[2][KJ];
         DwordRun<DW> v[8];
-        if (whole) {
-            // 16 keys that start at a multiple of 16 lie in one page: one uniform lookup each
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int64_t at = row_of(key0 + 16 * hf);
-                const uint16_t *kp = a.k_cache + at + r * D + 8 * g;
+        for (int hf = 0; hf < 2; ++hf) {
+            const uint16_t *kp = a.k_cache + pg.page[hf] + pg.at[hf];
 #pragma unroll
-                for (int j = 0; j < KJ; ++j) k[hf][j] = *reinterpret_cast<const u4_t *>(kp + 32 * j);
-                const uint16_t *vp = a.v_cache + at + 4 * g * D + VE * r;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[4 * hf + e] = *reinterpret_cast<const DwordRun<DW> *>(vp + e * D);
-            }
-        } else {
-            // keys that are not visible read the last one, which is
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int key = key0 + 16 * hf + r;
-                const uint16_t *kp = a.k_cache + row_of(seen(key) ? key : n - 1) + 8 * g;
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) k[hf][j] = *reinterpret_cast<const u4_t *>(kp + 32 * j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int vk = key0 + 16 * hf + 4 * g + e;
-                    const bool ok = seen(vk);
-                    v[4 * hf + e] = *reinterpret_cast<const DwordRun<DW> *>(
-                        a.v_cache + row_of(ok ? vk : n - 1) + VE * r);
-#pragma unroll
-                    for (int i = 0; i < DW; ++i) v[4 * hf + e].v[i] = ok ? v[4 * hf + e].v[i] : 0u;
-                }
-            }
+            for (int j = 0; j < KJ; ++j) k[hf][j] = *reinterpret_cast<const u4_t *>(kp + 32 * j + koff);
         }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const uint16_t *vp = a.v_cache + pg.page[hf] + pg.at[hf];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[4 * hf + e] = *reinterpret_cast<const DwordRun<DW> *>(vp + e * D + voff);
+        }
+        if (t + waves < t1) pg = look_up(t + waves);  // the next tile's pages, ahead of its loads
         float p[8];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -377,8 +370,16 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
 #pragma unroll
             for (int j = 0; j < KJ; ++j) s = mma32<DT>(k[hf][j], q[j], s);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                p[4 * hf + e] = (whole || seen(key0 + 16 * hf + 4 * g + e)) ? s[e] * a.scale_log2 : -INFINITY;
+            for (int e = 0; e < 4; ++e) p[4 * hf + e] = s[e] * a.scale_log2;
+        }
+        if (!whole) {  // what is not visible counts as -inf, and its values as zeros
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool ok = seen(key0 + 16 * (e / 4) + 4 * g + e % 4);
+                p[e] = ok ? p[e] : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < DW; ++i) v[e].v[i] = ok ? v[e].v[i] : 0u;
+            }
         }
         float top = p[0];
 #pragma unroll
@@ -418,14 +419,15 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     sum = across_groups(sum, [](float x, float y) { return x + y; });
     if (__any(bad)) sum = NAN;
 
-    // ---- join the waves: sm = max [W][16], sum [W][16], channels [W][G][D] ----
-    float *wm = sm, *ws = sm + ATTN_WAVES * 16, *wa = sm + ATTN_WAVES * 32;
+    // ---- join the waves: sm = maximum [W][16], sum [W][16], channels [W][G][D + pad] ----
+    float *wm = sm, *ws = sm + waves * 16, *wa = sm + waves * 32;
+    constexpr int LD = D + ATTN_PAD;
     if (g == 0) {
         wm[wave * 16 + r] = mx;
         ws[wave * 16 + r] = sum;
     }
     if (r < G) {
-        float *dst = wa + ((size_t)wave * G + r) * D;
+        float *dst = wa + (wave * G + r) * LD;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -433,60 +435,72 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     }
     __syncthreads();
     const bool alone = a.splits == 1 || tl.T <= a.tiles_per_split;
-    for (int e = threadIdx.x; e < G * D; e += 64 * ATTN_WAVES) {
-        const int h = e / D, d = e % D;
+    for (int e = threadIdx.x; e < G * (D / 4); e += blockDim.x) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
         float top = wm[h];
-#pragma unroll
-        for (int w = 1; w < ATTN_WAVES; ++w) top = fmaxf(top, wm[w * 16 + h]);
+        for (int w = 1; w < waves; ++w) top = fmaxf(top, wm[w * 16 + h]);
         const float from = top == -INFINITY ? 0.0f : top;
-        float o = 0.0f, l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < ATTN_WAVES; ++w) {
+        f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+        float l = 0.0f;
+        for (int w = 0; w < waves; ++w) {
             const float f = __builtin_amdgcn_exp2f(wm[w * 16 + h] - from);
-            o += f * wa[((size_t)w * G + h) * D + d];
+            o += f * *reinterpret_cast<const f4_t *>(wa + (w * G + h) * LD + d);
             l += f * ws[w * 16 + h];
         }
         if (alone) {
-            out[e] = (uint16_t)pack16<DT>(o / l, 0.0f);
+            const u2_t y = {pack16<DT>(o[0] / l, o[1] / l), pack16<DT>(o[2] / l, o[3] / l)};
+            *reinterpret_cast<any2_t *>(out + h * D + d) = y;
         } else {
             const int64_t at = ((int64_t)b * a.heads + h0 + h) * a.splits + split;
-            a.part[at * D + d] = o;
+            *reinterpret_cast<f4_t *>(a.part + at * D + d) = o;
             if (d == 0) a.stat[at] = make_float2(top, l);
         }
     }
 }
 
-// out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the splits that had tiles.
+// out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the splits that had tiles: one workgroup
+// per (sequence, head). The weights of all splits are made first, in parallel, so that the channels' sum
+// is nothing but independent loads.
+constexpr int ATTN_MAX_SPLITS = 256;
 template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a)
 {
     constexpr int TC = D / 4, ROWS = 256 / TC;  // threads over the channels, splits at a time
     __shared__ float4 red[ROWS][TC];
-    __shared__ float tot[ROWS];
-    const int b = blockIdx.y, h = blockIdx.x;
+    __shared__ float weight[ATTN_MAX_SPLITS], wave_top[4], wave_sum[4];
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
     const AttnTiles tl = attn_tiles(a.lens[b], a);
     if (tl.T <= a.tiles_per_split) return;  // written by its only workgroup
     const int used = min(a.splits, (tl.T + a.tiles_per_split - 1) / a.tiles_per_split);
     const int64_t at = ((int64_t)b * a.heads + h) * a.splits;
-    float top = -INFINITY;
-    for (int s = 0; s < used; ++s) top = fmaxf(top, a.stat[at + s].x);
-    const float from = top == -INFINITY ? 0.0f : top;
-    const int c = threadIdx.x % TC, row = threadIdx.x / TC;
+    const float2 st = tid < used ? a.stat[at + tid] : make_float2(-INFINITY, 0.0f);
+    float top = st.x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((tid & 63) == 0) wave_top[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    const float f = __builtin_amdgcn_exp2f(st.x - (top == -INFINITY ? 0.0f : top));
+    weight[tid] = f;
+    float l = f * st.y;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    if ((tid & 63) == 0) wave_sum[wave] = l;
+    __syncthreads();
+    l = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+    const int c = tid % TC, row = tid / TC;
     float4 o = make_float4(0, 0, 0, 0);
-    float l = 0.0f;
-    if (row < ROWS)
-        for (int s = row; s < used; s += ROWS) {
-            const float2 st = a.stat[at + s];
-            const float f = __builtin_amdgcn_exp2f(st.x - from);
-            const float4 v = reinterpret_cast<const float4 *>(a.part + (at + s) * D)[c];
-            o.x += f * v.x;
-            o.y += f * v.y;
-            o.z += f * v.z;
-            o.w += f * v.w;
-            l += f * st.y;
-        }
     if (row < ROWS) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.part + at * D) + c;
+#pragma unroll 4
+        for (int s = row; s < used; s += ROWS) {
+            const float4 v = p[(int64_t)s * TC];
+            const float w = weight[s];
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
         red[row][c] = o;
-        if (c == 0) tot[row] = l;
     }
     __syncthreads();
     if (row == 0) {
@@ -496,17 +510,21 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
             o.y += v.y;
             o.z += v.z;
             o.w += v.w;
-            l += tot[s];
         }
-        uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h * D + 4 * c;
-        const uint32_t x = pack16<DT>(o.x / l, o.y / l), y = pack16<DT>(o.z / l, o.w / l);
-        out[0] = (uint16_t)x;
-        out[1] = (uint16_t)(x >> 16);
-        out[2] = (uint16_t)y;
-        out[3] = (uint16_t)(y >> 16);
+        const u2_t y = {pack16<DT>(o.x / l, o.y / l), pack16<DT>(o.z / l, o.w / l)};
+        *reinterpret_cast<any2_t *>(a.out + (int64_t)b * a.ldo + (int64_t)h * D + 4 * c) = y;
     }
 }
 
+// How many workgroups share a sequence. The lengths are on the device; only max_len is known here.
+//  - Where every wave gets a tile of its own and there still are CUs left (up to 1024 tiles in all), one
+//    wave per tile: 1001 tokens with one key/value head take 10.0 us, against 10.4 us in workgroups of 4.
+//  - With a window all sequences are about as long, and two sequences leave little to balance: few long
+//    runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 45.7 us with 1024 workgroups, 48.7
+//    us with 2048; 131071 and 87000 tokens, 8 heads: 163 us with 512, 173 us with 2048).
+//  - Otherwise the lengths differ, and the CUs stay evenly loaded with shorter ones (8 sequences of 1000 to
+//    32000 tokens, 8 heads: 99 us with 512, 89 us with 1024, 76 us with 2048; 32 of 256 to 8191: 113, 103
+//    and 82 us).
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks)
 {
     const int head_tiles = (heads / kv_heads + 15) / 16;
@@ -515,10 +533,14 @@ AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int 
         tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
     tiles = std::max<int64_t>(tiles, 1);
     const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
-    // about 2048 workgroups, each with at least one tile per wave
-    const int64_t want = std::min<int64_t>(std::max<int64_t>(2048 / rows, 1), 256);
     AttnPlan p;
-    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, ATTN_WAVES);
+    p.waves = rows * tiles <= 1024 && tiles <= ATTN_MAX_SPLITS ? 1 : ATTN_WAVES;
+    int64_t want = tiles;
+    if (p.waves > 1) {
+        const int workgroups = window > 0 ? 1024 : B <= 2 ? 512 : 2048;
+        want = std::min<int64_t>(std::max<int64_t>(workgroups / rows, 1), ATTN_MAX_SPLITS);
+    }
+    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, p.waves);
     p.splits = (int)((tiles + p.tiles_per_split - 1) / p.tiles_per_split);
     return p;
 }
@@ -526,12 +548,12 @@ AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int 
 template <int DT, int D> static int run_attn(const AttnArgs &a, hipStream_t s)
 {
     const int G = std::min(16, a.heads / a.kv_heads);
-    const size_t lds = (size_t)(ATTN_WAVES * 32 + ATTN_WAVES * G * D) * sizeof(float);
+    const size_t lds = (size_t)a.waves * (32 + G * (D + ATTN_PAD)) * sizeof(float);
     int rc;
     if ((rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_split<DT, D>), lds, "paged_attn")))
         return rc;
-    hipLaunchKernelGGL((k_attn_split<DT, D>), dim3(a.splits, a.kv_heads * a.head_tiles, a.B),
-                       dim3(64 * ATTN_WAVES), lds, s, a);
+    hipLaunchKernelGGL((k_attn_split<DT, D>), dim3((unsigned)(((int64_t)a.B * a.splits + 7) / 8 * 8 * a.kv_heads * a.head_tiles)),
+                       dim3(64 * a.waves), lds, s, a);
     if ((rc = check_launch("paged_attn_decode")) || a.splits == 1) return rc;
     hipLaunchKernelGGL((k_attn_join<DT, D>), dim3(a.heads, a.B), dim3(256), 0, s, a);
     return check_launch("paged_attn_decode join");
@@ -551,7 +573,6 @@ template <int DT> static int pick_dim(const AttnArgs &a, int D, hipStream_t s)
 int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s)
 {
     a.head_tiles = (a.heads / a.kv_heads + 15) / 16;
-    a.q_vec = (uintptr_t)a.q % 16 == 0 && a.ldq % 8 == 0;
     return dtype == W4A4_BF16 ? pick_dim<W4A4_BF16>(a, D, s) : pick_dim<W4A4_F16>(a, D, s);
 }
 

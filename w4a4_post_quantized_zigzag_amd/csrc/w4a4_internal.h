@@ -253,14 +253,13 @@ struct AttnArgs {
     const int32_t *table, *lens;
     int B, heads, kv_heads, num_pages, page_size, page_shift, table_width, window, sinks;
     float scale_log2;  // scale * log2(e)
-    int splits, tiles_per_split;
+    int splits, tiles_per_split, waves;
     float2 *stat;  // [B][heads][splits] (maximum, sum)
     float *part;   // [B][heads][splits][D]
-    int head_tiles;  // set by the launcher, as is q_vec
-    bool q_vec;
+    int head_tiles;  // set by the launcher
 };
 struct AttnPlan {
-    int splits, tiles_per_split;
+    int splits, tiles_per_split, waves;
 };
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks);
 int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s);
