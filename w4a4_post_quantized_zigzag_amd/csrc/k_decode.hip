@@ -37,6 +37,7 @@ template <int DT> __device__ __forceinline__ f2_t unpack16(uint32_t w)
 // take them all.
 typedef uint32_t any4_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t any2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef float anyf4_t __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ u4_t load8_any(const uint16_t *p) { return *reinterpret_cast<const any4_t *>(p); }
 __device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinterpret_cast<any4_t *>(p) = v; }
 
@@ -46,131 +47,190 @@ __device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinte
 //
 // Bound by the bytes: every element is read once and written once, in one launch for queries, keys
 // and values. A head is LH lanes of eight channels (one 16-byte load each), a wave works on 64 / LH
-// heads at a time and walks its token's heads, so the rotation's sines and cosines are computed once
-// per token (one lane per frequency, shared through LDS) and kept in registers over its heads. The
-// angle is reduced to a fraction of a turn in fp64, so far positions lose nothing.
+// heads at a time and walks its token's heads with HEADS_AHEAD loads in flight. The rotation's sines and
+// cosines are computed once per token (one lane per frequency, shared through LDS) and kept in registers
+// over its heads, multiplied with the norm's weights: y = (x (w cos) -+ x' (w' sin)) / sqrt(..), with the
+// partner channel x' taken from the neighbouring lanes' raw elements. The angle is reduced to a fraction
+// of a turn in fp64, so far positions lose nothing.
 // ================================================================================================
+constexpr int HEADS_AHEAD = 4;
+
+// Sum over LH neighbouring lanes (a power of two), in every lane.
+template <int CTRL> __device__ __forceinline__ float dpp_add(float x)
+{
+    const int y = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true);
+    return x + __builtin_bit_cast(float, y);
+}
+
+template <int LH> __device__ __forceinline__ float sum_lanes(float x)
+{
+    x = dpp_add<0xB1>(x);                       // quad_perm: lane ^ 1
+    x = dpp_add<0x4E>(x);                       // quad_perm: lane ^ 2
+    if (LH >= 8) x = dpp_add<0x141>(x);         // row_half_mirror: the other quad of eight
+    if (LH >= 16) x = dpp_add<0x140>(x);        // row_mirror: the other half of sixteen
+    if (LH >= 32) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, x);
+        const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        x = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+    }
+    if (LH >= 64) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, x);
+        const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        x = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+    }
+    return x;
+}
+
 template <int DT, int LH, bool PAIRS>
-__global__ __launch_bounds__(256) void k_norm_rope(const NormRopeArgs a)
+__global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
 {
     extern __shared__ float2 turns[];  // [tokens of the workgroup][rot / 2] (cos, sin)
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int half = a.rot >> 1;
-    const int wpt = a.waves_per_token, tpw = 4 / wpt;  // waves on one token, tokens per workgroup
-    const int slot_t = wave / wpt;
-    const int64_t m = (int64_t)blockIdx.x * tpw + slot_t;
-    float2 *cs = turns + slot_t * half;
-    if (m < a.M && half > 0) {
-        const double pos = (double)a.positions[m] * 0.15915494309189533577;  // 1 / (2 pi)
-        for (int f = (wave % wpt) * 64 + lane; f < half; f += wpt * 64) {
-            double t = pos * a.inv_freq[f];
-            t -= rint(t);
-            float s, c;
-            sincospif(2.0f * (float)t, &s, &c);
-            cs[f] = make_float2(c, s);
-        }
-    }
-    __syncthreads();
-    if (m >= a.M) return;
-
-    constexpr int HP = 64 / LH;  // heads at a time
+    constexpr int HP = 64 / LH;        // heads at a time
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wpt = a.waves_per_token, tpw = (blockDim.x >> 6) / wpt;  // waves on a token, tokens at a time
+    const int half = a.rot >> 1, slot_t = wave / wpt, sub = wave % wpt;
+    const int64_t m = (int64_t)blockIdx.x * tpw + slot_t, mc = min(m, a.M - 1);
     const int c = lane % LH, d = c * 8;
     const bool on = d < a.D;
-    const bool rotated = d < a.rot, first = PAIRS || d < half;
-    float co[8], si[8];  // per channel (PAIRS: per pair, in the first four)
-    int partner = lane;
-    if (rotated) {
-        if (PAIRS) {
+    const int dl = on ? d : 0;
+
+    // the first heads' loads go out before anything else
+    const int nq = a.heads, nk = a.kv_heads, total = nq + nk + (a.k_cache ? nk : 0);
+    const uint16_t *qs = a.q + mc * a.ldq + dl, *ks = a.k + mc * a.ldk + dl;
+    const uint16_t *vs = a.k_cache ? a.v + mc * a.ldv + dl : ks;
+    const int D = a.D;
+    auto load = [=](int h) {  // past the end: the last head
+        h = min(h, total - 1);
+        const uint16_t *pq = qs + h * D, *pk = ks + (h - nq) * D, *pv = vs + (h - nq - nk) * D;
+        return load8_any(h < nq ? pq : h < nq + nk ? pk : pv);
+    };
+    const int step = wpt * HP;
+    u4_t raw[HEADS_AHEAD];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 t = cs[d / 2 + i];
-                co[i] = t.x;
-                si[i] = t.y;
-            }
-        } else {
-            partner = first ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 t = cs[(first ? d : d - half) + i];
-                co[i] = t.x;
-                si[i] = first ? -t.y : t.y;
-            }
-        }
-    }
-    float wq[8], wk[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        wq[i] = (a.q_weight && on) ? a.q_weight[d + i] : 1.0f;
-        wk[i] = (a.k_weight && on) ? a.k_weight[d + i] : 1.0f;
-    }
+    for (int u = 0; u < HEADS_AHEAD; ++u)
+        if (u == 0 || sub * HP + u * step < total) raw[u] = load(sub * HP + u * step + lane / LH);
     int64_t row = -1;  // cache row offset of this token (elements), -1: not kept
     if (a.k_cache) {
-        const int64_t s = a.slots[m];
+        const int64_t s = a.slots[mc];
         if (s >= 0 && s < (int64_t)a.num_pages * a.page_size)
-            row = (s / a.page_size) * a.page_stride + (s % a.page_size) * a.D;
+            row = (s >> a.page_shift) * a.page_stride + (s & (a.page_size - 1)) * a.D;
     }
-    const int nq = a.heads, nk = a.kv_heads, total = nq + nk + (a.k_cache ? nk : 0);
+    float2 *cs = turns + slot_t * half;
+    if (half > 0) {
+        const double pos = (double)a.positions[mc] * 0.15915494309189533577;  // 1 / (2 pi)
+        for (int f = sub * 64 + lane; f < half; f += wpt * 64) {
+            double t = pos * a.inv_freq[f];
+            t -= rint(t);
+            float s, co;
+            sincospif(2.0f * (float)t, &s, &co);
+            cs[f] = make_float2(co, s);
+        }
+    }
+    // the partner channel: the same pair's other one, in this lane or in another
+    const bool rotated = d < a.rot, first = d < half;
+    const int partner = (PAIRS || !rotated) ? lane : first ? lane + half / 8 : lane - half / 8;
+    const int dp = on ? (partner % LH) * 8 : 0;
+    float cq[8], sq[8], ck[8], sk[8];  // of queries and of keys: w cos, w' sin
+    auto weights = [=](const float *w, float (&own)[8], float (&other)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own[i] = other[i] = 1.0f;
+        if (!w) return;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const anyf4_t x = *reinterpret_cast<const anyf4_t *>(w + dl + i);
+            const anyf4_t y = *reinterpret_cast<const anyf4_t *>(w + dp + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                own[i + e] = x[e];
+                other[i + (PAIRS ? e ^ 1 : e)] = y[e];
+            }
+        }
+    };
+    weights(a.q_weight, cq, sq);
+    weights(a.k_weight, ck, sk);
+    __syncthreads();
+    if (m >= a.M) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int f = PAIRS ? d / 2 + i / 2 : (first ? d : d - half) + i;
+        const float2 t = rotated ? cs[f] : make_float2(1.0f, 0.0f);
+        const float sn = (PAIRS ? i % 2 == 0 : first) ? -t.y : t.y;
+        cq[i] *= t.x;
+        sq[i] *= sn;
+        ck[i] *= t.x;
+        sk[i] *= sn;
+    }
     const float inv_d = 1.0f / (float)a.D;
 
-    for (int h0 = (wave % wpt) * HP; h0 < total; h0 += wpt * HP) {
+    auto finish = [&](int h0, u4_t x) {
         const int h = h0 + lane / LH;
         const bool is_q = h < nq, is_v = h >= nq + nk;
-        const int hk = is_q ? 0 : is_v ? h - nq - nk : h - nq;
-        const bool live = on && h < total;
-        u4_t raw = {0, 0, 0, 0};
-        if (live)
-            raw = load8_any(is_q   ? a.q + m * a.ldq + (int64_t)h * a.D + d
-                             : is_v ? a.v + m * a.ldv + (int64_t)hk * a.D + d
-                                    : a.k + m * a.ldk + (int64_t)hk * a.D + d);
-        float x[8], sq = 0.0f;
+        u4_t out = x;
+        if (h0 < nq + nk) {  // some of these heads are not values
+            if (a.D != LH * 8) x = on ? x : u4_t{0, 0, 0, 0};
+            float v[8], o[8], ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f2_t f = unpack16<DT>(raw[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-            sq = fmaf(f.x, f.x, sq);
-            sq = fmaf(f.y, f.y, sq);
-        }
+            for (int i = 0; i < 4; ++i) {
+                const f2_t f = unpack16<DT>(x[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+                ss = fmaf(f.x, f.x, ss);
+                ss = fmaf(f.y, f.y, ss);
+            }
+            if (PAIRS) {
 #pragma unroll
-        for (int off = 1; off < LH; off <<= 1) sq += __shfl_xor(sq, off, 64);
-        const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
-        if (PAIRS) {
-            if (rotated) {
+                for (int i = 0; i < 8; ++i) o[i] = v[i ^ 1];
+            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = y[2 * i], q = y[2 * i + 1];
-                    y[2 * i] = p * co[i] - q * si[i];
-                    y[2 * i + 1] = q * co[i] + p * si[i];
+                    const f2_t f = unpack16<DT>((uint32_t)__builtin_amdgcn_ds_bpermute(partner * 4, (int)x[i]));
+                    o[2 * i] = f.x;
+                    o[2 * i + 1] = f.y;
                 }
             }
-        } else if (half > 0) {
+            const float inv = rsqrtf(fmaf(sum_lanes<LH>(ss), inv_d, a.eps));
+            float y[8];
+            if (h0 + HP <= nq) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl(y[i], partner, 64);
-                if (rotated) y[i] = y[i] * co[i] + o * si[i];
+                for (int i = 0; i < 8; ++i) y[i] = fmaf(o[i], sq[i], v[i] * cq[i]) * inv;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s1 = sq[i], s2 = sk[i], c1 = cq[i], c2 = ck[i];
+                    y[i] = fmaf(o[i], is_q ? s1 : s2, v[i] * (is_q ? c1 : c2)) * inv;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = is_v ? out[i] : pack16<DT>(y[2 * i], y[2 * i + 1]);
+        }
+        if (!on || h >= total) return;
+        if (is_q) {
+            store8_any(a.q_out + m * a.ldqo + h * a.D + d, out);
+        } else {
+            const int hk = is_v ? h - nq - nk : h - nq;
+            if (!is_v && a.k_out) store8_any(a.k_out + m * a.ldko + hk * a.D + d, out);
+            if (row >= 0) {
+                uint16_t *kc = a.k_cache, *vc = a.v_cache;
+                store8_any((is_v ? vc : kc) + row + hk * a.page_size * a.D + d, out);
             }
         }
-        u4_t out;
+    };
+    for (int h0 = sub * HP; h0 < total; h0 += HEADS_AHEAD * step) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = is_v ? raw[i] : pack16<DT>(y[2 * i], y[2 * i + 1]);
-        if (!live) continue;
-        if (is_q) {
-            store8_any(a.q_out + m * a.ldqo + (int64_t)h * a.D + d, out);
-        } else {
-            if (!is_v && a.k_out) store8_any(a.k_out + m * a.ldko + (int64_t)hk * a.D + d, out);
-            if (row >= 0)
-                store8_any((is_v ? a.v_cache : a.k_cache) + row + (int64_t)hk * a.page_size * a.D + d, out);
+        for (int u = 0; u < HEADS_AHEAD; ++u) {
+            const int h = h0 + u * step;
+            if (h >= total) return;
+            const u4_t x = raw[u];
+            if (h + HEADS_AHEAD * step < total) raw[u] = load(h + HEADS_AHEAD * step + lane / LH);
+            finish(h, x);
         }
     }
 }
 
 template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool pairs, hipStream_t s)
 {
-    const int tpw = 4 / a.waves_per_token;
-    const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(256);
+    const int waves = std::max(4, a.waves_per_token), tpw = waves / a.waves_per_token;
+    const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(64 * waves);
     const size_t lds = (size_t)tpw * (a.rot / 2) * sizeof(float2);
     if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true>), grid, block, lds, s, a);
     else hipLaunchKernelGGL((k_norm_rope<DT, LH, false>), grid, block, lds, s, a);
@@ -188,8 +248,9 @@ template <int DT> static int pick_head(const NormRopeArgs &a, bool pairs, hipStr
 
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 {
-    // few tokens: all four waves on one; many: a wave each, so that its sines serve all heads
-    a.waves_per_token = a.M < 1024 ? 4 : 1;
+    // few tokens: several waves on one; many: a wave each, so that its sines serve all heads
+    a.page_shift = a.page_size ? __builtin_ctz((unsigned)a.page_size) : 0;
+    a.waves_per_token = a.M < 256 ? 8 : a.M < 2048 ? 4 : 1;
     return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, interleaved, s)
                               : pick_head<W4A4_F16>(a, interleaved, s);
 }

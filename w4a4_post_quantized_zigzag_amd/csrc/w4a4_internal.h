@@ -242,7 +242,7 @@ struct NormRopeArgs {
     int num_pages, page_size;
     int64_t page_stride;
     const int64_t *slots;  // [M]
-    int waves_per_token;   // set by the launcher
+    int waves_per_token, page_shift;  // set by the launcher
 };
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s);
 
