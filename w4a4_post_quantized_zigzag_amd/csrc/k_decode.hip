@@ -248,9 +248,12 @@ template <int DT> static int pick_head(const NormRopeArgs &a, bool pairs, hipStr
 
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 {
-    // few tokens: several waves on one; many: a wave each, so that its sines serve all heads
+    // Few tokens: up to eight waves on one. Many: a wave each, so that its sines serve all heads. About 3000
+    // waves are enough to load the memory (32 + 8 heads of 128: 256 tokens 8.7 us with one wave each, 4.8
+    // with eight; 1024 tokens 10.7, 9.2, 9.4, 10.8 us with 1, 2, 4, 8; 4096 tokens 18.9 and 30.8).
+    a.waves_per_token = 8;
+    while (a.waves_per_token > 1 && a.M * a.waves_per_token > 3200) a.waves_per_token /= 2;
     a.page_shift = a.page_size ? __builtin_ctz((unsigned)a.page_size) : 0;
-    a.waves_per_token = a.M < 256 ? 8 : a.M < 2048 ? 4 : 1;
     return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, interleaved, s)
                               : pick_head<W4A4_F16>(a, interleaved, s);
 }

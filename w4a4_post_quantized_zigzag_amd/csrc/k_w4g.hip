@@ -130,12 +130,6 @@ template <int DT> __device__ __forceinline__ f4_t mma(const u4_t &a, const u4_t 
                                                        __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
 }
 
-#ifndef W4G_F4_TILES
-#define W4G_F4_TILES 64
-#define W4G_F2_TILES 128
-#define W4G_TN4 1024
-#define W4G_TN2 512
-#endif
 struct W4gArgs {
     const void *X;
     int64_t ldx;
@@ -398,8 +392,8 @@ static int pick_group(const W4gArgs &a, hipStream_t s)
 template <int DT, int MT, int Q> static int pick_tiles(const W4gArgs &a, hipStream_t s)
 {
     const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.M + 16 * MT - 1) / (16 * MT));
-    if (MT == 1 && wgs >= W4G_TN4) return pick_group<DT, 1, MT, Q, MT == 1 ? 4 : 1>(a, s);
-    if (MT * ActOf<DT>::PARTS < 4 && wgs >= W4G_TN2) return pick_group<DT, 1, MT, Q, MT * ActOf<DT>::PARTS < 4 ? 2 : 1>(a, s);
+    if (MT == 1 && wgs >= 1024) return pick_group<DT, 1, MT, Q, MT == 1 ? 4 : 1>(a, s);
+    if (MT * ActOf<DT>::PARTS < 4 && wgs >= 512) return pick_group<DT, 1, MT, Q, MT * ActOf<DT>::PARTS < 4 ? 2 : 1>(a, s);
     return pick_group<DT, 1, MT, Q, 1>(a, s);
 }
 
@@ -407,8 +401,8 @@ template <int DT, int MT, int Q> static int pick_tiles(const W4gArgs &a, hipStre
 template <int DT> static int pick_rows(const W4gArgs &a, hipStream_t s)
 {
     const int tiles = (a.N + 15) / 16;
-    if (a.M <= 4 && a.K > 256 && tiles <= W4G_F4_TILES) return pick_group<DT, 4, 1, 4, 1>(a, s);
-    if (a.M <= 8 && a.K > 128 && tiles <= W4G_F2_TILES) return pick_group<DT, 2, 1, 4, 1>(a, s);
+    if (a.M <= 4 && a.K > 256 && tiles <= 64) return pick_group<DT, 4, 1, 4, 1>(a, s);
+    if (a.M <= 8 && a.K > 128 && tiles <= 128) return pick_group<DT, 2, 1, 4, 1>(a, s);
     if (a.M <= 4) return pick_tiles<DT, 1, 1>(a, s);
     if (a.M <= 16) return pick_tiles<DT, 1, 4>(a, s);
     // fp32 activations take three operand registers for one

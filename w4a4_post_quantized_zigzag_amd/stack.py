@@ -2,7 +2,10 @@
 replaced by identity) -> O with residual -> up with erf-GELU -> down with residual, every linear a
 W4A4 linear (or, for the linears named in w8, a W8A8 linear: the FoldQuantVLA summary's mixed
 configuration keeps the attention-output and FFN-down projections at W8A8) with its own zigzag
-permutation, block SVD factor, packed weights and per-step act_scale_table. This module only
+permutation, block SVD factor, packed weights and per-step act_scale_table. For the language
+backbone's single tokens the same stack can keep its activations in 16 bits (the linears named in
+w4g: group-scaled 4-bit weights) and put attention where the identity was (attention=, with a
+PagedCache): per-head norm and rotation, append, attention over the cache. This module only
 sequences library calls and owns buffers; all arithmetic runs in libw4a4.so.
 
 Per-step tables follow the pages' per-step scaling (vnrobo "Y tuong paper": the runtime looks up the
@@ -11,6 +14,8 @@ step, the stack is run in per-token mode over that step's stacked calibration dr
 linear's table entry is the scale of its rotated input on the way.
 """
 from __future__ import annotations
+
+from dataclasses import dataclass
 
 import numpy as np
 
@@ -60,6 +65,99 @@ class DeviceLinear:
         return self
 
 
+class GroupLinear:
+    """One linear with group-scaled 4-bit weights and unquantized activations (gemv_w4g)."""
+    bits, row_perm, gperm = None, None, None
+
+    def __init__(self, W, group: int):
+        torch = _torch()
+        W = W if isinstance(W, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(W)).cuda()
+        self.N, self.K = W.shape
+        self.wt, self.w_scale = bd.pack_weights_w4g(W, group)
+
+    def pack(self, row_perm=None):
+        return self
+
+
+@dataclass(frozen=True)
+class Attention:
+    """Attention between QKV and O: qkv holds heads query, kv_heads key and kv_heads value rows of
+    head_dim channels. rot_dim channels of each query and key are rotated (theta ** (-2 i / rot_dim) per
+    position). window > 0: only the last `window` and the first `sinks` tokens are visible."""
+    heads: int
+    kv_heads: int
+    head_dim: int
+    rot_dim: int | None = None
+    theta: float = 10000.0
+    eps: float = 1e-6
+    interleaved: bool = False
+    window: int = 0
+    sinks: int = 0
+
+    def inv_freq(self):
+        torch = _torch()
+        rot = self.head_dim if self.rot_dim is None else self.rot_dim
+        if rot == 0:
+            return None
+        i = torch.arange(0, rot, 2, device="cuda", dtype=torch.float64)
+        return self.theta ** (-i / rot)
+
+
+class PagedCache:
+    """Keys and values of `batch` sequences in pages shared by all of them, one pair of arrays per
+    layer. advance() makes room for one new token per sequence and sets the device tensors that run()
+    reads (table, lens, slots, positions) in place, so a captured run() can be replayed after it. Page
+    bookkeeping is on the host."""
+
+    def __init__(self, layers: int, attention: Attention, batch: int, pages: int, page_size: int = 16,
+                 max_len: int | None = None):
+        torch = _torch()
+        self.page_size, self.batch = page_size, batch
+        self.max_len = pages * page_size if max_len is None else max_len
+        shape = (pages, attention.kv_heads, page_size, attention.head_dim)
+        e = lambda: torch.zeros(shape, dtype=torch.float16, device="cuda")  # noqa: E731
+        self.k, self.v = [e() for _ in range(layers)], [e() for _ in range(layers)]
+        width = -(-self.max_len // page_size)
+        self._table = torch.full((batch, width), -1, dtype=torch.int32)
+        self._len = [0] * batch
+        self._free = list(range(pages))[::-1]
+        self.table = self._table.cuda()
+        self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.slots = torch.full((batch,), -1, dtype=torch.int64, device="cuda")
+        self.positions = torch.zeros(batch, dtype=torch.int64, device="cuda")
+
+    def advance(self, active=None):
+        """Room for one more token of every sequence (of those whose entry in `active` is true): a
+        sequence that does not take part keeps its length, and its row is not appended."""
+        torch = _torch()
+        on = [b for b in range(self.batch) if active is None or active[b]]
+        for b in on:
+            if self._len[b] >= self.max_len:
+                raise RuntimeError(f"sequence {b} is at max_len {self.max_len}")
+        if sum(self._len[b] % self.page_size == 0 for b in on) > len(self._free):
+            raise RuntimeError("no free pages")
+        slots = [-1] * self.batch
+        for b in on:
+            n = self._len[b]
+            if n % self.page_size == 0:
+                self._table[b, n // self.page_size] = self._free.pop()
+            slots[b] = int(self._table[b, n // self.page_size]) * self.page_size + n % self.page_size
+            self._len[b] = n + 1
+        self.slots.copy_(torch.tensor(slots, dtype=torch.int64))
+        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+        self.positions.copy_(torch.tensor([max(n - 1, 0) for n in self._len], dtype=torch.int64))
+        self.table.copy_(self._table)
+
+    def release(self, b: int):
+        """Give sequence b's pages back and start it over."""
+        used = -(-self._len[b] // self.page_size)
+        self._free += self._table[b, :used].tolist()
+        self._table[b] = -1
+        self._len[b] = 0
+        self.lens[b] = 0
+        self.table.copy_(self._table)
+
+
 def _gather_order(cols):
     """w4a4_gemm_rq_next's res_order for the residual map cols (int32 [N], N % 128 == 0): each
     128-column tile's columns sorted by the residual column they read (ties by column)."""
@@ -91,6 +189,40 @@ def _inverse(p):
     inv = torch.empty_like(p)
     inv[p] = torch.arange(p.numel(), device=p.device, dtype=p.dtype)
     return inv
+
+
+class _PlainBuffers:
+    """Buffers of a stack with group-scaled linears or attention: nothing is folded or fused there."""
+
+    def __init__(self, rows: int, layer: dict, block: int, attention: Attention | None):
+        torch = _torch()
+        e = lambda shape, dt=torch.float16: torch.empty(shape, dtype=dt, device="cuda")  # noqa: E731
+        L = bd.lib()
+        h, f = layer["o"].N, layer["up"].N
+        self.qkv, self.h2, self.g = e((rows, layer["qkv"].N)), e((rows, h)), e((rows, f))
+        self.hs = [e((rows, h)), e((rows, h))]
+        self.xs = e(max(rows, 1), torch.float32)
+        self.xq, self.ws, self.cws, self.gws = {}, {}, {}, {}
+        for lin in layer.values():
+            if isinstance(lin, GroupLinear):
+                continue
+            K, b = lin.K, lin.bits
+            self.xq[(K, b)] = e((rows, K // 2 if b == 4 else K), torch.uint8)
+            self.ws[K] = e(max(256, L.w4a4_act_workspace_bytes(rows, K, block, 1)), torch.uint8)
+            self.cws[K] = e(max(256, L.w4a4_calibrate_workspace_bytes(rows, K, block)), torch.uint8)
+            wsb = L.w4a4_gemm_workspace_bytes if b == 4 else L.w4a4_gemm_w8a8_workspace_bytes
+            self.gws[(lin.N, K, b)] = e(max(256, wsb(rows, lin.N, K)), torch.uint8)
+        if attention is not None:
+            A = attention
+            self.q, self.att = e((rows, A.heads, A.head_dim)), e((rows, A.heads, A.head_dim))
+            self.aws = {}  # attention workspaces by max_len
+
+    def attn_ws(self, A: Attention, rows: int, max_len: int):
+        if max_len not in self.aws:
+            n = bd.lib().w4a4_paged_attn_workspace_bytes(rows, A.heads, A.kv_heads, A.head_dim, max_len,
+                                                         A.window, A.sinks)
+            self.aws[max_len] = _torch().empty(max(256, n), dtype=_torch().uint8, device="cuda")
+        return self.aws[max_len]
 
 
 class _Buffers:
@@ -136,13 +268,25 @@ class DeviceStack:
         order and down's rows in the next layer's QKV order (the last layer's in natural order).
         The residual that O and down add is then read through a column map (w4a4_gemm_rq_next's
         res_cols). Outside calibration every rotate-quantize but layer 0's QKV input then runs in
-        the epilogue of the GEMM that produces the activation."""
+        the epilogue of the GEMM that produces the activation.
+    w4g: names of the linears that run with group-scaled 4-bit weights (`group` consecutive k per
+    scale) on unquantized activations. attention: an Attention instead of the identity; qkv is then
+    [(heads + 2 kv_heads) head_dim, h], o [h, heads head_dim], a layer's dict may hold q_norm and k_norm
+    (fp32 [head_dim]), and run() takes a PagedCache whose batch is the rows. With either, nothing is
+    folded."""
 
-    def __init__(self, weights, block: int, steps: int, calib=None, w8=(), fold_perms: bool = True):
+    def __init__(self, weights, block: int, steps: int, calib=None, w8=(), fold_perms: bool = True, w4g=(),
+                 group: int = 128, attention: Attention | None = None):
         torch = _torch()
         self.block, self.steps = block, steps
         self.h = weights[0]["o"].shape[0]
         self.f = weights[0]["up"].shape[0]
+        self.attention = attention
+        self.plain = attention is not None or bool(w4g)
+        self._bufs = {}
+        if self.plain:
+            self._init_plain(weights, steps, calib, w8, w4g, group)
+            return
         self.fold = fold_perms
         self.stream = fold_perms and not w8
         h = self.h
@@ -192,11 +336,34 @@ class DeviceStack:
                 lin[li][n].pack(rp[n])
             self.res_map.append(maps)
         self.layers = lin
-        self._bufs = {}
 
-    def bufs(self, rows: int) -> _Buffers:
+    def _init_plain(self, weights, steps, calib, w8, w4g, group):
+        torch = _torch()
+        unknown = [n for n in (*w8, *w4g) if n not in LINEARS]
+        if unknown or set(w8) & set(w4g):
+            raise ValueError(f"w8 {tuple(w8)} and w4g {tuple(w4g)} must name different linears of {LINEARS}")
+        self.fold = self.stream = False
+        A = self.attention
+        if A is not None:
+            want = ((A.heads + 2 * A.kv_heads) * A.head_dim, A.heads * A.head_dim)
+            for lw in weights:
+                if (lw["qkv"].shape[0], lw["o"].shape[1]) != want:
+                    raise ValueError(f"qkv rows and o columns must be {want} for {A}")
+            self.inv_freq = A.inv_freq()
+            norm = lambda lw, n: (torch.as_tensor(np.asarray(lw[n], np.float32)).cuda()  # noqa: E731
+                                  if lw.get(n) is not None else None)
+            self.norms = [(norm(lw, "q_norm"), norm(lw, "k_norm")) for lw in weights]
+        self.layers = []
+        for li, lw in enumerate(weights):
+            pu = lambda n: calib[li][n] if calib is not None else (None, None)  # noqa: E731
+            self.layers.append({n: (GroupLinear(lw[n], group) if n in w4g else
+                                    DeviceLinear(lw[n], self.block, steps, *pu(n), bits=8 if n in w8 else 4)
+                                    ).pack() for n in LINEARS})
+
+    def bufs(self, rows: int):
         if rows not in self._bufs:
-            self._bufs[rows] = _Buffers(rows, self.h, self.f, self.block)
+            self._bufs[rows] = (_PlainBuffers(rows, self.layers[0], self.block, self.attention) if self.plain
+                                else _Buffers(rows, self.h, self.f, self.block))
         return self._bufs[rows]
 
     def set_tables(self, tables):
@@ -204,6 +371,8 @@ class DeviceStack:
         torch = _torch()
         for layer, tl in zip(self.layers, tables):
             for name in LINEARS:
+                if isinstance(layer[name], GroupLinear):
+                    continue
                 layer[name].table.copy_(torch.from_numpy(np.asarray(tl[name], np.float32)))
 
     def layer_plan(self, li: int, cur, out, calib: bool, bufs: _Buffers, keep: bool = False):
@@ -218,6 +387,17 @@ class DeviceStack:
         cq = lambda lin: (bufs.xq[(lin.K, lin.bits)], bufs.xs)  # noqa: E731
         plan = [dict(name=n, lin=L[n]) for n in LINEARS]
         P = {d["name"]: d for d in plan}
+        if self.plain:
+            A = self.attention
+            v = bufs.qkv[:, 2 * h:3 * h] if A is None else bufs.att.view(-1, A.heads * A.head_dim)
+            for name, X, Y, epi, res in (("qkv", cur, bufs.qkv, bd.EPI_NONE, None),
+                                         ("o", v, bufs.h2, bd.EPI_RESIDUAL, cur),
+                                         ("up", bufs.h2, bufs.g, bd.EPI_GELU, None),
+                                         ("down", bufs.g, out, bd.EPI_RESIDUAL, bufs.h2)):
+                lin = L[name]
+                P[name].update(X=X, perm=lin.gperm, Y=Y, epi=epi, res=res,
+                               cin=None if isinstance(lin, GroupLinear) else cq(lin))
+            return plan
         if self.stream:
             maps = self.res_map[li]
             last = li + 1 == len(self.layers)
@@ -258,7 +438,7 @@ class DeviceStack:
     def rotate_quant_call(self, e, step: int, calib: bool, bufs: _Buffers):
         """The linear's own rotate-quantize (none when e["X"] is None)."""
         lin, X = e["lin"], e.get("X")
-        if X is None:
+        if X is None or isinstance(lin, GroupLinear):
             return
         xq, xs = e["cin"]
         if calib:
@@ -270,6 +450,9 @@ class DeviceStack:
     def gemm_call(self, e, step: int, calib: bool, bufs: _Buffers):
         """The linear's GEMM with its epilogue (and, with e["nxt"], the next linear's codes)."""
         lin, nxt, rmap = e["lin"], e.get("nxt"), e.get("res_map")
+        if isinstance(lin, GroupLinear):
+            bd.gemv_w4g(e["X"], lin.wt, lin.w_scale, Y=e["Y"], epilogue=e["epi"], residual=e["res"])
+            return
         xq, xs = e["cin"]
         if nxt is not None or rmap is not None:
             kn = nxt.K if nxt is not None else 0
@@ -285,14 +468,33 @@ class DeviceStack:
         bd.gemm(xq, xs, calib, lin.wq, lin.w_scale, lin.K, Y=e["Y"], epilogue=e["epi"],
                 residual=e.get("res"), ws=bufs.gws[(lin.N, lin.K, lin.bits)], bits=lin.bits)
 
-    def run(self, X, step: int, calib: bool = False, outputs=None, codes=None, rows=None):
+    def attention_call(self, li: int, cache: PagedCache, bufs: _PlainBuffers):
+        """Norm, rotation and append of the layer's queries, keys and values, then attention over the
+        cache (the new token included) into bufs.att."""
+        A, n = self.attention, bufs.qkv.shape[0]
+        qkv = bufs.qkv.view(n, A.heads + 2 * A.kv_heads, A.head_dim)
+        q, k, v = qkv.split((A.heads, A.kv_heads, A.kv_heads), dim=1)
+        bd.qk_norm_rope_append(q, k, v, *self.norms[li], self.inv_freq, cache.positions, cache.k[li],
+                               cache.v[li], cache.slots, eps=A.eps, interleaved=A.interleaved, q_out=bufs.q)
+        bd.paged_attn_decode(bufs.q, cache.k[li], cache.v[li], cache.table, cache.lens, window=A.window,
+                             sinks=A.sinks, max_len=cache.max_len, out=bufs.att,
+                             ws=bufs.attn_ws(A, n, cache.max_len))
+
+    def run(self, X, step: int, calib: bool = False, outputs=None, codes=None, rows=None, cache=None):
         """One pass of the stack for denoising step `step` on X fp16 [rows, h] (device); returns the
         last layer's output in natural channel order. In calib mode the linears quantize per token
         and record their table entry for `step`. Test hooks: if `outputs` is a list, each linear's
         output (columns in natural channel order) and its input are appended as (output, input,
         residual or None); if `codes` is a list, each linear's activation codes and scale are
         appended as (codes, x_scale). `rows` (device int64 index) keeps only those token rows in
-        what the hooks record."""
+        what the hooks record. cache: the PagedCache of a stack with attention, advanced for this pass;
+        row b is sequence b's new token."""
+        if (cache is not None) != (self.attention is not None):
+            raise ValueError("a cache goes with attention, and attention needs one")
+        if cache is not None and cache.batch != X.shape[0]:
+            raise ValueError(f"{X.shape[0]} rows for a cache of {cache.batch} sequences")
+        if codes is not None and self.plain:
+            raise ValueError("codes are recorded by fully quantized stacks only")
         bufs = self.bufs(X.shape[0])
         h = self.h
         cur = X
@@ -302,6 +504,8 @@ class DeviceStack:
         for li in range(len(self.layers)):
             out = bufs.hs[li % 2]
             for e in self.layer_plan(li, cur, out, calib, bufs, keep):
+                if cache is not None and e["name"] == "o":
+                    self.attention_call(li, cache, bufs)
                 self.rotate_quant_call(e, step, calib, bufs)
                 if codes is not None:
                     xq, xs = e["cin"]
@@ -313,8 +517,9 @@ class DeviceStack:
                 h2 = pick(self._natural(L["o"], bufs.h2))
                 g = pick(self._natural(L["up"], bufs.g))
                 y = pick(self._natural(L["down"], out))
-                outputs.extend([(qkv, x_nat, None), (h2, qkv[:, 2 * h:3 * h], x_nat), (g, h2, None),
-                                (y, g, h2)])
+                o_in = (qkv[:, 2 * h:3 * h] if self.attention is None
+                        else pick(bufs.att.flatten(1)))
+                outputs.extend([(qkv, x_nat, None), (h2, o_in, x_nat), (g, h2, None), (y, g, h2)])
                 x_nat = y
             cur = out
         return cur
@@ -330,6 +535,8 @@ class DeviceStack:
 
     def calibrate(self, X_calib_per_step):
         """X_calib_per_step[t]: list of fp16 numpy arrays [rows, h] (calibration draws of step t)."""
+        if self.attention is not None:
+            raise ValueError("tables of a stack with attention are set with set_tables")
         torch = _torch()
         for t, draws in enumerate(X_calib_per_step):
             X = torch.from_numpy(np.ascontiguousarray(np.concatenate(draws, axis=0))).cuda()
