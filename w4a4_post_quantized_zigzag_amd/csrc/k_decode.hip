@@ -614,7 +614,8 @@ template <int DT, int D> static int run_attn(const AttnArgs &a, hipStream_t s)
     const int G = std::min(16, a.heads / a.kv_heads);
     const size_t lds = (size_t)a.waves * (32 + G * (D + ATTN_PAD)) * sizeof(float);
     int rc;
-    if ((rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_split<DT, D>), lds, "paged_attn")))
+    if (lds > 65536 &&  // more than every kernel gets unasked
+        (rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_split<DT, D>), lds, "paged_attn")))
         return rc;
     hipLaunchKernelGGL((k_attn_split<DT, D>), dim3((unsigned)(((int64_t)a.B * a.splits + 7) / 8 * 8 * a.kv_heads * a.head_tiles)),
                        dim3(64 * a.waves), lds, s, a);

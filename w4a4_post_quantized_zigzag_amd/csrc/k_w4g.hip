@@ -99,23 +99,23 @@ template <int DT> __device__ __forceinline__ void act_parts(const ActRun<DT> &x,
     if constexpr (DT != W4A4_F32) {
         p[0] = x.v[0];
     } else {
+        auto cut = [](float f) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, f) & 0xFFFF0000u); };
+        auto high = [](float a, float b) {  // the upper halves of two floats, the first one's low
+            return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+        };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t h[2][3];
+            float f[2], r[2], t[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t bits = x.v[i / 2][2 * (i % 2) + e];
-                const float f = __builtin_bit_cast(float, bits);
-                const bool fin = (bits & 0x7F800000u) != 0x7F800000u;
-                const bool nan = !fin && (bits & 0x007FFFFFu) != 0;
-                // an infinity or NaN stays whole in the first part
-                h[e][0] = (bits & 0xFFFF0000u) | (nan ? 0x00400000u : 0u);
-                const float r1 = fin ? f - __builtin_bit_cast(float, h[e][0]) : 0.0f;
-                h[e][1] = __builtin_bit_cast(uint32_t, r1) & 0xFFFF0000u;
-                h[e][2] = __builtin_bit_cast(uint32_t, r1 - __builtin_bit_cast(float, h[e][1]));
+                f[e] = __builtin_bit_cast(float, (uint32_t)x.v[i / 2][2 * (i % 2) + e]);
+                // an infinity is whole in the first part; a NaN stays one in the second
+                r[e] = fabsf(f[e]) == INFINITY ? 0.0f : f[e] - cut(f[e]);
+                t[e] = r[e] - cut(r[e]);
             }
-#pragma unroll
-            for (int q = 0; q < 3; ++q) p[q][i] = (h[0][q] >> 16) | (h[1][q] & 0xFFFF0000u);
+            p[0][i] = high(f[0], f[1]);
+            p[1][i] = high(r[0], r[1]);
+            p[2][i] = high(t[0], t[1]);
         }
     }
 }
@@ -141,6 +141,7 @@ struct W4gArgs {
     int epilogue;
     const uint16_t *residual;
     int64_t ldr;
+    int row_blocks;  // set per launch
 };
 
 __device__ __forceinline__ float gelu_f32(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
@@ -165,12 +166,14 @@ __device__ __forceinline__ void turn_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// One workgroup: TN tiles of C = 16 / F output channels (blockIdx.x) for 16 MT rows (blockIdx.y), its
-// waves splitting K. A wave turns the activations of U steps into matrix operands once and keeps them in
-// registers over its TN tiles. All loads of the next steps are in flight while it works on these. GS groups
-// per 128-k stage (1 for group >= 128).
+// One workgroup: TN tiles of C = 16 / F output channels for 16 rows, its waves splitting K. A wave turns
+// the activations of U steps into matrix operands once and keeps them in registers over its TN tiles. All
+// loads of the next steps are in flight while it works on these. GS groups per 128-k stage (1 for group >=
+// 128). More than 16 rows are blocks of 16 in workgroups of their own: two or four blocks in one workgroup
+// read the weights less often but leave too few waves (64 tokens, 16384x2048: 12.9 us with one block, 15.0
+// with two, 25.6 with four).
 //
-// F (1, 2, 4; MT = 1): few activation rows leave most of the 16 x 16 results of a product unused, and few
+// F (1, 2, 4): few activation rows leave most of the 16 x 16 results of a product unused, and few
 // output channels leave CUs without work. With F > 1 a product takes F stages at once: row and column
 // f C + i of the operands hold row i of the activations and channel i of stage f, so that its F diagonal
 // blocks are partial sums of the same C x C results. One step is then F stages, a workgroup has C channels
@@ -181,24 +184,28 @@ __device__ __forceinline__ void turn_fence()
 // 16 neighbouring lanes and turns the 16 x 128 tile in its own corner of LDS (no barrier), where run c
 // of row r sits in slot c ^ r so that both sides are free of bank conflicts.
 // Q: quads of operand rows that hold activations at most (1 for M <= 4 with F = 1, else 4).
-template <int DT, int F, int MT, int Q, int GS, int U, int TN> struct GemvStep {
+template <int DT, int Q, int GS, int U, int TN> struct GemvStep {
     u4_t w[U][TN];
     uint16_t sc[U][TN][GS];
-    ActRun<DT> x[U][MT][Q];
+    ActRun<DT> x[U][Q];
 };
 
-template <int DT, int F, int MT, int Q, int GS, int U, int TN, int MAXW>
+template <int DT, int F, int Q, int GS, int U, int TN, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 {
     typedef typename ActOf<DT>::raw raw;
     constexpr int P = ActOf<DT>::PARTS, C = 16 / F;
     constexpr int TILE = P * 4 * Q * 16;  // 16-byte slots of a tile in turn
-    // per wave: one tile in turn [P][4 Q][16]; afterwards [waves][TN][MT][4][64] floats
+    // per wave: one tile in turn [P][4 Q][16]; afterwards [waves][TN][4][64] floats
     extern __shared__ u4_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int c0 = blockIdx.x * (TN * C), m0 = blockIdx.y * (16 * MT);
+    // consecutive workgroups go to different XCDs: the row blocks of one tile follow each other on one
+    // XCD, so that its L2 holds the tile's weights for all of them
+    const int block = blockIdx.x / 8;
+    const int c0 = (block / a.row_blocks * 8 + blockIdx.x % 8) * (TN * C), m0 = block % a.row_blocks * 16;
+    if (c0 >= a.N) return;
     const int stages = (a.K + 127) >> 7, steps = (stages + F - 1) / F, ngroups = a.K >> (5 + a.gshift);
     u4_t *turn = lds + wave * TILE;
 
@@ -221,37 +228,31 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     for (int t = 0; t < TN; ++t) soff[t] = (uint32_t)min(c0 + t * C + r % C, a.N - 1);
     auto scale = [&](int t, int grp) { return (a.w_scale + (int64_t)grp * a.N)[soff[t]]; };
     // as loader: lane (g, r) holds run r of operand rows 4 q + g, row (4 q + g) % C of stage (4 q + g) / C.
-    // Rows past M repeat the last one; their results are not stored. 64 rows stay inside 32-bit offsets.
-    uint32_t xoff[MT][Q];
+    // Rows past M repeat the last one; their results are not stored. 16 rows stay inside 32-bit offsets.
+    uint32_t xoff[Q];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            xoff[m][q] = (uint32_t)min(16 * m + (4 * q) % C + g, a.M - m0 - 1) * (uint32_t)a.ldx;
+    for (int q = 0; q < Q; ++q)
+        xoff[q] = (uint32_t)min((4 * q) % C + g, a.M - m0 - 1) * (uint32_t)a.ldx;
     const raw *xbase = reinterpret_cast<const raw *>(a.X) + (int64_t)m0 * a.ldx;
     // start of the stage that operand row 4 q is from
     auto stage_k = [&](int step, int q) { return (step * F + 4 * q / C) * 128; };
 
-    f4_t acc[TN][MT];
+    f4_t acc[TN];
 #pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < TN; ++t) acc[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    typedef GemvStep<DT, F, MT, Q, GS, U, TN> Step;
+    typedef GemvStep<DT, Q, GS, U, TN> Step;
     // activations first: they are needed first, and the weights can then be used as they arrive
     auto load = [&](int s0, Step &d) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int step = s0 + u * waves;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    const int k0 = stage_k(step, q), k = k0 < a.K ? k0 : 0;
-                    // runs past K read the last one; turn_rows makes them zeros
-                    d.x[u][m][q] = load_run<DT>(xbase + k + (xoff[m][q] + (uint32_t)min(8 * r, a.K - 8 - k)));
-                }
+            for (int q = 0; q < Q; ++q) {
+                const int k0 = stage_k(step, q), k = k0 < a.K ? k0 : 0;
+                // runs past K read the last one; turn_rows makes them zeros
+                d.x[u][q] = load_run<DT>(xbase + k + (xoff[q] + (uint32_t)min(8 * r, a.K - 8 - k)));
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -266,33 +267,29 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
                     d.sc[u][t][q] = scale(t, grp);
                 }
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-                d.w[u][t] = *weights(t, s);
+            for (int t = 0; t < TN; ++t) d.w[u][t] = *weights(t, s);
         }
     };
-    u4_t x[U][MT][P][4];
+    u4_t x[U][P][4];
     auto turn_rows = [&](int s0, Step &d, auto last) {  // only a wave's last steps can reach past K
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int q = 0; q < Q; ++q) {
+                if (last.value && stage_k(s0 + u * waves, q) + 8 * r >= a.K) d.x[u][q] = ActRun<DT>{};
+                u4_t p[P];
+                act_parts<DT>(d.x[u][q], p);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    if (last.value && stage_k(s0 + u * waves, q) + 8 * r >= a.K) d.x[u][m][q] = ActRun<DT>{};
-                    u4_t p[P];
-                    act_parts<DT>(d.x[u][m][q], p);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) turn[(i * 4 * Q + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
-                }
-                turn_fence();
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)  // with one quad of rows the operand's other rows repeat them
-                        x[u][m][i][j] =
-                            turn[(i * 4 * Q + r % (4 * Q)) * 16 + ((4 * j + g) ^ (r % (4 * Q)))];
-                turn_fence();
+                for (int i = 0; i < P; ++i) turn[(i * 4 * Q + 4 * q + g) * 16 + (r ^ (4 * q + g))] = p[i];
             }
+            turn_fence();
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // with one quad of rows the operand's other rows repeat them
+                    x[u][i][j] = turn[(i * 4 * Q + r % (4 * Q)) * 16 + ((4 * j + g) ^ (r % (4 * Q)))];
+            turn_fence();
+        }
     };
     auto multiply = [&](int s0, const Step &d) {
 #pragma unroll
@@ -300,21 +297,15 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
             if (u > 0 && s0 + u * waves >= steps) break;
 #pragma unroll
             for (int t = 0; t < TN; ++t) {
-                f4_t part[MT];
+                f4_t part;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const u4_t b = DT == W4A4_F16 ? widen_f16(d.w[u][t][j]) : widen_bf16(d.w[u][t][j]);
+                    if (j % (4 / GS) == 0) part = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (j % (4 / GS) == 0) part[m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = P - 1; i >= 0; --i) part[m] = mma<DT>(x[u][m][i][j], b, part[m]);
-                    }
-                    if ((j + 1) % (4 / GS) == 0) {
-                        const float f = __half2float(__ushort_as_half(d.sc[u][t][j * GS / 4]));
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) acc[t][m] += part[m] * f;
-                    }
+                    for (int i = P - 1; i >= 0; --i) part = mma<DT>(x[u][i][j], b, part);
+                    if ((j + 1) % (4 / GS) == 0)
+                        acc[t] += part * __half2float(__ushort_as_half(d.sc[u][t][j * GS / 4]));
                 }
             }
         }
@@ -338,13 +329,10 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[(((wave * TN + t) * MT + m) * 4 + i) * 64 + lane] = acc[t][m][i];
+        for (int i = 0; i < 4; ++i) red[((wave * TN + t) * 4 + i) * 64 + lane] = acc[t][i];
     __syncthreads();
     // result (m, c) of a tile: operand row f C + m (lanes of group row / 4, register row % 4), column f C + c
-    const int live = min(a.M - m0, F == 1 ? 16 * MT : C);
+    const int live = min(a.M - m0, C);
     for (int e = tid; e < TN * C * live; e += blockDim.x) {
         const int c = e % C, t = e / C % TN, m = e / (C * TN);
         const int col = c0 + t * C + c;
@@ -354,67 +342,67 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const int row = f * C + m;
-                y += red[(((v * TN + t) * MT + row / 16) * 4 + row % 4) * 64 + (row % 16) / 4 * 16 + f * C + c];
+                y += red[((v * TN + t) * 4 + row % 4) * 64 + row / 4 * 16 + f * C + c];
             }
         if (DT != W4A4_F16) y *= 16.0f;  // the codes were sixteenths
         if (a.epilogue == W4A4_EPI_GELU) y = gelu_f32(y);
-        else if (a.epilogue == W4A4_EPI_RESIDUAL) y += load_y<DT>(a.residual[(m0 + m) * a.ldr + col]);
-        a.Y[(m0 + m) * a.ldy + col] = store_y<DT>(y);
+        else if (a.epilogue == W4A4_EPI_RESIDUAL) y += load_y<DT>(a.residual[(int64_t)(m0 + m) * a.ldr + col]);
+        a.Y[(int64_t)(m0 + m) * a.ldy + col] = store_y<DT>(y);
     }
 }
 
-template <int DT, int F, int MT, int Q, int GS, int TN>
-static int run_gemv(const W4gArgs &a, hipStream_t s)
+// Waves: enough of them to keep the memory busy, at most one per step (16384x2048 with eight tokens: 11.4 us
+// with 1024 waves in all, 7.8 with 2048, 7.5 with 3072 and with more).
+template <int DT, int F, int Q, int GS, int TN>
+static int run_gemv(W4gArgs a, hipStream_t s)
 {
-    constexpr int P = ActOf<DT>::PARTS;
-    constexpr int U = P == 1 && Q == 1 && TN <= 2 ? 2 : 1;
-    constexpr int MAXW = MT * P >= 6 ? 4 : MT == 1 && P == 1 ? 16 : 8;
-    constexpr int C = 16 / F;
-    const int tiles = (a.N + TN * C - 1) / (TN * C), rows = (a.M + 16 * MT - 1) / (16 * MT);
-    const int steps = ((a.K + 127) / 128 + F - 1) / F;
+    constexpr int P = ActOf<DT>::PARTS, U = P == 1 && Q == 1 && TN <= 2 && TN * GS <= 4 ? 2 : 1;
+    constexpr int MAXW = P == 1 ? 16 : 8, C = 16 / F;
+    const int tiles = (a.N + TN * C - 1) / (TN * C), steps = ((a.K + 127) / 128 + F - 1) / F;
+    a.row_blocks = (a.M + 15) / 16;
     int waves = 1;
-    while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * rows * waves < 4096)) waves *= 2;
-    const size_t lds = (size_t)waves * 1024 * std::max(P * Q, TN * MT);
-    const auto kernel = k_gemv_w4g<DT, F, MT, Q, GS, U, TN, MAXW>;
-    if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, "gemv_w4g")) return rc;
-    hipLaunchKernelGGL(kernel, dim3(tiles, rows), dim3(64 * waves), lds, s, a);
+    while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * a.row_blocks * waves < 3072))
+        waves *= 2;
+    const size_t lds = (size_t)waves * 1024 * std::max(P * Q, TN);
+    const auto kernel = k_gemv_w4g<DT, F, Q, GS, U, TN, MAXW>;
+    if (lds > 65536)  // more than every kernel gets unasked
+        if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, "gemv_w4g")) return rc;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)(tiles + 7) / 8 * 8 * a.row_blocks)), dim3(64 * waves),
+                       lds, s, a);
     return check_launch("gemv_w4g");
 }
 
-template <int DT, int F, int MT, int Q, int TN>
-static int pick_group(const W4gArgs &a, hipStream_t s)
+template <int DT, int F, int Q, int TN> static int pick_group(const W4gArgs &a, hipStream_t s)
 {
-    if (a.gshift == 0) return run_gemv<DT, F, MT, Q, 4, TN>(a, s);
-    if (a.gshift == 1) return run_gemv<DT, F, MT, Q, 2, TN>(a, s);
-    return run_gemv<DT, F, MT, Q, 1, TN>(a, s);
+    // four scales a stage leave registers for two tiles of 16 rows
+    if (a.gshift == 0) return run_gemv<DT, F, Q, 4, (Q == 4 && TN == 4) ? 2 : TN>(a, s);
+    if (a.gshift == 1) return run_gemv<DT, F, Q, 2, TN>(a, s);
+    return run_gemv<DT, F, Q, 1, TN>(a, s);
 }
 
-template <int DT, int MT, int Q> static int pick_tiles(const W4gArgs &a, hipStream_t s)
+// Two or four tiles per workgroup share its turned activations where there are tiles enough for all CUs.
+template <int DT, int Q> static int pick_tiles(const W4gArgs &a, hipStream_t s)
 {
-    const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.M + 16 * MT - 1) / (16 * MT));
-    if (MT == 1 && wgs >= 1024) return pick_group<DT, 1, MT, Q, MT == 1 ? 4 : 1>(a, s);
-    if (MT * ActOf<DT>::PARTS < 4 && wgs >= 512) return pick_group<DT, 1, MT, Q, MT * ActOf<DT>::PARTS < 4 ? 2 : 1>(a, s);
-    return pick_group<DT, 1, MT, Q, 1>(a, s);
+    const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.M + 15) / 16);
+    if (wgs >= 1024) return pick_group<DT, 1, Q, 4>(a, s);
+    if (wgs >= 512) return pick_group<DT, 1, Q, 2>(a, s);
+    return pick_group<DT, 1, Q, 1>(a, s);
 }
 
 // F stages per product while that gives the CUs workgroups they lack.
 template <int DT> static int pick_rows(const W4gArgs &a, hipStream_t s)
 {
     const int tiles = (a.N + 15) / 16;
-    if (a.M <= 4 && a.K > 256 && tiles <= 64) return pick_group<DT, 4, 1, 4, 1>(a, s);
-    if (a.M <= 8 && a.K > 128 && tiles <= 128) return pick_group<DT, 2, 1, 4, 1>(a, s);
-    if (a.M <= 4) return pick_tiles<DT, 1, 1>(a, s);
-    if (a.M <= 16) return pick_tiles<DT, 1, 4>(a, s);
-    // fp32 activations take three operand registers for one
-    if (a.M <= 32 || DT == W4A4_F32) return pick_tiles<DT, 2, 4>(a, s);
-    return pick_tiles<DT, DT == W4A4_F32 ? 2 : 4, 4>(a, s);
+    if (a.M <= 4 && a.K > 256 && tiles <= 64) return pick_group<DT, 4, 4, 1>(a, s);
+    if (a.M <= 8 && a.K > 128 && tiles <= 128) return pick_group<DT, 2, 4, 1>(a, s);
+    return a.M <= 4 ? pick_tiles<DT, 1>(a, s) : pick_tiles<DT, 4>(a, s);
 }
 
 int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const uint8_t *wt,
                     const uint16_t *w_scale, int gshift, int N, uint16_t *Y, int64_t ldy, int epilogue,
                     const uint16_t *residual, int64_t ldr, hipStream_t s)
 {
-    const W4gArgs a{X, ldx, wt, w_scale, M, K, N, gshift, Y, ldy, epilogue, residual, ldr};
+    const W4gArgs a{X, ldx, wt, w_scale, M, K, N, gshift, Y, ldy, epilogue, residual, ldr, 0};
     switch (x_dtype) {
     case W4A4_F16: return pick_rows<W4A4_F16>(a, s);
     case W4A4_BF16: return pick_rows<W4A4_BF16>(a, s);
