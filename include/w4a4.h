@@ -395,9 +395,11 @@ int w4a4_pack_weights_gptq(const void *W, int w_dtype, int N, int K, int64_t ldw
  *    |w| / 7)), 1 for a group of zeros, and held inside fp16's range (2^-24 below, 65504 above);
  *    c = clamp(rint(fp32(w / s)), -8, 7). W must be finite.
  *  - w4a4_codes_to_w4g: packed int4 codes [N][K/2] of any other solver -> wt (K % 32 == 0).
- *  - w4a4_gemv_w4g: the product, for any M (M == 0 is a valid empty call). X fp16, fp32 or bf16 with
- *    any row stride; Y and residual fp16, for bf16 X bf16. Epilogues as in w4a4_gemm (residual is
- *    added to the fp32 sum; it may be Y itself). No workspace.
+ *  - w4a4_gemv_w4g: the product for M >= 0 rows (M == 0 is a valid empty call; meant for a few, right
+ *    for any). X fp16, fp32 or bf16 at any element's address and row stride; Y and residual fp16, for
+ *    bf16 X bf16. Epilogues as in w4a4_gemm (residual is added to the fp32 sum; it may be Y itself). No
+ *    workspace; results do not depend on timing. Limits (W4A4_ERR_UNSUPPORTED above): N 2^24, K 2^23,
+ *    N K 2^34, M 2^21, ldx 2^24.
  * ------------------------------------------------------------------------------------------- */
 size_t w4a4_w4g_operand_bytes(int N, int K);
 int w4a4_pack_weights_w4g(const void *W, int w_dtype, int N, int K, int64_t ldw, int group,
@@ -420,7 +422,7 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
  * w4a4_qk_norm_rope: per-head RMS norm and position rotation of queries and keys in one pass, and the
  * append of keys and values to the cache. Rows q [M][heads][head_dim], k and v [M][kv_heads][head_dim]
  * with row strides ldq, ldk, ldv (slices of a QKV output; heads are adjacent); head_dim a multiple of
- * 16 up to 512.
+ * 16 up to 512, M up to 2^25.
  *   y = x / sqrt(mean(x^2) + eps) * weight  (weight NULL: ones; the mean square is an fp32 number)
  * then the first rot_dim channels (a multiple of 16, 0: none) are rotated in pairs (a, b) ->
  * (a cos t - b sin t, b cos t + a sin t), t = positions[m] * inv_freq[i]: pair i is channels
@@ -438,8 +440,9 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
  * visible page outside [0, num_pages), or lens[b] > table_width * page_size, makes that sequence's
  * output NaN and reads nothing outside the cache. max_len is the largest length the work is split for:
  * a longer sequence is still right, only slower. head_dim 64, 96, 128, 192 or 256 (else
- * W4A4_ERR_UNSUPPORTED); out [B][heads][head_dim] with row stride ldo. Results do not depend on
- * timing. ws: w4a4_paged_attn_workspace_bytes(...) bytes of the same sizes, 256-byte aligned.
+ * W4A4_ERR_UNSUPPORTED), B up to 65535 and B * heads up to 2^23; out [B][heads][head_dim] with row
+ * stride ldo. Results do not depend on timing. ws: w4a4_paged_attn_workspace_bytes(...) bytes of the
+ * same sizes, 256-byte aligned.
  * ------------------------------------------------------------------------------------------- */
 int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
                       int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,

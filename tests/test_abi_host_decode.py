@@ -34,6 +34,8 @@ def gemv(L, *, X=FAKE, dt=bd.W4A4_F16, M=2, K=256, ldx=256, wt=FAKE, s=FAKE, gro
     (dict(M=-1), bd.W4A4_ERR_ARG),
     (dict(M=(1 << 21) + 1), bd.W4A4_ERR_UNSUPPORTED),
     (dict(K=(1 << 23) + 64, ldx=(1 << 23) + 64), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(K=1 << 20, ldx=1 << 20, N=1 << 20, ldy=1 << 20), bd.W4A4_ERR_UNSUPPORTED),  # N K above 2^34
+    (dict(ldx=(1 << 24) + 8), bd.W4A4_ERR_UNSUPPORTED),
     (dict(dt=3), bd.W4A4_ERR_ARG),
     (dict(ldx=255), bd.W4A4_ERR_SHAPE),
     (dict(ldy=47), bd.W4A4_ERR_SHAPE),
@@ -130,6 +132,7 @@ def rope(L, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=bd.W4A4_F32), bd.W4A4_ERR_ARG),
     (dict(M=-1), bd.W4A4_ERR_ARG),
+    (dict(M=(1 << 25) + 1), bd.W4A4_ERR_UNSUPPORTED),
     (dict(H=0), bd.W4A4_ERR_ARG),
     (dict(KV=0), bd.W4A4_ERR_ARG),
     (dict(D=0), bd.W4A4_ERR_ARG),
@@ -195,6 +198,7 @@ def attn(L, **kw):
     (dict(dt=bd.W4A4_F32), bd.W4A4_ERR_ARG),
     (dict(B=-1), bd.W4A4_ERR_ARG),
     (dict(B=1 << 16), bd.W4A4_ERR_UNSUPPORTED),
+    (dict(B=60000, H=256, ldq=1 << 14, ldo=1 << 14), bd.W4A4_ERR_UNSUPPORTED),  # B heads above 2^23
     (dict(H=0), bd.W4A4_ERR_ARG),
     (dict(H=9, ldq=576, ldo=576), bd.W4A4_ERR_SHAPE),      # heads not a multiple of kv_heads
     (dict(D=80, ldq=640, ldo=640), bd.W4A4_ERR_UNSUPPORTED),
@@ -234,7 +238,8 @@ def test_paged_attn_rejects(L, kw, code):
 
 def test_paged_attn_empty_and_workspace(L):
     assert attn(L, B=0, q=NULL, out=NULL, table=NULL, lens=NULL) == bd.W4A4_OK
-    assert L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 64, 0, 0) == 0          # one split
+    assert L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 32, 0, 0) == 0          # nothing to split
+    assert attn(L, B=0, q=NULL, out=NULL, table=NULL, lens=NULL, max_len=1 << 30) == bd.W4A4_OK
     big = L.w4a4_paged_attn_workspace_bytes(2, 8, 2, 64, 100000, 0, 0)
     assert big > 0
     # a window bounds what there is to split

@@ -215,3 +215,17 @@ def test_repeats_bit_for_bit():
     first = bd.gemv_w4g(X, wt, sd)
     for _ in range(5):
         assert torch.equal(bd.gemv_w4g(X, wt, sd), first)
+
+
+def test_more_rows_than_one_launch_holds():
+    """Rows past the workgroups of one launch (here 1008 rows for 2^20 channels) continue in the next."""
+    import torch
+    M, K, N, group = 1030, 32, 1 << 20, 32
+    g = torch.Generator(device="cuda").manual_seed(0)
+    X = torch.randn((M, K), generator=g, device="cuda").half()
+    wt = torch.randint(0, 256, (N // 16 * 1024,), generator=g, dtype=torch.uint8, device="cuda")
+    s = torch.rand((1, N), generator=g, device="cuda").half()
+    r = torch.randn((M, N), generator=g, device="cuda").half()
+    Y = bd.gemv_w4g(X, wt, s, epilogue=bd.EPI_RESIDUAL, residual=r)
+    for a, b in ((0, 16), (992, 1008), (1008, 1024), (1024, 1030)):
+        assert torch.equal(Y[a:b], bd.gemv_w4g(X[a:b], wt, s, epilogue=bd.EPI_RESIDUAL, residual=r[a:b])), a

@@ -1017,6 +1017,8 @@ static int check_group(int N, int K, int group, int *gshift)
     if (K % group) return fail(W4A4_ERR_SHAPE, "K = %d is not a multiple of the group %d", K, group);
     if (K > (1 << 23) || N > (1 << 24))
         return fail(W4A4_ERR_UNSUPPORTED, "N = %d, K = %d above 2^24, 2^23", N, K);
+    if ((int64_t)N * K > ((int64_t)1 << 34))
+        return fail(W4A4_ERR_UNSUPPORTED, "N * K = %lld above 2^34", (long long)N * K);
     *gshift = group == 32 ? 0 : group == 64 ? 1 : group == 128 ? 2 : 3;
     return W4A4_OK;
 }
@@ -1136,6 +1138,7 @@ int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, in
     int rc;
     if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim))) return rc;
     if (M < 0) return fail(W4A4_ERR_ARG, "M = %d negative", M);
+    if (M > (1 << 25)) return fail(W4A4_ERR_UNSUPPORTED, "M = %d above 2^25", M);
     if (head_dim % 16 || head_dim > 512)
         return fail(W4A4_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 16 up to 512", head_dim);
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
@@ -1222,6 +1225,8 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
         return fail(W4A4_ERR_SHAPE, "heads %d is not a multiple of kv_heads %d", heads, kv_heads);
     if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
         return fail(W4A4_ERR_UNSUPPORTED, "head_dim %d is not 64, 96, 128, 192 or 256", head_dim);
+    if ((int64_t)B * heads > (1 << 23))
+        return fail(W4A4_ERR_UNSUPPORTED, "B * heads = %lld above 2^23", (long long)B * heads);
     const int64_t width = (int64_t)heads * head_dim;
     if ((rc = check_rows16(q, B, ldq, width, "q")) || (rc = check_rows16(out, B, ldo, width, "out")) ||
         (rc = check_cache(k_cache, v_cache, kv_heads, head_dim, num_pages, page_size, page_stride)))

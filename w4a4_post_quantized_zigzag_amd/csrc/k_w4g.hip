@@ -402,12 +402,18 @@ int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const
                     const uint16_t *w_scale, int gshift, int N, uint16_t *Y, int64_t ldy, int epilogue,
                     const uint16_t *residual, int64_t ldr, hipStream_t s)
 {
-    const W4gArgs a{X, ldx, wt, w_scale, M, K, N, gshift, Y, ldy, epilogue, residual, ldr, 0};
-    switch (x_dtype) {
-    case W4A4_F16: return pick_rows<W4A4_F16>(a, s);
-    case W4A4_BF16: return pick_rows<W4A4_BF16>(a, s);
-    default: return pick_rows<W4A4_F32>(a, s);
+    // a launch holds less than 2^32 threads: at most 2^22 workgroups of 1024
+    const int rows = 16 * std::max(1, (1 << 22) / ((N + 15) / 16 + 8));
+    for (int64_t m = 0; m < M; m += rows) {
+        const char *x = reinterpret_cast<const char *>(X) + m * ldx * (x_dtype == W4A4_F32 ? 4 : 2);
+        const W4gArgs a{x,         ldx, wt,       w_scale,  (int)std::min<int64_t>(rows, M - m), K, N, gshift,
+                        Y + m * ldy, ldy, epilogue, residual ? residual + m * ldr : nullptr, ldr, 0};
+        const int rc = x_dtype == W4A4_F16    ? pick_rows<W4A4_F16>(a, s)
+                       : x_dtype == W4A4_BF16 ? pick_rows<W4A4_BF16>(a, s)
+                                              : pick_rows<W4A4_F32>(a, s);
+        if (rc) return rc;
     }
+    return W4A4_OK;
 }
 
 // ---- weight operand -----------------------------------------------------------------------------
