@@ -273,15 +273,19 @@ def test_graph_replays_with_growing_lengths():
         torch.cuda.synchronize()
 
 
-def test_side_stream_and_caller_workspace():
+@pytest.mark.parametrize("n", [2000, 20000])
+def test_side_stream_and_caller_workspace(n):
     import torch
-    b = Batch([2000], 4, 1, 64, 16, "fp16", seed=12)
+    b = Batch([n], 4, 1, 64, 16, "fp16", seed=12)
     want = b.run()
     need = bd.lib().w4a4_paged_attn_workspace_bytes(1, 4, 1, 64, b.table.shape[1] * 16, 0, 0)
-    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN bytes: nothing stale is read
-    assert need > 0 and torch.equal(b.run(ws=ws), want)
-    with pytest.raises(bd.W4A4Error, match="workspace"):
-        b.run(ws=ws[:need - 256])
+    assert need > 0 or n == 2000            # the longer one is split and joined
+    # NaN bytes: nothing stale is read
+    ws = torch.full((max(need, 256),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(b.run(ws=ws), want)
+    if need:
+        with pytest.raises(bd.W4A4Error, match="workspace"):
+            b.run(ws=ws[:need - 256])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):

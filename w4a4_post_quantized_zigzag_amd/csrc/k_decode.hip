@@ -347,8 +347,9 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     if (split >= a.splits) return;
     const int group = a.heads / a.kv_heads, G = min(16, group - ht * 16), h0 = kvh * group + ht * 16;
     const int n = a.lens[b];
-    const AttnTiles tl = attn_tiles(n, a);
+    const int32_t *table = a.table + (int64_t)b * a.ldt;
     const int t0 = split * a.tiles_per_split;
+    const AttnTiles tl = attn_tiles(n, a);
     const int t1 = split + 1 == a.splits ? tl.T : min(tl.T, t0 + a.tiles_per_split);
     uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h0 * D;
     if (tl.T == 0) {  // nothing visible: zeros
@@ -370,7 +371,6 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a
     for (int i = 0; i < VE; ++i) acc[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float mx = -INFINITY, sum = 0.0f;
     bool bad = tl.over;
-    const int32_t *table = a.table + (int64_t)b * a.ldt;
     const int first_in_window = a.window > 0 ? n - a.window : 0;
     auto seen = [&](int key) { return key < n && (key >= first_in_window || key < a.sinks); };
 
@@ -529,14 +529,23 @@ constexpr int ATTN_MAX_SPLITS = 256;
 template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a)
 {
     constexpr int TC = D / 4, ROWS = 256 / TC;  // threads over the channels, splits at a time
+    constexpr int AHEAD = 8;
     __shared__ float4 red[ROWS][TC];
     __shared__ float weight[ATTN_MAX_SPLITS], wave_top[4], wave_sum[4];
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
+    const int c = tid % TC, row = tid / TC;
+    const int64_t at = ((int64_t)b * a.heads + h) * a.splits;
+    const float4 *p = reinterpret_cast<const float4 *>(a.part + at * D) + c;
+    // everything is asked for before the length has arrived; what no split wrote is not used
+    float2 st = tid < a.splits ? a.stat[at + tid] : make_float2(0.0f, 0.0f);
+    float4 v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (row < ROWS && row + i * ROWS < a.splits) v[i] = p[(int64_t)(row + i * ROWS) * TC];
     const AttnTiles tl = attn_tiles(a.lens[b], a);
     if (tl.T <= a.tiles_per_split) return;  // written by its only workgroup
     const int used = min(a.splits, (tl.T + a.tiles_per_split - 1) / a.tiles_per_split);
-    const int64_t at = ((int64_t)b * a.heads + h) * a.splits;
-    const float2 st = tid < used ? a.stat[at + tid] : make_float2(-INFINITY, 0.0f);
+    if (tid >= used) st = make_float2(-INFINITY, 0.0f);
     float top = st.x;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
@@ -551,19 +560,19 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
     if ((tid & 63) == 0) wave_sum[wave] = l;
     __syncthreads();
     l = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
-    const int c = tid % TC, row = tid / TC;
     float4 o = make_float4(0, 0, 0, 0);
+    auto add = [&](const float4 &x, float w) {
+        o.x = fmaf(w, x.x, o.x);
+        o.y = fmaf(w, x.y, o.y);
+        o.z = fmaf(w, x.z, o.z);
+        o.w = fmaf(w, x.w, o.w);
+    };
     if (row < ROWS) {
-        const float4 *p = reinterpret_cast<const float4 *>(a.part + at * D) + c;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (row + i * ROWS < used) add(v[i], weight[row + i * ROWS]);
 #pragma unroll 4
-        for (int s = row; s < used; s += ROWS) {
-            const float4 v = p[(int64_t)s * TC];
-            const float w = weight[s];
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
-        }
+        for (int s = row + AHEAD * ROWS; s < used; s += ROWS) add(p[(int64_t)s * TC], weight[s]);
         red[row][c] = o;
     }
     __syncthreads();
@@ -580,9 +589,11 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
     }
 }
 
-// How many workgroups share a sequence. The lengths are on the device; only max_len is known here.
-//  - Where every wave gets a tile of its own and there still are CUs left (up to 1024 tiles in all), one
-//    wave per tile: 1001 tokens with one key/value head take 10.0 us, against 10.4 us in workgroups of 4.
+// How many waves and workgroups share a sequence. The lengths are on the device; only max_len is known.
+//  - With at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one tile
+//    per workgroup. (1001 tokens, one key/value head of 256: 10.0 us, 10.4 us in workgroups of 4 waves;
+//    one workgroup of up to 16 waves without a join is faster only below about 300 tokens, and takes twice
+//    as long at 1000.)
 //  - With a window all sequences are about as long, and two sequences leave little to balance: few long
 //    runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 45.7 us with 1024 workgroups, 48.7
 //    us with 2048; 131071 and 87000 tokens, 8 heads: 163 us with 512, 173 us with 2048).
