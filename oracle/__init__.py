@@ -2,7 +2,7 @@
 rotation, symmetric int4 RTN / per-step / per-token quantization, integer GEMM and dequantization;
 the same steps on the int8 grid for the W8A8 linears (``bits=8``); group-wise (per rotation block)
 per-step activation scales with their block-wise GEMM (``*_grouped``, linear mode "per_block");
-the GPTQ weight solver (``gptq_*``).
+the GPTQ weight solver (``gptq_*``). The single-token operators' oracle is ``oracle.decode``.
 
 TEST INFRASTRUCTURE ONLY. Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` leg
 of ``bench.py`` may import this package. It shares no code with the GPU library and never imports
