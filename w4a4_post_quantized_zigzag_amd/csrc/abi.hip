@@ -1026,7 +1026,7 @@ static int check_group(int N, int K, int group, int *gshift)
 size_t w4a4_w4g_operand_bytes(int N, int K)
 {
     if (N <= 0 || K <= 0) return 0;
-    return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128) * 1024;
+    return (size_t)(((int64_t)N + 15) / 16) * (size_t)(((int64_t)K + 127) / 128) * 1024;
 }
 
 int w4a4_pack_weights_w4g(const void *W, int w_dtype, int N, int K, int64_t ldw, int group,

@@ -52,6 +52,8 @@ __device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinte
 // over its heads, multiplied with the norm's weights: y = (x (w cos) -+ x' (w' sin)) / sqrt(..), with the
 // partner channel x' taken from the neighbouring lanes' raw elements. The angle is reduced to a fraction
 // of a turn in fp64, so far positions lose nothing.
+// Measured: 8191 tokens of 32 + 8 heads of 128 41 us (4.9 TB/s, what a large copy reaches); 1600 tokens of 16
+// + 16 heads of 64 6.7 us; one token 4.0 us per launch in a graph, most of it latency.
 // ================================================================================================
 constexpr int HEADS_AHEAD = 4;
 
@@ -271,8 +273,11 @@ int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 //    loads D / 16 neighbouring channels of those eight keys and pairs them up with byte permutes;
 //    nothing passes through LDS and no cross-lane step is needed but the maximum's.
 //  - p is split in two 16-bit parts (p = hi + lo to 2^-16 or better), two products per tile.
-// Tiles of one sequence go round-robin to the four waves of a workgroup and, above that, in equal
-// runs to `splits` workgroups, joined in LDS and by k_attn_join in a fixed order.
+// Tiles of one sequence go in equal runs to `splits` workgroups and there round-robin to the waves (four,
+// one where there is little to do), joined in LDS and by k_attn_join in a fixed order.
+// Measured: 32 sequences of 0 to 8191 tokens, 32 heads over 8 of 128, 81 us (5.05 TB/s); two of 131071 and 87000
+// tokens 154 us (5.8 TB/s, part of it from the last-level cache); 64 with a window of 1000 and 16 heads of 64
+// 42.5 us (5.0 TB/s); one of 1001 tokens, one key/value head of 256, 9.6 us, the chain of two launches.
 // ================================================================================================
 
 // Tiles of 32 keys that hold something visible: tiles [0, ns) and from w0 on, T in all.
@@ -602,7 +607,7 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
 //    and 82 us).
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks)
 {
-    const int head_tiles = (heads / kv_heads + 15) / 16;
+    const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;
     int64_t tiles = ((int64_t)max_len + 31) / 32;
     if (window > 0)  // a run of w keys touches at most w / 32 + 2 tiles
         tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
