@@ -354,7 +354,7 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
 }
 
 // Waves: enough of them to keep the memory busy, at most one per step (16384x2048 with eight tokens: 11.4 us
-// with 1024 waves in all, 7.8 with 2048, 7.5 with 3072 and with more).
+// with 1024 waves in all, 7.8 with 2048, 7.5 from 3000 on).
 template <int DT, int F, int Q, int GS, int TN>
 static int run_gemv(W4gArgs a, hipStream_t s)
 {
@@ -363,7 +363,7 @@ static int run_gemv(W4gArgs a, hipStream_t s)
     const int tiles = (a.N + TN * C - 1) / (TN * C), steps = ((a.K + 127) / 128 + F - 1) / F;
     a.row_blocks = (a.M + 15) / 16;
     int waves = 1;
-    while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * a.row_blocks * waves < 3072))
+    while (waves < MAXW && waves * 2 <= steps && (waves < 4 || (int64_t)tiles * a.row_blocks * waves < 3000))
         waves *= 2;
     const size_t lds = (size_t)waves * 1024 * std::max(P * Q, TN);
     const auto kernel = k_gemv_w4g<DT, F, Q, GS, U, TN, MAXW>;
