@@ -114,6 +114,17 @@ def test_window_and_sinks(window, sinks, dtype):
     b.check(b.run(window=window, sinks=sinks), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("KV,D", [(2, 64), (16, 96), (1, 256)])
+def test_one_workgroup_per_row(KV, D, dtype):
+    """Rows enough for one workgroup each up to 32 tiles, and a max_len that is shorter than the sequences."""
+    rng = np.random.default_rng(D)
+    b = Batch([0, 1024, 1, 255, 1009] + list(rng.integers(0, 700, 11)), KV, KV, D, 32, dtype, seed=D)
+    for max_len in (1024, 256, 1, 0):
+        b.check(b.run(max_len=max_len))
+    b.check(b.run(max_len=200, window=700, sinks=40), window=700, sinks=40)
+
+
 def test_window_reads_no_hidden_page():
     """Pages without a visible token may be gone from the table and hold anything."""
     import torch

@@ -595,10 +595,12 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
 }
 
 // How many waves and workgroups share a sequence. The lengths are on the device; only max_len is known.
-//  - With at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one tile
-//    per workgroup. (1001 tokens, one key/value head of 256: 10.0 us, 10.4 us in workgroups of 4 waves;
-//    one workgroup of up to 16 waves without a join is faster only below about 300 tokens, and takes twice
-//    as long at 1000.)
+//  - Short sequences get one workgroup of four waves each and no join, which costs 3 us: up to 8 tiles always
+//    (64, 128 and 256 tokens, 8 key/value heads of 128: 4.1, 4.7 and 6.0 us, split 6.9, 6.9 and 7.1; 384 tokens
+//    7.6 and 7.1), up to 32 where the rows alone fill the CUs (16 sequences of 1024 tokens, 8 heads: 13.7 us,
+//    split 17.1; 64 of 768: 39 and 45; 64 of 1 to 768: 23 and 26; but 4 of 1024: 13.2 and 10.5).
+//  - Else, with at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one
+//    tile per workgroup (1001 tokens, one key/value head of 256: 10.0 us, 10.4 us in workgroups of 4 waves).
 //  - With a window all sequences are about as long, and two sequences leave little to balance: few long
 //    runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 45.7 us with 1024 workgroups, 48.7
 //    us with 2048; 131071 and 87000 tokens, 8 heads: 163 us with 512, 173 us with 2048).
@@ -613,6 +615,7 @@ AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int 
         tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
     tiles = std::max<int64_t>(tiles, 1);
     const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
+    if (tiles <= std::clamp<int64_t>(rows / 4, 8, 32)) return {1, (int)tiles, ATTN_WAVES};
     AttnPlan p;
     p.waves = rows * tiles <= 1024 && tiles <= ATTN_MAX_SPLITS ? 1 : ATTN_WAVES;
     int64_t want = tiles;
