@@ -209,3 +209,23 @@ def test_empty_batch():
     q, k, v, wq, wk, pos = make(2, 2, 1, 64, "fp16")
     qo, ko = bd.qk_norm_rope(q[:0], k[:0], wq, wk, dev(freqs(64)), pos[:0])
     assert qo.shape == (0, 2, 64) and ko.shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 32), (96, 16), (64, 0), (128, 128)])
+def test_infinity_stays_in_its_pair(D, rot, interleaved, dtype):
+    """An infinite channel makes its head's mean infinite: every other channel is 0, the channel itself and,
+    where it is rotated, the other one of its pair are NaN. Neighbours that are not rotated are no pair."""
+    import torch
+    q, k, _, wq, wk, pos = make(D, 2, 1, D, dtype, seed=D + rot)
+    f = freqs(rot)
+    for m in range(D):
+        q[m, 0, m] = float("inf") if m % 2 else float("-inf")
+        k[m, 0, D - 1 - m] = float("inf")
+    qo, ko = bd.qk_norm_rope(q, k, wq, wk, None if f is None else dev(f), pos if rot else None, 1e-6, interleaved)
+    for got, x, w in ((qo[:, :1], q[:, :1], wq), (ko, k, wk)):
+        with np.errstate(invalid="ignore"):
+            want = od.norm_rope(f64(x), host(w), 1e-6, f, host(pos), interleaved)
+        assert np.array_equal(f64(got), want, equal_nan=True), np.argwhere(np.isnan(f64(got)) != np.isnan(want))[:5]
+    assert torch.isfinite(qo[:, 1]).all()
