@@ -1,9 +1,10 @@
 """Build libw4a4.so in-tree with hipcc for gfx950, and the torch-facing marshalling of the single-token
-calls beside it (python -m w4a4_post_quantized_zigzag_amd.build)."""
+calls beside it where torch and a C++ compiler are there (python -m w4a4_post_quantized_zigzag_amd.build)."""
 from __future__ import annotations
 
 import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -36,12 +37,27 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_marshalling() -> str:
+def _lacks_for_marshalling() -> str | None:
+    """What this machine lacks for _decode.so (the library itself needs hipcc alone), or None."""
+    try:
+        from torch.utils.cpp_extension import include_paths
+    except ImportError as e:
+        return f"torch ({e})"
+    cxx = os.environ.get("CXX", "g++")
+    if shutil.which(cxx) is None:
+        return f"the C++ compiler {cxx}"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    if not any(os.path.exists(os.path.join(p, "c10", "hip", "HIPStream.h")) for p in include_paths()):
+        return "torch's HIP headers"
+    return None
+
+
+def _build_marshalling(out: str) -> None:
     """_decode.so: host code against torch's headers and the library just linked beside it."""
     import torch
-    from torch.utils.cpp_extension import include_paths
-    out = os.path.join(PKG, "_decode.so")
-    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    from torch.utils.cpp_extension import ROCM_HOME, include_paths
+    rocm = ROCM_HOME or os.path.dirname(os.path.dirname(shutil.which(HIPCC) or HIPCC))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__=1",
            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(rocm, "include"),
@@ -53,9 +69,8 @@ def _build_marshalling() -> str:
             "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"marshalling build failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{LIB} is complete, but the marshalling build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(out + ".tmp", out)
-    return out
 
 
 def build(verbose: bool = True) -> str:
@@ -68,9 +83,15 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    mod = _build_marshalling()
+    mod = os.path.join(PKG, "_decode.so")
+    if os.path.exists(mod):  # it belongs to the library that was just replaced
+        os.remove(mod)
+    lacks = _lacks_for_marshalling()
+    if lacks is None:
+        _build_marshalling(mod)
     if verbose:
-        print(f"built {LIB} and {mod}")
+        print(f"built {LIB} and {mod}" if lacks is None else
+              f"built {LIB}; without {lacks} the single-token calls have no Python side ({mod})")
     return LIB
 
 
