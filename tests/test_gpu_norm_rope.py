@@ -229,3 +229,29 @@ def test_infinity_stays_in_its_pair(D, rot, interleaved, dtype):
             want = od.norm_rope(f64(x), host(w), 1e-6, f, host(pos), interleaved)
         assert np.array_equal(f64(got), want, equal_nan=True), np.argwhere(np.isnan(f64(got)) != np.isnan(want))[:5]
     assert torch.isfinite(qo[:, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("M", [399, 500, 801, 1400, 1700, 3300])
+def test_any_number_of_waves_per_token(M, interleaved, dtype):
+    """From eight waves on a token to four tokens in a workgroup: against the oracle, and a token's values do not
+    depend on how many others there are."""
+    import torch
+    H, KV, D = 9, 3, 64
+    q, k, v, wq, wk, pos = make(M, H, KV, D, dtype, seed=M)
+    f = freqs(32)
+    page = 16
+    P = -(-M // page) + 1
+    slots = np.random.default_rng(M).permutation(P * page)[:M].astype(np.int64)
+    slots[M // 2] = -1
+    kc, vc = (torch.full((P, KV, page, D), 5.0, dtype=q.dtype, device="cuda") for _ in range(2))
+    ko = torch.empty_like(k)
+    qo = bd.qk_norm_rope_append(q, k, v, wq, wk, dev(f), pos, kc, vc, dev(slots), interleaved=interleaved, k_out=ko)
+    check(qo, q, wq, 1e-6, f, pos, interleaved, dtype)
+    check(ko, k, wk, 1e-6, f, pos, interleaved, dtype)
+    assert np.array_equal(f64(kc), od.append(np.full(kc.shape, 5.0), f64(ko), slots))
+    assert np.array_equal(f64(vc), od.append(np.full(vc.shape, 5.0), f64(v), slots))
+    for a in (0, M - 7):
+        qa, ka = bd.qk_norm_rope(q[a:a + 7], k[a:a + 7], wq, wk, dev(f), pos[a:a + 7], interleaved=interleaved)
+        assert torch.equal(qa, qo[a:a + 7]) and torch.equal(ka, ko[a:a + 7])
