@@ -284,3 +284,14 @@ def test_binding_checks_shapes():
         bd.qk_norm_rope_append(q, k, k, w, w, f, pos, kc, kc.clone(), pos.int())
     with pytest.raises(ValueError, match="required"):
         bd.qk_norm_rope_append(q, k, None, w, w, f, pos, kc, kc, pos)
+
+
+@pytest.mark.parametrize("B,H,KV,D,max_len", [(32, 32, 8, 128, 8191), (64, 16, 16, 64, 8000), (1, 8, 1, 256, 20000),
+                                              (2, 8, 8, 128, 131071), (4, 4, 2, 96, 65), (3, 40, 2, 192, 5000)])
+def test_paged_attn_plans_a_window_that_hides_nothing_as_none(L, B, H, KV, D, max_len):
+    """The lengths differ as much as without a window, so the work is split the same way (the workspace is a
+    measure of it)."""
+    size = lambda window, sinks: L.w4a4_paged_attn_workspace_bytes(B, H, KV, D, max_len, window, sinks)  # noqa: E731
+    most = (1 << 31) - 1
+    for window, sinks in ((max_len, 0), (max_len - 3, 3), (max_len - 40, 100), (1, max_len), (most, 0), (1, most), (most, most)):
+        assert size(window, sinks) == size(0, 0) == size(0, sinks), (window, sinks)

@@ -618,6 +618,7 @@ AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int 
 {
     const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;
     int64_t tiles = ((int64_t)max_len + 31) / 32;
+    if ((int64_t)window + sinks >= max_len) window = 0;  // it hides nothing
     if (window > 0)  // a run of w keys touches at most w / 32 + 2 tiles
         tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
     tiles = std::max<int64_t>(tiles, 1);
