@@ -83,7 +83,8 @@ template <int LH> __device__ __forceinline__ float sum_lanes(float x)
     return x;
 }
 
-template <int DT, int LH, bool PAIRS>
+// PART: with PAIRS, some channels are not rotated.
+template <int DT, int LH, bool PAIRS, bool PART>
 __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
 {
     extern __shared__ float2 turns[];  // [tokens of the workgroup][rot / 2] (cos, sin)
@@ -191,13 +192,6 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
                 }
             }
             const float inv = rsqrtf(fmaf(sum_lanes<LH>(ss), inv_d, a.eps));
-            // A channel that is not rotated takes its neighbour times 0, which must not be an infinity times 0.
-            // A head with one has inv = 0; the selects for every head would cost the pairs 1.4 of 8.7 us (1600
-            // tokens of 16 + 16 heads of 64).
-            if (PAIRS && __any(inv == 0.0f)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = rotated ? o[i] : v[i];
-            }
             float y[8];
             if (h0 + HP <= nq) {
 #pragma unroll
@@ -211,6 +205,19 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) out[i] = is_v ? out[i] : pack16<DT>(y[2 * i], y[2 * i + 1]);
+            // A channel that is not rotated has taken its neighbour times 0, which an infinity there turns into a
+            // NaN. Such a head has inv = 0, so that the channel is 0, or NaN if it is infinite itself. (This keeps
+            // the elements in seven more registers, 103 in all and one wave per SIMD less: 2 % at 1600 tokens of 16
+            // + 16 heads of 64, 14 % at 5000, 6 % at 12000. Selects on every head's values: 20 % at 1600.)
+            if (PART && __any(inv == 0.0f)) {
+                constexpr uint32_t ONES = DT == W4A4_BF16 ? 0x7F80u : 0x7C00u;  // the exponent of what is not finite
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = (x[i] & ONES) == ONES ? 0x7FFFu : 0u;
+                    const uint32_t hi = (x[i] >> 16 & ONES) == ONES ? 0x7FFF0000u : 0u;
+                    out[i] = rotated || is_v || inv != 0.0f ? out[i] : lo | hi;
+                }
+            }
         }
         if (!on || h >= total) return;
         if (is_q) {
@@ -241,8 +248,9 @@ template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool p
     const int waves = std::max(4, a.waves_per_token), tpw = waves / a.waves_per_token;
     const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(64 * waves);
     const size_t lds = (size_t)tpw * (a.rot / 2) * sizeof(float2);
-    if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false>), grid, block, lds, s, a);
+    if (pairs && a.rot < a.D) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, true>), grid, block, lds, s, a);
+    else if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, false>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false, false>), grid, block, lds, s, a);
     return check_launch("qk_norm_rope");
 }
 
