@@ -265,11 +265,16 @@ template <int DT> static int pick_head(const NormRopeArgs &a, bool pairs, hipStr
 
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 {
-    // Few tokens: up to eight waves on one. Many: a wave each, so that its sines serve all heads. About 3000
-    // waves are enough to load the memory (32 + 8 heads of 128: 256 tokens 8.7 us with one wave each, 4.8
-    // with eight; 1024 tokens 10.7, 9.2, 9.4, 10.8 us with 1, 2, 4, 8; 4096 tokens 18.9 and 30.8).
-    a.waves_per_token = 8;
-    while (a.waves_per_token > 1 && a.M * a.waves_per_token > 3200) a.waves_per_token /= 2;
+    // Few tokens: up to eight waves on one. Many: a wave each, so that its sines serve all heads. The limits are
+    // whole workgroups per CU: one of eight waves, three of four, four of four waves with two tokens. Measured
+    // on both sides, us per launch:
+    //   32 + 8 heads of 128    256 tokens: 4.6 with eight waves, 4.9 with four;  300: 5.7, 5.3
+    //                          700: 7.0 with four, 7.6 with two;  850: 8.1, 8.4;  1032: 10.7, 9.3
+    //                          2048: 12.1 with two, 12.3 with one;  2056: 14.6, 13.0
+    //   8 + 1 heads of 256     256: 4.3, 4.5;  264: 4.9, 4.4;  700: 5.2, 5.5;  850: 5.9, 5.7;  1032: 7.2, 6.2
+    //                          2048: 8.4, 8.8;  2056: 10.0, 9.2
+    //   5 + 1 heads of 96      200: 3.8, 3.8;  300: 4.5, 4.2;  768: 4.4, 4.3;  850: 4.8, 4.4;  2056: 6.3, 5.5
+    a.waves_per_token = a.M <= 256 ? 8 : a.M <= 768 ? 4 : a.M <= 2048 ? 2 : 1;
     a.page_shift = a.page_size ? __builtin_ctz((unsigned)a.page_size) : 0;
     return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, interleaved, s)
                               : pick_head<W4A4_F16>(a, interleaved, s);
