@@ -398,9 +398,9 @@ int w4a4_pack_weights_gptq(const void *W, int w_dtype, int N, int K, int64_t ldw
  *  - w4a4_gemv_w4g: the product for M >= 0 rows (M == 0 is a valid empty call; meant for a few, right
  *    for any). X fp16, fp32 or bf16 at any element's address and row stride; Y and residual fp16, for
  *    bf16 X bf16. Epilogues as in w4a4_gemm (residual is added to the fp32 sum; it may be Y itself, X may
- *    not overlap Y). No
- *    workspace; results do not depend on timing. Limits (W4A4_ERR_UNSUPPORTED above): N 2^24, K 2^23,
- *    N K 2^34, M 2^21, ldx 2^24.
+ *    not overlap Y). Scales must be finite. Every 16 rows read and widen the weights again: meant for up to
+ *    about 64 rows. No workspace; results do not depend on timing. Limits (W4A4_ERR_UNSUPPORTED above):
+ *    N 2^24, K 2^23, N K 2^34, M 2^21, ldx 2^24.
  * ------------------------------------------------------------------------------------------- */
 size_t w4a4_w4g_operand_bytes(int N, int K);
 int w4a4_pack_weights_w4g(const void *W, int w_dtype, int N, int K, int64_t ldw, int group,
@@ -441,10 +441,11 @@ int w4a4_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const u
  * visible page outside [0, num_pages), or lens[b] > table_width * page_size, makes that sequence's
  * output NaN and reads nothing outside the cache. What is not visible may hold anything; a visible value
  * that is infinite makes its channel infinite or NaN. max_len is the largest length the work is split for:
- * a longer sequence is still right, only slower. head_dim 64, 96, 128, 192 or 256 (else
- * W4A4_ERR_UNSUPPORTED), B up to 65535 and B * heads up to 2^23; out [B][heads][head_dim] with row
- * stride ldo. Results do not depend on timing. ws: w4a4_paged_attn_workspace_bytes(...) bytes of the
- * same sizes, 256-byte aligned.
+ * any value is right for any lengths, but a sequence that is longer, or far shorter, is slower than with its
+ * own length (2000 tokens of 32 heads over 8 of 128: 8.3 us, with a max_len of 131072 23.5 us). head_dim 64,
+ * 96, 128, 192 or 256 (else W4A4_ERR_UNSUPPORTED), B up to 65535 and B * heads up to 2^23; out [B][heads]
+ * [head_dim] with row stride ldo. Results do not depend on timing. ws: w4a4_paged_attn_workspace_bytes(...)
+ * bytes of the same sizes, 256-byte aligned.
  * ------------------------------------------------------------------------------------------- */
 int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
                       int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,

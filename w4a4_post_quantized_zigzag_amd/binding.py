@@ -573,7 +573,8 @@ def paged_attn_decode(q, k_cache, v_cache, table, lens, scale: float | None = No
                       sinks: int = 0, max_len: int | None = None, out=None, ws=None):
     """Attention of one new token per sequence, q [B, heads, D], over the first lens[b] tokens of the
     paged cache [pages, kv_heads, page_size, D] through table int32 [B, width]; lens int32 [B]. window >
-    0: only the last `window` and the first `sinks` tokens. scale defaults to D ** -0.5, max_len (what the
-    work is split for) to what the table holds. ws: a workspace of w4a4_paged_attn_workspace_bytes."""
+    0: only the last `window` and the first `sinks` tokens. scale defaults to D ** -0.5. max_len is what the
+    work is split for, by default what the table holds; any value is right, the longest length is fastest. ws: a
+    workspace of w4a4_paged_attn_workspace_bytes."""
     return (_native or _decode()).paged_attn(q, k_cache, v_cache, table, lens, scale, window, sinks, max_len,
                                              out, ws)

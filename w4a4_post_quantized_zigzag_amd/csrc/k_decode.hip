@@ -295,9 +295,10 @@ int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 //  - p is split in two 16-bit parts (p = hi + lo to 2^-16 or better), two products per tile.
 // Tiles of one sequence go in equal runs to `splits` workgroups and there round-robin to the waves (four,
 // one where there is little to do), joined in LDS and by k_attn_join in a fixed order.
-// Measured: 32 sequences of 0 to 8191 tokens, 32 heads over 8 of 128, 81 us (5.05 TB/s); two of 131071 and 87000
-// tokens 154 us (5.8 TB/s, part of it from the last-level cache); 64 with a window of 1000 and 16 heads of 64
-// 42.5 us (5.0 TB/s); one of 1001 tokens, one key/value head of 256, 9.6 us, the chain of two launches.
+// Measured (calls one after another): 32 sequences of 0 to 8191 tokens, 32 heads over 8 of 128, 81 us (5.05 TB/s);
+// two of 131071 and 87000 tokens 154 us (5.8 TB/s, part of it from the last-level cache); 64 with a window of 1000 and
+// 16 heads of 64 42.5 us (5.0 TB/s); one of 1001 tokens, one key/value head of 256, 9.6 us, the chain of two
+// launches.
 // ================================================================================================
 
 // Tiles of 32 keys that hold something visible: tiles [0, ns) and from w0 on, T in all.
@@ -614,19 +615,22 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
     }
 }
 
-// How many waves and workgroups share a sequence. The lengths are on the device; only max_len is known.
+// How many waves and workgroups share a sequence. The lengths are on the device; only max_len is known, and every
+// sequence is cut by it: a max_len far above the lengths leaves their tiles to few workgroups (one sequence of 2000
+// tokens, 32 heads over 8 of 128: 8.3 us, 23.5 with a max_len of 131072; 32 of 256 to 8191: 84 and 109). All
+// figures are us per call in a graph.
 //  - Short sequences get one workgroup of four waves each and no join, which costs 3 us: up to 8 tiles always
-//    (64, 128 and 256 tokens, 8 key/value heads of 128: 4.1, 4.7 and 6.0 us, split 6.9, 6.9 and 7.1; 384 tokens
-//    7.6 and 7.1), up to 32 where the rows alone fill the CUs (16 sequences of 1024 tokens, 8 heads: 13.7 us,
-//    split 17.1; 64 of 768: 39 and 45; 64 of 1 to 768: 23 and 26; but 4 of 1024: 13.2 and 10.5).
-//  - Else, with at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one
-//    tile per workgroup (1001 tokens, one key/value head of 256: 10.0 us, 10.4 us in workgroups of 4 waves).
-//  - With a window all sequences are about as long, and two sequences leave little to balance: few long
-//    runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 45.7 us with 1024 workgroups, 48.7
-//    us with 2048; 131071 and 87000 tokens, 8 heads: 163 us with 512, 173 us with 2048).
-//  - Otherwise the lengths differ, and the CUs stay evenly loaded with shorter ones (8 sequences of 1000 to
-//    32000 tokens, 8 heads: 99 us with 512, 89 us with 1024, 76 us with 2048; 32 of 256 to 8191: 113, 103
-//    and 82 us).
+//    (64, 128 and 256 tokens, 8 key/value heads of 128: 4.2, 4.7 and 6.1, split 7.0, 7.1 and 7.5; 384 tokens 7.7
+//    and 7.3), up to 32 where the rows alone fill the CUs (16 sequences of 1024 tokens, 8 heads: 13.7, split 16.7;
+//    64 of 768: 38 and 42; 64 of 1 to 768: 16.4 and 16.0; but 4 of 1024: 13.3 and 9.7).
+//  - Else, with at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one tile
+//    per workgroup (one key/value head of 256, eight heads: 600 and 1001 tokens 9.1 and 9.4, in workgroups of four
+//    waves 9.7 and 9.8; 4 sequences of 4 heads of 64 and 1275 tokens: 7.4 and 7.6).
+//  - With a window that hides something all sequences are about as long, and two sequences leave little to balance:
+//    few long runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 43.4 with 1024 workgroups, 47.0
+//    with 2048; 131071 and 87000 tokens, 8 heads: 163 with 512, 169 with 2048).
+//  - Otherwise the lengths differ, and the CUs stay evenly loaded with shorter ones (8 sequences of 1000 to 32000
+//    tokens, 8 heads: 99 with 512, 84 with 1024, 70 with 2048; 32 of 0 to 8191: 113, 100 and 82).
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks)
 {
     const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;

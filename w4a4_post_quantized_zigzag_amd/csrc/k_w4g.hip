@@ -13,7 +13,9 @@
 //  - The waves of a workgroup share one tile of 16 channels and split K; their partial sums meet in
 //    LDS in a fixed order, so results do not depend on timing.
 // Measured: one bf16 token, 2048x16384, group 64, 6.2 us and eight fp16 tokens, 16384x2048, group 128, 7.2 us, of
-// which 1.7 us are the launch and 2.1 us the bare reading of the 17 MB; 50 tokens, 1024x4099, group 32, 5.6 us.
+// which 1.7 us are the launch and 2.1 us the bare reading of the 17 MB from the last-level cache (in a graph over 24
+// weights, 430 MB, which that cache does not hold, a call takes 6.5 and 7.5 us, with three 6.8 and 7.9); 50 tokens,
+// 1024x4099, group 32, 5.6 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -353,8 +355,9 @@ __global__ __launch_bounds__(64 * MAXW) void k_gemv_w4g(const W4gArgs a)
     }
 }
 
-// Waves: enough of them to keep the memory busy, at most one per step (16384x2048 with eight tokens: 11.4 us
-// with 1024 waves in all, 7.8 with 2048, 7.5 from 3000 on).
+// Waves: enough of them to keep the memory busy, at most one per step. They double until the grid has 3000 in all
+// (16384x2048, fp16, eight tokens: 19.2 us with 512, 11.6 with 1024, 8.3 with 2048, 7.7 with 4096; four tokens: 18.9,
+// 11.4, 8.1 and 6.8).
 template <int DT, int F, int Q, int GS, int TN>
 static int run_gemv(W4gArgs a, hipStream_t s)
 {

@@ -105,9 +105,10 @@ class Attention:
 
 class PagedCache:
     """Keys and values of `batch` sequences in pages shared by all of them, one pair of arrays per
-    layer. advance() makes room for one new token per sequence and sets the device tensors that run()
-    reads (table, lens, slots, positions) in place, so a captured run() can be replayed after it. Page
-    bookkeeping is on the host."""
+    layer, fp16. advance() makes room for one new token per sequence and sets the device tensors that run()
+    reads (table, lens, slots, positions) in place, so a captured run() can be replayed after it; its four
+    copies wait for the stream. Page bookkeeping is on the host. max_len is the longest that a sequence may
+    get, and what run() splits its attention for: the closer to the real lengths, the faster."""
 
     def __init__(self, layers: int, attention: Attention, batch: int, pages: int, page_size: int = 16,
                  max_len: int | None = None):
@@ -536,7 +537,8 @@ class DeviceStack:
     def calibrate(self, X_calib_per_step):
         """X_calib_per_step[t]: list of fp16 numpy arrays [rows, h] (calibration draws of step t)."""
         if self.attention is not None:
-            raise ValueError("tables of a stack with attention are set with set_tables")
+            raise ValueError("tables of a stack with attention are set with set_tables, or step by step with "
+                             "run(calib=True, cache=)")
         torch = _torch()
         for t, draws in enumerate(X_calib_per_step):
             X = torch.from_numpy(np.ascontiguousarray(np.concatenate(draws, axis=0))).cuda()
