@@ -27,12 +27,13 @@ def test_split_and_joined(H, KV, D, dtype):
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("D", DIMS)
 def test_most_splits(D, dtype):
-    """256 tiles in as many one-wave workgroups, beyond what the join loads ahead; 300 tiles in four-wave ones; and
-    a hint of 256 tiles for a longer sequence, whose last split takes what is left."""
-    b = Batch([8190], 2, 1, D, 32, dtype, seed=D)
-    b.check(b.run())
-    b = Batch([9577], 2, 1, D, 32, dtype, seed=D + 1)
-    for max_len in (9577, 8192, 1 << 20):
+    """One wave on a tile in as many workgroups as one sequence gets, four waves in as many as there are splits,
+    beyond what the join loads ahead; and hints below the length, whose last split takes what is left."""
+    b = Batch([3050], 2, 1, D, 32, dtype, seed=D)
+    for max_len in (3050, 2900):
+        b.check(b.run(max_len=max_len))
+    b = Batch([33001], 2, 1, D, 32, dtype, seed=D + 1)
+    for max_len in (33001, 30000, 8192, 1 << 20):
         b.check(b.run(max_len=max_len))
 
 

@@ -623,9 +623,12 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_attn_join(cons
 //    (64, 128 and 256 tokens, 8 key/value heads of 128: 4.2, 4.7 and 6.1, split 7.0, 7.1 and 7.5; 384 tokens 7.7
 //    and 7.3), up to 32 where the rows alone fill the CUs (16 sequences of 1024 tokens, 8 heads: 13.7, split 16.7;
 //    64 of 768: 38 and 42; 64 of 1 to 768: 16.4 and 16.0; but 4 of 1024: 13.3 and 9.7).
-//  - Else, with at most 1024 tiles in all there are CUs left, and only the latency counts: one wave and one tile
-//    per workgroup (one key/value head of 256, eight heads: 600 and 1001 tokens 9.1 and 9.4, in workgroups of four
-//    waves 9.7 and 9.8; 4 sequences of 4 heads of 64 and 1275 tokens: 7.4 and 7.6).
+//  - Else, with at most 512 tiles in all and 96 of one sequence there are CUs left, and only the latency counts: one
+//    wave and one tile per workgroup. With more the join of so many parts costs more than the shorter chains save.
+//    One and four waves, one sequence with one key/value head of 256, eight heads: 1001 tokens 9.4 and 9.8, 3067:
+//    11.2 and 10.0, 8000: 15.6 and 11.4; one head of 64: 6.8 and 7.3, 6.8 and 7.2, 7.8 and 7.3. 16 rows of one head
+//    of 128, 507 tokens: 7.4 and 8.2, 1019: 7.8 and 8.4, 2043: 10.4 and 10.1; of eight heads: 8.2 and 8.5, 9.4 and
+//    8.8, 12.3 and 10.4.
 //  - With a window that hides something all sequences are about as long, and two sequences leave little to balance:
 //    few long runs read fastest (64 sequences of 16 heads and 1004 visible tokens: 43.4 with 1024 workgroups, 47.0
 //    with 2048; 131071 and 87000 tokens, 8 heads: 163 with 512, 169 with 2048).
@@ -642,7 +645,7 @@ AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int 
     const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
     if (tiles <= std::clamp<int64_t>(rows / 4, 8, 32)) return {1, (int)tiles, ATTN_WAVES};
     AttnPlan p;
-    p.waves = rows * tiles <= 1024 && tiles <= ATTN_MAX_SPLITS ? 1 : ATTN_WAVES;
+    p.waves = rows * tiles <= 512 && tiles <= 96 ? 1 : ATTN_WAVES;
     int64_t want = tiles;
     if (p.waves > 1) {
         const int workgroups = window > 0 ? 1024 : B <= 2 ? 512 : 2048;
