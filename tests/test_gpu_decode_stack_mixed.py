@@ -132,3 +132,22 @@ def test_graph_replayed_over_tokens():
         got = captured.clone()
         assert torch.equal(got, ds.run(X, 2, cache=caches[1])), t
         torch.cuda.synchronize()
+
+
+def test_weights_and_norms_already_on_the_device():
+    """Device tensors in place of numpy arrays, the norms in any float type and stride: the same stack."""
+    import torch
+    W = weights(A, 384, 512, 1, seed=8)
+    for n in ("q_norm", "k_norm"):
+        W[0][n] = W[0][n].astype(np.float16).astype(np.float32)
+    there = {n: dev(w) for n, w in W[0].items()}
+    there["q_norm"] = there["q_norm"].half()
+    there["k_norm"] = torch.stack((there["k_norm"], there["k_norm"]), 1)[:, 0]
+    X = dev(np.random.default_rng(9).standard_normal((2, 384)).astype(np.float16))
+    outs = []
+    for w in (W, [there]):
+        ds = DeviceStack(w, BLOCK, 1, w4g=LINEARS, group=GROUP, attention=A)
+        cache = PagedCache(1, A, 2, pages=2)
+        cache.advance()
+        outs.append(ds.run(X, 0, cache=cache).clone())
+    assert torch.equal(*outs)

@@ -351,7 +351,8 @@ class DeviceStack:
                 if (lw["qkv"].shape[0], lw["o"].shape[1]) != want:
                     raise ValueError(f"qkv rows and o columns must be {want} for {A}")
             self.inv_freq = A.inv_freq()
-            norm = lambda lw, n: (torch.as_tensor(np.asarray(lw[n], np.float32)).cuda()  # noqa: E731
+            norm = lambda lw, n: (torch.as_tensor(lw[n], dtype=torch.float32, device="cuda")  # noqa: E731
+                                  .clone(memory_format=torch.contiguous_format)
                                   if lw.get(n) is not None else None)
             self.norms = [(norm(lw, "q_norm"), norm(lw, "k_norm")) for lw in weights]
         self.layers = []
