@@ -495,6 +495,8 @@ class DeviceStack:
             raise ValueError("a cache goes with attention, and attention needs one")
         if cache is not None and cache.batch != X.shape[0]:
             raise ValueError(f"{X.shape[0]} rows for a cache of {cache.batch} sequences")
+        if cache is not None and len(cache.k) < len(self.layers):
+            raise ValueError(f"a cache of {len(cache.k)} layers for a stack of {len(self.layers)}")
         if codes is not None and self.plain:
             raise ValueError("codes are recorded by fully quantized stacks only")
         bufs = self.bufs(X.shape[0])
