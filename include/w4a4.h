@@ -63,6 +63,9 @@ enum w4a4_status {
 
 enum w4a4_dtype { W4A4_F16 = 0, W4A4_F32 = 1, W4A4_BF16 = 2 };
 
+/* What a key-value cache holds (the single-token calls at the end). */
+enum w4a4_kv_format { W4A4_KV_16BIT = 0, W4A4_KV_INT8 = 1, W4A4_KV_FP4 = 2 };
+
 enum w4a4_epilogue {
     W4A4_EPI_NONE = 0,     /* Y = fp16(dequant) */
     W4A4_EPI_GELU = 1,     /* Y = fp16(gelu_erf(dequant)), GELU evaluated in fp32 */
@@ -462,6 +465,91 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
                            int64_t ldt, const int32_t *lens, int max_len, float scale, int window,
                            int sinks, void *out, int64_t ldo, void *ws, size_t ws_bytes,
                            hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Quantized key-value cache: what grows with batch and length, held in 8 or 4 bits [vnrobo.com "Vi sao W4A4 kho
+ * hon W4A16?": the memory of the deployed model is the point]. kv_format says how a row (one token's key or value of
+ * one head, D = head_dim channels: 64, 96, 128, 192 or 256) is held:
+ *  - W4A4_KV_INT8: codes int8, c = rint(fp32(x * fp32(127 / m))), and one fp32 scale s = fp32(m / 127), with
+ *    m = max(max|x|, 2^-100). It stands for c * s.
+ *  - W4A4_KV_FP4 (the OCP Microscaling E2M1 format): per 32 channels a scale 2^e, held as the byte e + 127, with the
+ *    smallest e that has 6 * 2^e >= max|x|, kept in [-23, 13] for fp16 and [-100, 125] for bf16 so that every value
+ *    is exact and finite in the element type; codes 0..7 are 0, .5, 1, 1.5, 2, 3, 4, 6, the fourth bit is the sign,
+ *    x / 2^e is rounded to the nearest (half to the even code) and at most 6. Two codes per byte, the even channel
+ *    low. Byte 255 is NaN.
+ * A row (fp4: its 32 channels) that holds an infinity or a NaN is stored as NaN.
+ * Arrays (keys and values each): codes int8 [kv_heads][page_size][D], or uint8 [kv_heads][page_size][D / 2], page p at
+ * p * page_stride elements; scales fp32 [kv_heads][page_size], or uint8 [kv_heads][D / 32][page_size], page p at p *
+ * scale_stride elements. Bases and pages start at multiples of 16 bytes (W4A4_ERR_ALIGN). Pages, slots, tables and
+ * limits as for the 16-bit cache above.
+ *
+ * w4a4_qk_norm_rope_quant: w4a4_qk_norm_rope with the append into such a cache (required here). Keys are rounded to
+ * `dtype` first, so that the cache holds what w4a4_kv_append_quant makes of k_out and v, bit for bit.
+ * w4a4_kv_append_quant: rows k and v [M][kv_heads][D] as they are.
+ * w4a4_kv_read_quant: slots back to rows of `dtype`, one rounding of c * s; a slot outside the cache gives zeros.
+ * k_out or v_out may be NULL. (fp4 written as bf16 and read as fp16 may leave fp16's range.)
+ * w4a4_paged_attn_decode_quant: w4a4_paged_attn_decode over such a cache: the values above in the same formula, sums in
+ * fp32, nothing rounded before the end but the weights p (to two 16-bit parts, 2^-17 of each). Workspace:
+ * w4a4_paged_attn_quant_workspace_bytes. What is not visible may hold anything, scales included.
+ *
+ * w4a4_paged_attn_shared: the attention of one new token per sequence for a batch whose sequences all begin with the
+ * same tokens. Sequence b sees the prefix_len[0] tokens of the pages in prefix_table[prefix_width], and after them the
+ * lens[b] tokens of its own table row (lens[b] <= 0: none). The prefix's keys and values are read once for all
+ * sequences. Over a cache of any format; for W4A4_KV_16BIT k and v hold `dtype`, page_stride counts its elements and
+ * the scales are ignored. prefix_len is on the device, so that a captured call follows it; max_prefix and max_len are
+ * what the work is split for: any value is right. A bad page of the prefix, or a prefix_len beyond its table, makes
+ * every output NaN. No window. Workspace: w4a4_paged_attn_shared_workspace_bytes of the same sizes.
+ * ------------------------------------------------------------------------------------------- */
+int w4a4_qk_norm_rope_quant(const void *q, const void *k, const void *v, int dtype, int M, int heads,
+                            int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
+                            const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
+                            int rot_dim, int interleaved, const int64_t *positions, void *q_out,
+                            int64_t ldqo, void *k_out, int64_t ldko, int kv_format, void *k_codes, void *v_codes,
+                            void *k_scale, void *v_scale, int num_pages, int page_size, int64_t page_stride,
+                            int64_t scale_stride, const int64_t *slots, hipStream_t stream);
+int w4a4_kv_append_quant(const void *k, const void *v, int dtype, int M, int kv_heads, int head_dim, int64_t ldk,
+                         int64_t ldv, int kv_format, void *k_codes, void *v_codes, void *k_scale, void *v_scale,
+                         int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                         const int64_t *slots, hipStream_t stream);
+int w4a4_kv_read_quant(int kv_format, const void *k_codes, const void *v_codes, const void *k_scale,
+                       const void *v_scale, int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                       const int64_t *slots, int M, int kv_heads, int head_dim, int dtype, void *k_out, int64_t ldk,
+                       void *v_out, int64_t ldv, hipStream_t stream);
+size_t w4a4_paged_attn_quant_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_len, int window,
+                                             int sinks);
+int w4a4_paged_attn_decode_quant(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim, int64_t ldq,
+                                 int kv_format, const void *k_codes, const void *v_codes, const void *k_scale,
+                                 const void *v_scale, int num_pages, int page_size, int64_t page_stride,
+                                 int64_t scale_stride, const int32_t *table, int table_width, int64_t ldt,
+                                 const int32_t *lens, int max_len, float scale, int window, int sinks, void *out,
+                                 int64_t ldo, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t w4a4_paged_attn_shared_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_prefix,
+                                              int max_len);
+int w4a4_paged_attn_shared(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim, int64_t ldq,
+                           int kv_format, const void *k, const void *v, const void *k_scale, const void *v_scale,
+                           int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                           const int32_t *prefix_table, int prefix_width, const int32_t *prefix_len, int max_prefix,
+                           const int32_t *table, int table_width, int64_t ldt, const int32_t *lens, int max_len,
+                           float scale, void *out, int64_t ldo, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection [vnrobo.com "Build DiT action head pack": --svd-rank
+ * names a low-rank branch beside the quantized weight]. Row m takes adapter a = ids[m]:
+ *   out[m] = epilogue(Y[m] + scale[a] * (X[m] A_a^T) B_a^T)
+ * with A [n][R][K] and B [n][N][R] dense inside an adapter, adapters stride_a / stride_b elements apart, scale fp32 [n]
+ * (NULL: ones). A row whose id is outside [0, n) has no adapter and gets epilogue(Y[m]). X, A, B, Y, residual and out
+ * are all of `dtype` (fp16 or bf16), at any element's address and row stride; Y is the shared projection's output
+ * (with no epilogue of its own), out may be Y. Epilogues as in w4a4_gemm, after the sum. The inner products are fp32
+ * and enter the second product as two 16-bit parts (2^-17 of each is dropped), sums are fp32, one rounding at the end.
+ * Rows are independent of each other: another row's adapter, whatever it holds, does not touch them. K and R multiples
+ * of 8 (W4A4_ERR_SHAPE), R up to 256, M up to 2^25, K up to 2^23, N up to 2^24 (W4A4_ERR_UNSUPPORTED). X may not
+ * overlap out. ws: w4a4_adapter_workspace_bytes(M, K, R) bytes, 256-byte aligned. Results do not depend on timing.
+ * ------------------------------------------------------------------------------------------- */
+size_t w4a4_adapter_workspace_bytes(int M, int K, int R);
+int w4a4_adapter_add(const void *X, int dtype, int M, int K, int64_t ldx, const void *A, int64_t stride_a, const void *B,
+                     int64_t stride_b, int n, int R, const int32_t *ids, const float *scale, int N, const void *Y,
+                     int64_t ldy, int epilogue, const void *residual, int64_t ldr, void *out, int64_t ldo, void *ws,
+                     size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Diagnostics (host only).

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libw4a4.so")
@@ -15,6 +16,7 @@ W4A4_OK, W4A4_ERR_ARG, W4A4_ERR_SHAPE, W4A4_ERR_STEP_RANGE = 0, 1, 2, 3
 W4A4_ERR_UNSUPPORTED, W4A4_ERR_ALIGN, W4A4_ERR_WORKSPACE, W4A4_ERR_HIP = 4, 5, 6, 7
 W4A4_F16, W4A4_F32, W4A4_BF16 = 0, 1, 2
 EPI_NONE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
+KV_16BIT, KV_INT8, KV_FP4 = 0, 1, 2
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -83,6 +85,24 @@ SIGNATURES = {
     "w4a4_paged_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "w4a4_paged_attn_decode": (_i, [_vp, _i, _i, _i, _i, _i, _i64, _vp, _vp, _i, _i, _i64, _vp, _i,
                                     _i64, _vp, _i, ctypes.c_float, _i, _i, _vp, _i64, _vp, _sz, _vp]),
+    "w4a4_qk_norm_rope_quant": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i64, _i64, _i64, _vp, _vp,
+                                     ctypes.c_float, _vp, _i, _i, _vp, _vp, _i64, _vp, _i64, _i, _vp, _vp, _vp,
+                                     _vp, _i, _i, _i64, _i64, _vp, _vp]),
+    "w4a4_kv_append_quant": (_i, [_vp, _vp, _i, _i, _i, _i, _i64, _i64, _i, _vp, _vp, _vp, _vp, _i, _i, _i64,
+                                  _i64, _vp, _vp]),
+    "w4a4_kv_read_quant": (_i, [_i, _vp, _vp, _vp, _vp, _i, _i, _i64, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _vp,
+                                _i64, _vp]),
+    "w4a4_paged_attn_quant_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "w4a4_paged_attn_decode_quant": (_i, [_vp, _i, _i, _i, _i, _i, _i64, _i, _vp, _vp, _vp, _vp, _i, _i, _i64,
+                                          _i64, _vp, _i, _i64, _vp, _i, ctypes.c_float, _i, _i, _vp, _i64, _vp,
+                                          _sz, _vp]),
+    "w4a4_paged_attn_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "w4a4_paged_attn_shared": (_i, [_vp, _i, _i, _i, _i, _i, _i64, _i, _vp, _vp, _vp, _vp, _i, _i, _i64, _i64,
+                                    _vp, _i, _vp, _i, _vp, _i, _i64, _vp, _i, ctypes.c_float, _vp, _i64, _vp,
+                                    _sz, _vp]),
+    "w4a4_adapter_workspace_bytes": (_sz, [_i, _i, _i]),
+    "w4a4_adapter_add": (_i, [_vp, _i, _i, _i, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp, _vp, _i, _vp, _i64, _i,
+                              _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
     "w4a4_last_error": (ctypes.c_char_p, []),
     "w4a4_status_string": (ctypes.c_char_p, [_i]),
     "w4a4_abi_version": (_i, []),
@@ -578,3 +598,82 @@ def paged_attn_decode(q, k_cache, v_cache, table, lens, scale: float | None = No
     workspace of w4a4_paged_attn_workspace_bytes."""
     return (_native or _decode()).paged_attn(q, k_cache, v_cache, table, lens, scale, window, sinks, max_len,
                                              out, ws)
+
+
+class QuantPages(NamedTuple):
+    """A quantized key-value cache. kind "int8": codes int8 [pages, kv_heads, page_size, D], scales fp32
+    [pages, kv_heads, page_size]; "fp4": two codes per byte, uint8 [.., D / 2], scales uint8 [pages, kv_heads,
+    D / 32, page_size]. Any tuple of four such tensors will do where one is asked for."""
+    k: object
+    v: object
+    k_scale: object
+    v_scale: object
+
+
+def quant_pages(pages: int, kv_heads: int, page_size: int, head_dim: int, kind: str, device="cuda") -> QuantPages:
+    """An empty QuantPages (all zeros)."""
+    torch = _torch()
+    if kind not in ("int8", "fp4"):
+        raise ValueError(f"kind must be int8 or fp4, not {kind!r}")
+    fp4 = kind == "fp4"
+    if fp4 and head_dim % 32:
+        raise ValueError(f"head_dim {head_dim} is not a multiple of 32")
+    shapes = [((pages, kv_heads, page_size, head_dim // 2), torch.uint8),
+              ((pages, kv_heads, head_dim // 32, page_size), torch.uint8)] if fp4 else [
+        ((pages, kv_heads, page_size, head_dim), torch.int8), ((pages, kv_heads, page_size), torch.float32)]
+    (c, cdt), (s, sdt) = shapes
+    e = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
+    return QuantPages(e(c, cdt), e(c, cdt), e(s, sdt), e(s, sdt))
+
+
+def qk_norm_rope_append_quant(q, k, v, q_weight, k_weight, inv_freq, positions, cache, slots, eps: float = 1e-6,
+                              interleaved: bool = False, q_out=None, k_out=None):
+    """qk_norm_rope_append into a quantized cache (QuantPages): it then holds what kv_append_quant makes of the
+    16-bit keys and values. Returns q_out."""
+    return (_native or _decode()).norm_rope_quant(q, k, v, q_weight, k_weight, inv_freq, positions, eps,
+                                                  interleaved, q_out, k_out, cache, slots)
+
+
+def kv_append_quant(k, v, cache, slots):
+    """Rows k, v [M, kv_heads, D] as they are into slots int64 [M] of a quantized cache (-1: skipped)."""
+    (_native or _decode()).kv_append(k, v, cache, slots)
+
+
+def kv_read_quant(cache, slots, dtype=None, k_out=None, v_out=None):
+    """The rows at slots int64 [M] of a quantized cache as 16-bit rows (k, v), each [M, kv_heads, D]; zeros for a
+    slot outside it. dtype: fp16 unless k_out or v_out say otherwise."""
+    torch = _torch()
+    if k_out is None or v_out is None:
+        given = k_out if k_out is not None else v_out
+        codes = cache[0]
+        D = codes.shape[-1] * (2 if codes.dtype == torch.uint8 else 1)
+        dt = given.dtype if given is not None else dtype or torch.float16
+        e = lambda: torch.empty((slots.shape[0], codes.shape[1], D), dtype=dt, device=codes.device)  # noqa: E731
+        k_out, v_out = e() if k_out is None else k_out, e() if v_out is None else v_out
+    (_native or _decode()).kv_read(cache, slots, k_out, v_out)
+    return k_out, v_out
+
+
+def paged_attn_decode_quant(q, cache, table, lens, scale: float | None = None, window: int = 0, sinks: int = 0,
+                            max_len: int | None = None, out=None, ws=None):
+    """paged_attn_decode over a quantized cache (QuantPages). ws: w4a4_paged_attn_quant_workspace_bytes."""
+    return (_native or _decode()).attn_quant(q, cache, table, lens, scale, window, sinks, max_len, out, ws)
+
+
+def paged_attn_shared(q, cache, prefix_table, prefix_len, table, lens, scale: float | None = None,
+                      max_prefix: int | None = None, max_len: int | None = None, out=None, ws=None):
+    """Attention of one new token per sequence, q [B, heads, D], for sequences that all begin with the
+    prefix_len[0] tokens (int32 [1], on the device) of the pages in prefix_table int32 [width] and go on with the
+    lens[b] tokens of their own table row. cache: QuantPages, or (k_cache, v_cache) of 16 bits. The prefix is read
+    once for all sequences. max_prefix and max_len are what the work is split for, by default what the tables
+    hold. ws: w4a4_paged_attn_shared_workspace_bytes."""
+    return (_native or _decode()).attn_shared(q, cache, prefix_table, prefix_len, table, lens, scale, max_prefix,
+                                              max_len, out, ws)
+
+
+def adapter_add(Y, X, A, B, ids, scale=None, epilogue: int = EPI_NONE, residual=None, out=None, ws=None):
+    """out[m] = epilogue(Y[m] + scale[a] (X[m] A[a]^T) B[a]^T), a = ids[m]: low-rank adapters A [n, R, K], B [n, N,
+    R] of many requests beside the shared projection that made Y [M, N] (without an epilogue of its own). ids int32
+    [M]; a row whose id is outside [0, n) gets epilogue(Y[m]). scale fp32 [n] or None. All of one 16-bit dtype. out
+    may be Y. ws: w4a4_adapter_workspace_bytes."""
+    return (_native or _decode()).adapter_add(Y, X, A, B, ids, scale, epilogue, residual, out, ws)

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a4.so")
 SOURCES = ["abi.hip", "k_pack.hip", "k_act.hip", "k_gemm.hip", "k_calib.hip", "k_gptq.hip",
-           "k_w4g.hip", "k_decode.hip"]
+           "k_w4g.hip", "k_decode.hip", "k_kvq.hip", "k_adapter.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Device code is built without packed-fp32 instructions (v_pk_*_f32); every unit is gfx950-only.
@@ -25,7 +25,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
 # Per-unit extras: the activation kernels keep MFMA accumulators in ordinary VGPRs (their results
 # feed VALU work right away, so the accumulation-register form would only add copies).
 EXTRA_FLAGS = {"k_act.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "k_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "k_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "k_kvq.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

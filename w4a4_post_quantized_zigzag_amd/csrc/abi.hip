@@ -1127,13 +1127,11 @@ static int check_rows16(const void *p, int M, int64_t ld, int64_t width, const c
     return W4A4_OK;
 }
 
-int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
-                      int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
-                      const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
-                      int rot_dim, int interleaved, const int64_t *positions, void *q_out,
-                      int64_t ldqo, void *k_out, int64_t ldko, void *k_cache, void *v_cache,
-                      int num_pages, int page_size, int64_t page_stride, const int64_t *slots,
-                      hipStream_t stream)
+// what both forms of the call check, but for the cache
+static int check_norm_rope(const void *q, const void *k, int dtype, int M, int heads, int kv_heads, int head_dim,
+                           int64_t ldq, int64_t ldk, const float *q_weight, const float *k_weight, float eps,
+                           const double *inv_freq, int rot_dim, const int64_t *positions, const void *q_out,
+                           int64_t ldqo, const void *k_out, int64_t ldko, const int64_t *slots)
 {
     int rc;
     if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim))) return rc;
@@ -1148,20 +1146,35 @@ int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, in
     if ((rc = check_rows16(q, M, ldq, wq, "q")) || (rc = check_rows16(k, M, ldk, wk, "k")) ||
         (rc = check_rows16(q_out, M, ldqo, wq, "q_out")))
         return rc;
-    const bool cache = k_cache || v_cache;
-    if (M > 0 && !cache && !k_out) return fail(W4A4_ERR_ARG, "keys need k_out or a cache");
     if (k_out && (rc = check_rows16(k_out, M, ldko, wk, "k_out"))) return rc;
-    if (cache) {
-        if ((rc = check_cache(k_cache, v_cache, kv_heads, head_dim, num_pages, page_size, page_stride)) ||
-            (rc = check_rows16(v, M, ldv, wk, "v")))
-            return rc;
-        if (M > 0 && !slots) return fail(W4A4_ERR_ARG, "slots is NULL");
-    }
     if (M > 0 && rot_dim > 0 && (!inv_freq || !positions))
         return fail(W4A4_ERR_ARG, "inv_freq and positions are required for rot_dim %d", rot_dim);
     if (!aligned(inv_freq, 8) || !aligned(positions, 8) || !aligned(slots, 8) || !aligned(q_weight, 4) ||
         !aligned(k_weight, 4))
         return fail(W4A4_ERR_ALIGN, "inv_freq / positions / slots / weights misaligned");
+    return W4A4_OK;
+}
+
+int w4a4_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int M, int heads,
+                      int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
+                      const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
+                      int rot_dim, int interleaved, const int64_t *positions, void *q_out,
+                      int64_t ldqo, void *k_out, int64_t ldko, void *k_cache, void *v_cache,
+                      int num_pages, int page_size, int64_t page_stride, const int64_t *slots,
+                      hipStream_t stream)
+{
+    int rc;
+    if ((rc = check_norm_rope(q, k, dtype, M, heads, kv_heads, head_dim, ldq, ldk, q_weight, k_weight, eps, inv_freq,
+                              rot_dim, positions, q_out, ldqo, k_out, ldko, slots)))
+        return rc;
+    const bool cache = k_cache || v_cache;
+    if (M > 0 && !cache && !k_out) return fail(W4A4_ERR_ARG, "keys need k_out or a cache");
+    if (cache) {
+        if ((rc = check_cache(k_cache, v_cache, kv_heads, head_dim, num_pages, page_size, page_stride)) ||
+            (rc = check_rows16(v, M, ldv, (int64_t)kv_heads * head_dim, "v")))
+            return rc;
+        if (M > 0 && !slots) return fail(W4A4_ERR_ARG, "slots is NULL");
+    }
     if (M == 0) return ok();
     NormRopeArgs a{};
     a.q = (const uint16_t *)q;
@@ -1277,6 +1290,345 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
             align_up((size_t)B * heads * plan.splits * sizeof(float2), 256));
     }
     if ((rc = launch_paged_attn(a, dtype, head_dim, stream))) return rc;
+    return ok();
+}
+
+// ------------------------------------------------------------------ quantized cache, shared prefix
+
+// The cache in any format: 16-bit ones as check_cache has them, the others with their scales. `kv` is filled in.
+static int check_kv(int format, const void *k, const void *v, const void *k_scale, const void *v_scale, int kv_heads,
+                    int head_dim, int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                    bool sixteen, KvPages *kv)
+{
+    int rc;
+    if (format != W4A4_KV_INT8 && format != W4A4_KV_FP4 && !(sixteen && format == W4A4_KV_16BIT))
+        return fail(W4A4_ERR_ARG, "cache format %d unknown here", format);
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+        return fail(W4A4_ERR_UNSUPPORTED, "head_dim %d is not 64, 96, 128, 192 or 256", head_dim);
+    // rows of 16-bit elements, of int8 codes, of bytes with two fp4 codes
+    const int row = format == W4A4_KV_FP4 ? head_dim / 2 : head_dim;
+    if ((rc = check_cache(k, v, kv_heads, row, num_pages, page_size, page_stride))) return rc;
+    if (format != W4A4_KV_16BIT) {
+        if (page_stride % 16) return fail(W4A4_ERR_ALIGN, "cache pages must be 16-byte aligned");
+        if (!k_scale || !v_scale) return fail(W4A4_ERR_ARG, "k_scale and v_scale are required");
+        const int64_t page = (int64_t)kv_heads * page_size * (format == W4A4_KV_FP4 ? head_dim / 32 : 1);
+        if (scale_stride < page)
+            return fail(W4A4_ERR_SHAPE, "scale_stride %lld < %lld", (long long)scale_stride, (long long)page);
+        if ((int64_t)num_pages > (((int64_t)1 << 44) / scale_stride))
+            return fail(W4A4_ERR_UNSUPPORTED, "scales above 2^44 elements");
+        if (!aligned(k_scale, 16) || !aligned(v_scale, 16) || scale_stride % (format == W4A4_KV_FP4 ? 16 : 4))
+            return fail(W4A4_ERR_ALIGN, "a page's scales must be 16-byte aligned");
+    }
+    *kv = KvPages{(uint8_t *)k, (uint8_t *)v, (void *)k_scale, (void *)v_scale,
+                  page_stride * (format == W4A4_KV_16BIT ? 2 : 1), scale_stride, format, num_pages, page_size,
+                  __builtin_ctz((unsigned)page_size)};
+    return W4A4_OK;
+}
+
+int w4a4_qk_norm_rope_quant(const void *q, const void *k, const void *v, int dtype, int M, int heads,
+                            int kv_heads, int head_dim, int64_t ldq, int64_t ldk, int64_t ldv,
+                            const float *q_weight, const float *k_weight, float eps, const double *inv_freq,
+                            int rot_dim, int interleaved, const int64_t *positions, void *q_out,
+                            int64_t ldqo, void *k_out, int64_t ldko, int kv_format, void *k_codes, void *v_codes,
+                            void *k_scale, void *v_scale, int num_pages, int page_size, int64_t page_stride,
+                            int64_t scale_stride, const int64_t *slots, hipStream_t stream)
+{
+    int rc;
+    NormRopeArgs a{};
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim)) ||
+        (rc = check_kv(kv_format, k_codes, v_codes, k_scale, v_scale, kv_heads, head_dim, num_pages, page_size,
+                       page_stride, scale_stride, false, &a.kv)) ||
+        (rc = check_norm_rope(q, k, dtype, M, heads, kv_heads, head_dim, ldq, ldk, q_weight, k_weight, eps, inv_freq,
+                              rot_dim, positions, q_out, ldqo, k_out, ldko, slots)) ||
+        (rc = check_rows16(v, M, ldv, (int64_t)kv_heads * head_dim, "v")))
+        return rc;
+    if (M > 0 && !slots) return fail(W4A4_ERR_ARG, "slots is NULL");
+    if (M == 0) return ok();
+    a.q = (const uint16_t *)q;
+    a.k = (const uint16_t *)k;
+    a.v = (const uint16_t *)v;
+    a.M = M;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.D = head_dim;
+    a.rot = rot_dim;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    a.q_out = (uint16_t *)q_out;
+    a.k_out = (uint16_t *)k_out;
+    a.ldqo = ldqo;
+    a.ldko = ldko;
+    a.slots = slots;
+    if ((rc = launch_norm_rope(a, dtype, interleaved != 0, stream))) return rc;
+    return ok();
+}
+
+static int kv_rows(bool read, void *k, void *v, int dtype, int M, int kv_heads, int head_dim, int64_t ldk, int64_t ldv,
+                   int kv_format, void *k_codes, void *v_codes, void *k_scale, void *v_scale, int num_pages,
+                   int page_size, int64_t page_stride, int64_t scale_stride, const int64_t *slots, hipStream_t stream)
+{
+    int rc;
+    KvRowsArgs a{};
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(kv_heads, kv_heads, head_dim))) return rc;
+    if (M < 0) return fail(W4A4_ERR_ARG, "M = %d negative", M);
+    if (M > (1 << 25)) return fail(W4A4_ERR_UNSUPPORTED, "M = %d above 2^25", M);
+    const int64_t width = (int64_t)kv_heads * head_dim;
+    if ((rc = check_kv(kv_format, k_codes, v_codes, k_scale, v_scale, kv_heads, head_dim, num_pages, page_size,
+                       page_stride, scale_stride, false, &a.kv)))
+        return rc;
+    if (read && M > 0 && !k && !v) return fail(W4A4_ERR_ARG, "k_out or v_out is required");
+    if (((k || !read) && (rc = check_rows16(k, M, ldk, width, "k"))) ||
+        ((v || !read) && (rc = check_rows16(v, M, ldv, width, "v"))))
+        return rc;
+    if (M > 0 && !slots) return fail(W4A4_ERR_ARG, "slots is NULL");
+    if (!aligned(slots, 8)) return fail(W4A4_ERR_ALIGN, "slots misaligned");
+    if (M == 0) return ok();
+    a.k = (uint16_t *)k;
+    a.v = (uint16_t *)v;
+    a.M = M;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.kv_heads = kv_heads;
+    a.D = head_dim;
+    a.slots = slots;
+    if ((rc = read ? launch_kv_read(a, dtype, stream) : launch_kv_append(a, dtype, stream))) return rc;
+    return ok();
+}
+
+int w4a4_kv_append_quant(const void *k, const void *v, int dtype, int M, int kv_heads, int head_dim, int64_t ldk,
+                         int64_t ldv, int kv_format, void *k_codes, void *v_codes, void *k_scale, void *v_scale,
+                         int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                         const int64_t *slots, hipStream_t stream)
+{
+    return kv_rows(false, (void *)k, (void *)v, dtype, M, kv_heads, head_dim, ldk, ldv, kv_format, k_codes, v_codes,
+                   k_scale, v_scale, num_pages, page_size, page_stride, scale_stride, slots, stream);
+}
+
+int w4a4_kv_read_quant(int kv_format, const void *k_codes, const void *v_codes, const void *k_scale,
+                       const void *v_scale, int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                       const int64_t *slots, int M, int kv_heads, int head_dim, int dtype, void *k_out, int64_t ldk,
+                       void *v_out, int64_t ldv, hipStream_t stream)
+{
+    return kv_rows(true, k_out, v_out, dtype, M, kv_heads, head_dim, ldk, ldv, kv_format, (void *)k_codes,
+                   (void *)v_codes, (void *)k_scale, (void *)v_scale, num_pages, page_size, page_stride, scale_stride,
+                   slots, stream);
+}
+
+// How the calls over any format and behind a prefix are cut, and their workspace
+struct KvAttnPlan {
+    AttnPlan own;
+    PrefixPlan prefix;  // splits 0: none
+    size_t stat_bytes, ws_bytes;
+};
+
+static KvAttnPlan kv_attn_plan(int B, int heads, int kv_heads, int head_dim, bool shared, int max_prefix, int max_len,
+                               int window, int sinks)
+{
+    KvAttnPlan p{};
+    p.own = attn_plan(B, heads, kv_heads, max_len, window, sinks);
+    if (shared) {
+        p.prefix = prefix_plan(B, heads, kv_heads, max_prefix);
+        p.own.splits = std::min(p.own.splits, 128);  // the join weighs 256 parts at most
+    }
+    if (B > 0 && (shared || p.own.splits > 1)) {
+        const size_t n = (size_t)B * heads * (p.own.splits + p.prefix.splits);
+        p.stat_bytes = align_up(n * sizeof(float2), 256);
+        p.ws_bytes = p.stat_bytes + align_up(n * head_dim * sizeof(float), 256);
+    }
+    return p;
+}
+
+static bool attn_sizes_ok(int B, int heads, int kv_heads, int head_dim, int max_len, int window, int sinks)
+{
+    return B > 0 && heads > 0 && kv_heads > 0 && heads % kv_heads == 0 && head_dim > 0 && max_len >= 0 && window >= 0 &&
+           sinks >= 0;
+}
+
+size_t w4a4_paged_attn_quant_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_len, int window,
+                                             int sinks)
+{
+    if (!attn_sizes_ok(B, heads, kv_heads, head_dim, max_len, window, sinks)) return 0;
+    return kv_attn_plan(B, heads, kv_heads, head_dim, false, 0, max_len, window, sinks).ws_bytes;
+}
+
+size_t w4a4_paged_attn_shared_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int max_prefix,
+                                              int max_len)
+{
+    if (!attn_sizes_ok(B, heads, kv_heads, head_dim, max_len, 0, 0) || max_prefix < 0) return 0;
+    return kv_attn_plan(B, heads, kv_heads, head_dim, true, max_prefix, max_len, 0, 0).ws_bytes;
+}
+
+// Both calls: a.kv and the prefix's fields are set and checked
+static int kv_attn(AttnArgs &a, bool shared, int max_prefix, const void *q, int dtype, int B, int heads, int kv_heads,
+                   int head_dim, int64_t ldq, const int32_t *table, int table_width, int64_t ldt, const int32_t *lens,
+                   int max_len, float scale, int window, int sinks, void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                   hipStream_t stream)
+{
+    int rc;
+    if (B < 0) return fail(W4A4_ERR_ARG, "B = %d negative", B);
+    if (B > 65535) return fail(W4A4_ERR_UNSUPPORTED, "B = %d above 65535", B);
+    if (heads % kv_heads)
+        return fail(W4A4_ERR_SHAPE, "heads %d is not a multiple of kv_heads %d", heads, kv_heads);
+    if ((int64_t)B * heads > (1 << 23))
+        return fail(W4A4_ERR_UNSUPPORTED, "B * heads = %lld above 2^23", (long long)B * heads);
+    const int64_t width = (int64_t)heads * head_dim;
+    if ((rc = check_rows16(q, B, ldq, width, "q")) || (rc = check_rows16(out, B, ldo, width, "out"))) return rc;
+    if (table_width <= 0) return fail(W4A4_ERR_ARG, "table_width = %d must be positive", table_width);
+    if (ldt < table_width)
+        return fail(W4A4_ERR_SHAPE, "table row stride %lld < %d", (long long)ldt, table_width);
+    if ((int64_t)table_width * a.kv.page_size > ((int64_t)1 << 30))
+        return fail(W4A4_ERR_UNSUPPORTED, "a table row of more than 2^30 tokens");
+    if (B > 0 && (!table || !lens)) return fail(W4A4_ERR_ARG, "table and lens are required");
+    if (!aligned(table, 4) || !aligned(lens, 4)) return fail(W4A4_ERR_ALIGN, "table / lens misaligned");
+    if (max_len < 0 || window < 0 || sinks < 0)
+        return fail(W4A4_ERR_ARG, "max_len %d, window %d and sinks %d must not be negative", max_len,
+                    window, sinks);
+    if (!std::isfinite(scale)) return fail(W4A4_ERR_ARG, "scale must be finite");
+    const KvAttnPlan plan = kv_attn_plan(B, heads, kv_heads, head_dim, shared, max_prefix, max_len, window, sinks);
+    if ((rc = check_ws(ws, ws_bytes, plan.ws_bytes))) return rc;
+    if (B == 0) return ok();
+    a.q = (const uint16_t *)q;
+    a.out = (uint16_t *)out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.ldt = ldt;
+    a.table = table;
+    a.lens = lens;
+    a.B = B;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.page_size = a.kv.page_size;
+    a.table_width = table_width;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.splits = plan.own.splits;
+    a.tiles_per_split = plan.own.tiles_per_split;
+    a.waves = plan.own.waves;
+    a.prefix_splits = plan.prefix.splits;
+    a.prefix_tiles = plan.prefix.tiles;
+    a.prefix_row_waves = plan.prefix.row_waves;
+    a.prefix_row_blocks = plan.prefix.row_blocks;
+    if (plan.ws_bytes) {
+        a.stat = reinterpret_cast<float2 *>(ws);
+        a.part = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + plan.stat_bytes);
+    }
+    if ((rc = launch_kv_attn(a, dtype, head_dim, plan.prefix.rt, stream))) return rc;
+    return ok();
+}
+
+int w4a4_paged_attn_decode_quant(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim, int64_t ldq,
+                                 int kv_format, const void *k_codes, const void *v_codes, const void *k_scale,
+                                 const void *v_scale, int num_pages, int page_size, int64_t page_stride,
+                                 int64_t scale_stride, const int32_t *table, int table_width, int64_t ldt,
+                                 const int32_t *lens, int max_len, float scale, int window, int sinks, void *out,
+                                 int64_t ldo, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    int rc;
+    AttnArgs a{};
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim)) ||
+        (rc = check_kv(kv_format, k_codes, v_codes, k_scale, v_scale, kv_heads, head_dim, num_pages, page_size,
+                       page_stride, scale_stride, false, &a.kv)))
+        return rc;
+    return kv_attn(a, false, 0, q, dtype, B, heads, kv_heads, head_dim, ldq, table, table_width, ldt, lens, max_len,
+                   scale, window, sinks, out, ldo, ws, ws_bytes, stream);
+}
+
+int w4a4_paged_attn_shared(const void *q, int dtype, int B, int heads, int kv_heads, int head_dim, int64_t ldq,
+                           int kv_format, const void *k, const void *v, const void *k_scale, const void *v_scale,
+                           int num_pages, int page_size, int64_t page_stride, int64_t scale_stride,
+                           const int32_t *prefix_table, int prefix_width, const int32_t *prefix_len, int max_prefix,
+                           const int32_t *table, int table_width, int64_t ldt, const int32_t *lens, int max_len,
+                           float scale, void *out, int64_t ldo, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    int rc;
+    AttnArgs a{};
+    if ((rc = check_dtype16(dtype)) || (rc = check_heads(heads, kv_heads, head_dim)) ||
+        (rc = check_kv(kv_format, k, v, k_scale, v_scale, kv_heads, head_dim, num_pages, page_size, page_stride,
+                       scale_stride, true, &a.kv)))
+        return rc;
+    if (prefix_width < 0 || max_prefix < 0)
+        return fail(W4A4_ERR_ARG, "prefix_width %d and max_prefix %d must not be negative", prefix_width, max_prefix);
+    if ((int64_t)prefix_width * page_size > ((int64_t)1 << 30))
+        return fail(W4A4_ERR_UNSUPPORTED, "a prefix table of more than 2^30 tokens");
+    if (B > 0 && (!prefix_len || (prefix_width > 0 && !prefix_table)))
+        return fail(W4A4_ERR_ARG, "prefix_table and prefix_len are required");
+    if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+        return fail(W4A4_ERR_ALIGN, "prefix_table / prefix_len misaligned");
+    a.prefix_table = prefix_table;
+    a.prefix_len = prefix_len;
+    a.prefix_width = prefix_width;
+    return kv_attn(a, true, max_prefix, q, dtype, B, heads, kv_heads, head_dim, ldq, table, table_width, ldt, lens,
+                   max_len, scale, 0, 0, out, ldo, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ low-rank adapters
+
+size_t w4a4_adapter_workspace_bytes(int M, int K, int R)
+{
+    if (M <= 0 || K <= 0 || R <= 0) return 0;
+    return align_up((size_t)adapter_parts(M, K) * M * R * sizeof(float), 256);
+}
+
+int w4a4_adapter_add(const void *X, int dtype, int M, int K, int64_t ldx, const void *A, int64_t stride_a, const void *B,
+                     int64_t stride_b, int n, int R, const int32_t *ids, const float *scale, int N, const void *Y,
+                     int64_t ldy, int epilogue, const void *residual, int64_t ldr, void *out, int64_t ldo, void *ws,
+                     size_t ws_bytes, hipStream_t stream)
+{
+    int rc;
+    if ((rc = check_dtype16(dtype))) return rc;
+    if (M < 0 || K <= 0 || N <= 0 || n <= 0 || R <= 0)
+        return fail(W4A4_ERR_ARG, "M %d must not be negative, K %d, N %d, n %d and R %d positive", M, K, N, n, R);
+    if (K % 8 || R % 8) return fail(W4A4_ERR_SHAPE, "K %d and R %d must be multiples of 8", K, R);
+    if (R > 256) return fail(W4A4_ERR_UNSUPPORTED, "R = %d above 256", R);
+    if (M > (1 << 25) || K > (1 << 23) || N > (1 << 24))
+        return fail(W4A4_ERR_UNSUPPORTED, "M %d, K %d, N %d above 2^25, 2^23, 2^24", M, K, N);
+    if ((rc = check_rows16(X, M, ldx, K, "X")) || (rc = check_rows16(Y, M, ldy, N, "Y")) ||
+        (rc = check_rows16(out, M, ldo, N, "out")))
+        return rc;
+    if (epilogue != W4A4_EPI_NONE && epilogue != W4A4_EPI_GELU && epilogue != W4A4_EPI_RESIDUAL)
+        return fail(W4A4_ERR_ARG, "epilogue %d unknown", epilogue);
+    if (epilogue == W4A4_EPI_RESIDUAL && (rc = check_rows16(residual, M, ldr, N, "residual"))) return rc;
+    if (stride_a < (int64_t)R * K || stride_b < (int64_t)N * R)
+        return fail(W4A4_ERR_SHAPE, "adapter strides %lld, %lld below R K, N R", (long long)stride_a, (long long)stride_b);
+    if (n > ((int64_t)1 << 44) / std::max(stride_a, stride_b))
+        return fail(W4A4_ERR_UNSUPPORTED, "adapters above 2^44 elements");
+    if (!A || !B) return fail(W4A4_ERR_ARG, "A and B are required");
+    if (M > 0 && !ids) return fail(W4A4_ERR_ARG, "ids is NULL");
+    if (!aligned(A, 2) || !aligned(B, 2) || !aligned(ids, 4) || !aligned(scale, 4))
+        return fail(W4A4_ERR_ALIGN, "A / B / ids / scale misaligned");
+    if ((rc = check_ws(ws, ws_bytes, w4a4_adapter_workspace_bytes(M, K, R)))) return rc;
+    if (M == 0) return ok();
+    AdapterArgs a{};
+    a.X = (const uint16_t *)X;
+    a.A = (const uint16_t *)A;
+    a.B = (const uint16_t *)B;
+    a.Y = (const uint16_t *)Y;
+    a.residual = epilogue == W4A4_EPI_RESIDUAL ? (const uint16_t *)residual : nullptr;
+    a.out = (uint16_t *)out;
+    a.M = M;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.ldr = ldr;
+    a.ldo = ldo;
+    a.stride_a = stride_a;
+    a.stride_b = stride_b;
+    a.K = K;
+    a.N = N;
+    a.R = R;
+    a.n = n;
+    a.ids = ids;
+    a.scale = scale;
+    a.epilogue = epilogue;
+    a.parts = adapter_parts(M, K);
+    a.T = (float *)ws;
+    if ((rc = launch_adapter(a, dtype, stream))) return rc;
     return ok();
 }
 

@@ -3,43 +3,9 @@
 // over that cache.
 #include <algorithm>
 
-#include "w4a4_internal.h"
+#include "kv_quant.h"
 
 namespace w4a4 {
-
-typedef float f4_t __attribute__((ext_vector_type(4)));
-typedef float f2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
-
-// two fp32 values rounded to the 16-bit type, low value first, and back
-template <int DT> __device__ __forceinline__ uint32_t pack16(float a, float b)
-{
-    if constexpr (DT == W4A4_BF16)
-        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, b2_t));
-    else
-        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, h2_t));
-}
-
-template <int DT> __device__ __forceinline__ f2_t unpack16(uint32_t w)
-{
-    if constexpr (DT == W4A4_BF16)
-        return f2_t{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
-    else
-        return __builtin_convertvector(__builtin_bit_cast(h2_t, w), f2_t);
-}
-
-// Eight consecutive 16-bit elements from and to any element's address: the hardware's vector accesses
-// take them all.
-typedef uint32_t any4_t __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t any2_t __attribute__((ext_vector_type(2), aligned(2)));
-typedef float anyf4_t __attribute__((ext_vector_type(4), aligned(4)));
-__device__ __forceinline__ u4_t load8_any(const uint16_t *p) { return *reinterpret_cast<const any4_t *>(p); }
-__device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinterpret_cast<any4_t *>(p) = v; }
 
 // ================================================================================================
 // Norm, rotation, append. Per head x of D channels: y = x / sqrt(mean(x^2) + eps) * w, then the first
@@ -57,34 +23,9 @@ __device__ __forceinline__ void store8_any(uint16_t *p, const u4_t &v) { *reinte
 // ================================================================================================
 constexpr int HEADS_AHEAD = 4;
 
-// Sum over LH neighbouring lanes (a power of two), in every lane.
-template <int CTRL> __device__ __forceinline__ float dpp_add(float x)
-{
-    const int y = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true);
-    return x + __builtin_bit_cast(float, y);
-}
-
-template <int LH> __device__ __forceinline__ float sum_lanes(float x)
-{
-    x = dpp_add<0xB1>(x);                       // quad_perm: lane ^ 1
-    x = dpp_add<0x4E>(x);                       // quad_perm: lane ^ 2
-    if (LH >= 8) x = dpp_add<0x141>(x);         // row_half_mirror: the other quad of eight
-    if (LH >= 16) x = dpp_add<0x140>(x);        // row_mirror: the other half of sixteen
-    if (LH >= 32) {
-        const uint32_t u = __builtin_bit_cast(uint32_t, x);
-        const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-        x = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
-    }
-    if (LH >= 64) {
-        const uint32_t u = __builtin_bit_cast(uint32_t, x);
-        const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-        x = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
-    }
-    return x;
-}
-
-// PART: with PAIRS, some channels are not rotated.
-template <int DT, int LH, bool PAIRS, bool PART>
+// PART: with PAIRS, some channels are not rotated. KV: what the cache holds; rows for a quantized one are rounded to
+// 16 bits as any other, and then quantized, so that it holds what a 16-bit cache's rows would be quantized to.
+template <int DT, int LH, bool PAIRS, bool PART, int KV>
 __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
 {
     extern __shared__ float2 turns[];  // [tokens of the workgroup][rot / 2] (cos, sin)
@@ -98,9 +39,10 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
     const int dl = on ? d : 0;
 
     // the first heads' loads go out before anything else
-    const int nq = a.heads, nk = a.kv_heads, total = nq + nk + (a.k_cache ? nk : 0);
+    const bool cached = KV != W4A4_KV_16BIT || a.k_cache;
+    const int nq = a.heads, nk = a.kv_heads, total = nq + nk + (cached ? nk : 0);
     const uint16_t *qs = a.q + mc * a.ldq + dl, *ks = a.k + mc * a.ldk + dl;
-    const uint16_t *vs = a.k_cache ? a.v + mc * a.ldv + dl : ks;
+    const uint16_t *vs = cached ? a.v + mc * a.ldv + dl : ks;
     const int D = a.D;
     auto load = [=](int h) {  // past the end: the last head
         h = min(h, total - 1);
@@ -113,7 +55,10 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
     for (int u = 0; u < HEADS_AHEAD; ++u)
         if (u == 0 || sub * HP + u * step < total) raw[u] = load(sub * HP + u * step + lane / LH);
     int64_t row = -1;  // cache row offset of this token (elements), -1: not kept
-    if (a.k_cache) {
+    KvSlot slot{-1, 0};
+    if constexpr (KV != W4A4_KV_16BIT) {
+        slot = kv_slot(a.kv, a.slots[mc]);
+    } else if (a.k_cache) {
         const int64_t s = a.slots[mc];
         if (s >= 0 && s < (int64_t)a.num_pages * a.page_size)
             row = (s >> a.page_shift) * a.page_stride + (s & (a.page_size - 1)) * a.D;
@@ -219,13 +164,22 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
                 }
             }
         }
+        QuantRun<KV> coded;
+        if constexpr (KV != W4A4_KV_16BIT)
+            if (h0 + HP > nq) coded = quant_run<DT, KV, LH>(out);  // some of these heads go to the cache
         if (!on || h >= total) return;
         if (is_q) {
             store8_any(a.q_out + m * a.ldqo + h * a.D + d, out);
         } else {
             const int hk = is_v ? h - nq - nk : h - nq;
             if (!is_v && a.k_out) store8_any(a.k_out + m * a.ldko + hk * a.D + d, out);
-            if (row >= 0) {
+            if constexpr (KV != W4A4_KV_16BIT) {
+                if (slot.page >= 0) {
+                    uint8_t *kc = a.kv.k, *vc = a.kv.v;
+                    void *ksc = a.kv.k_scale, *vsc = a.kv.v_scale;
+                    quant_store<KV>(a.kv, is_v ? vc : kc, is_v ? vsc : ksc, slot, hk, a.D, d, coded);
+                }
+            } else if (row >= 0) {
                 uint16_t *kc = a.k_cache, *vc = a.v_cache;
                 store8_any((is_v ? vc : kc) + row + hk * a.page_size * a.D + d, out);
             }
@@ -243,24 +197,33 @@ __global__ __launch_bounds__(512) void k_norm_rope(const NormRopeArgs a)
     }
 }
 
-template <int DT, int LH> static int run_norm_rope(const NormRopeArgs &a, bool pairs, hipStream_t s)
+template <int DT, int LH, int KV> static int run_norm_rope(const NormRopeArgs &a, bool pairs, hipStream_t s)
 {
     const int waves = std::max(4, a.waves_per_token), tpw = waves / a.waves_per_token;
     const dim3 grid((unsigned)((a.M + tpw - 1) / tpw)), block(64 * waves);
     const size_t lds = (size_t)tpw * (a.rot / 2) * sizeof(float2);
-    if (pairs && a.rot < a.D) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, true>), grid, block, lds, s, a);
-    else if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, false>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false, false>), grid, block, lds, s, a);
+    if (pairs && a.rot < a.D) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, true, KV>), grid, block, lds, s, a);
+    else if (pairs) hipLaunchKernelGGL((k_norm_rope<DT, LH, true, false, KV>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_norm_rope<DT, LH, false, false, KV>), grid, block, lds, s, a);
     return check_launch("qk_norm_rope");
 }
 
-template <int DT> static int pick_head(const NormRopeArgs &a, bool pairs, hipStream_t s)
+template <int DT, int KV> static int pick_head(const NormRopeArgs &a, bool pairs, hipStream_t s)
 {
-    if (a.D <= 32) return run_norm_rope<DT, 4>(a, pairs, s);
-    if (a.D <= 64) return run_norm_rope<DT, 8>(a, pairs, s);
-    if (a.D <= 128) return run_norm_rope<DT, 16>(a, pairs, s);
-    if (a.D <= 256) return run_norm_rope<DT, 32>(a, pairs, s);
-    return run_norm_rope<DT, 64>(a, pairs, s);
+    if constexpr (KV == W4A4_KV_16BIT) {
+        if (a.D <= 32) return run_norm_rope<DT, 4, KV>(a, pairs, s);
+        if (a.D > 256) return run_norm_rope<DT, 64, KV>(a, pairs, s);
+    }
+    if (a.D <= 64) return run_norm_rope<DT, 8, KV>(a, pairs, s);
+    if (a.D <= 128) return run_norm_rope<DT, 16, KV>(a, pairs, s);
+    return run_norm_rope<DT, 32, KV>(a, pairs, s);
+}
+
+template <int DT> static int pick_format(const NormRopeArgs &a, bool pairs, hipStream_t s)
+{
+    if (a.kv.format == W4A4_KV_INT8) return pick_head<DT, W4A4_KV_INT8>(a, pairs, s);
+    if (a.kv.format == W4A4_KV_FP4) return pick_head<DT, W4A4_KV_FP4>(a, pairs, s);
+    return pick_head<DT, W4A4_KV_16BIT>(a, pairs, s);
 }
 
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
@@ -276,8 +239,8 @@ int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
     //   5 + 1 heads of 96      200: 3.8, 3.8;  300: 4.5, 4.2;  768: 4.4, 4.3;  850: 4.8, 4.4;  2056: 6.3, 5.5
     a.waves_per_token = a.M <= 256 ? 8 : a.M <= 768 ? 4 : a.M <= 2048 ? 2 : 1;
     a.page_shift = a.page_size ? __builtin_ctz((unsigned)a.page_size) : 0;
-    return dtype == W4A4_BF16 ? pick_head<W4A4_BF16>(a, interleaved, s)
-                              : pick_head<W4A4_F16>(a, interleaved, s);
+    return dtype == W4A4_BF16 ? pick_format<W4A4_BF16>(a, interleaved, s)
+                              : pick_format<W4A4_F16>(a, interleaved, s);
 }
 
 // ================================================================================================
@@ -300,59 +263,6 @@ int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s)
 // 16 heads of 64 42.5 us (5.0 TB/s); one of 1001 tokens, one key/value head of 256, 9.6 us, the chain of two
 // launches.
 // ================================================================================================
-
-// Tiles of 32 keys that hold something visible: tiles [0, ns) and from w0 on, T in all.
-struct AttnTiles {
-    int ns, w0, T;
-    bool over;  // longer than the table can say: poisoned, one logical tile
-};
-
-__device__ __forceinline__ AttnTiles attn_tiles(int n, const AttnArgs &a)
-{
-    AttnTiles t{0, 0, 0, false};
-    if (n <= 0) return t;
-    if ((int64_t)n > (int64_t)a.table_width * a.page_size) {
-        t.over = true;
-        t.T = 1;
-        return t;
-    }
-    const int all = (int)(((int64_t)n + 31) >> 5);
-    if (a.window > 0 && (int64_t)n > (int64_t)a.window + a.sinks) {
-        t.ns = (a.sinks + 31) >> 5;
-        t.w0 = max((n - a.window) >> 5, t.ns);
-    }
-    t.T = t.ns + all - t.w0;
-    return t;
-}
-
-template <int DT> __device__ __forceinline__ f4_t mma32(const u4_t &a, const u4_t &b, const f4_t &c)
-{
-    if constexpr (DT == W4A4_F16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a),
-                                                      __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a),
-                                                       __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
-}
-
-// combine the four 16-lane groups of a wave: every lane gets the result over lanes l, l^16, l^32, l^48
-template <typename F> __device__ __forceinline__ float across_groups(float x, F f)
-{
-    uint32_t u = __builtin_bit_cast(uint32_t, x);
-    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    x = f(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
-    u = __builtin_bit_cast(uint32_t, x);
-    auto b = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    return f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
-}
-
-constexpr int ATTN_WAVES = 4;   // waves of a workgroup, or one where there is little to do
-constexpr int ATTN_PAD = 4;     // floats between the heads' rows in LDS, against bank conflicts
-
-// N dwords from a 4-byte aligned address
-template <int N> struct __attribute__((aligned(4))) DwordRun {
-    uint32_t v[N];
-};
 
 template <int DT, int D>
 __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_split(const AttnArgs a)

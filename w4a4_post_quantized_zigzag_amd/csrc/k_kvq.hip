@@ -1,0 +1,458 @@
+// The quantized key-value cache: rows into it and back, the attention of one new token per sequence over it, and the
+// same attention behind a prefix that all sequences of a batch share (over a quantized or a 16-bit cache).
+#include <algorithm>
+#include <type_traits>
+
+#include "kv_tile.h"
+
+namespace w4a4 {
+
+// ================================================================================================
+// Rows as they are into the cache, and back. A lane takes eight channels of one head of one token, a head is LH
+// lanes. Bound by the bytes.
+// ================================================================================================
+template <int DT, int F, int LH> __global__ __launch_bounds__(256) void k_kv_append(const KvRowsArgs a)
+{
+    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LH;  // key and value heads of all tokens
+    const int d = threadIdx.x % LH * 8;
+    const int64_t heads = 2 * a.kv_heads, m = id / heads;
+    const int h = (int)(id % heads);
+    const bool is_v = h >= a.kv_heads, on = m < a.M && d < a.D;
+    const int64_t mc = min(m, a.M - 1);
+    const uint16_t *row = is_v ? a.v + mc * a.ldv + (h - a.kv_heads) * a.D : a.k + mc * a.ldk + h * a.D;
+    const QuantRun<F> q = quant_run<DT, F, LH>(load8_any(row + (d < a.D ? d : 0)));
+    const KvSlot s = kv_slot(a.kv, a.slots[mc]);
+    if (!on || s.page < 0) return;
+    quant_store<F>(a.kv, is_v ? a.kv.v : a.kv.k, is_v ? a.kv.v_scale : a.kv.k_scale, s, is_v ? h - a.kv_heads : h, a.D, d,
+                   q);
+}
+
+template <int DT, int F, int LH> __global__ __launch_bounds__(256) void k_kv_read(const KvRowsArgs a)
+{
+    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LH;
+    const int d = threadIdx.x % LH * 8;
+    const int64_t heads = 2 * a.kv_heads, m = id / heads;
+    int h = (int)(id % heads);
+    const bool is_v = h >= a.kv_heads;
+    if (m >= a.M || d >= a.D) return;
+    if (is_v) h -= a.kv_heads;
+    uint16_t *out = is_v ? a.v : a.k;
+    if (!out) return;
+    out += m * (is_v ? a.ldv : a.ldk) + h * a.D + d;
+    const KvSlot s = kv_slot(a.kv, a.slots[m]);
+    u4_t x = {0, 0, 0, 0};
+    if (s.page >= 0) {
+        const uint8_t *codes = (is_v ? a.kv.v : a.kv.k) + s.page * a.kv.page_stride;
+        const void *scale = is_v ? a.kv.v_scale : a.kv.k_scale;
+        const int64_t row = (int64_t)h * a.kv.page_size + s.at;
+        if constexpr (F == W4A4_KV_INT8) {
+            const u2_t c = *reinterpret_cast<const u2_t *>(codes + row * a.D + d);
+            const float f = reinterpret_cast<const float *>(scale)[s.page * a.kv.scale_stride + row];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = c[i / 2] >> (16 * (i % 2));
+                x[i] = pack16<DT>((float)(int8_t)w * f, (float)(int8_t)(w >> 8) * f);
+            }
+        } else {
+            const uint32_t c = *reinterpret_cast<const uint32_t *>(codes + row * (a.D / 2) + d / 2);
+            const uint32_t e = reinterpret_cast<const uint8_t *>(
+                scale)[s.page * a.kv.scale_stride + ((int64_t)h * (a.D / 32) + d / 32) * a.kv.page_size + s.at];
+            typedef KvTile<DT, 128, F> T;
+            const float f = T::byte_scale(e);
+            x = u4_t{T::template widen4<0>(c, f), T::template widen4<1>(c, f), T::template widen4<2>(c, f),
+                     T::template widen4<3>(c, f)};
+        }
+    }
+    store8_any(out, x);
+}
+
+template <int DT, int F, int LH> static int run_rows(const KvRowsArgs &a, bool read, hipStream_t s)
+{
+    // a launch holds less than 2^32 threads
+    const int64_t per_token = 2 * a.kv_heads * LH, rows = ((int64_t)1 << 31) / per_token;
+    for (int64_t m = 0; m < a.M; m += rows) {
+        KvRowsArgs b = a;
+        b.M = std::min(rows, a.M - m);
+        b.k = a.k ? a.k + m * a.ldk : nullptr;
+        b.v = a.v ? a.v + m * a.ldv : nullptr;
+        b.slots = a.slots + m;
+        const dim3 grid((unsigned)((b.M * per_token + 255) / 256));
+        if (read) hipLaunchKernelGGL((k_kv_read<DT, F, LH>), grid, dim3(256), 0, s, b);
+        else hipLaunchKernelGGL((k_kv_append<DT, F, LH>), grid, dim3(256), 0, s, b);
+        if (int rc = check_launch(read ? "kv_read_quant" : "kv_append_quant")) return rc;
+    }
+    return W4A4_OK;
+}
+
+template <int DT, int F> static int pick_rows(const KvRowsArgs &a, bool read, hipStream_t s)
+{
+    if (a.D <= 64) return run_rows<DT, F, 8>(a, read, s);
+    if (a.D <= 128) return run_rows<DT, F, 16>(a, read, s);
+    return run_rows<DT, F, 32>(a, read, s);
+}
+
+static int pick_rows(const KvRowsArgs &a, int dtype, bool read, hipStream_t s)
+{
+    if (dtype == W4A4_BF16)
+        return a.kv.format == W4A4_KV_INT8 ? pick_rows<W4A4_BF16, W4A4_KV_INT8>(a, read, s)
+                                           : pick_rows<W4A4_BF16, W4A4_KV_FP4>(a, read, s);
+    return a.kv.format == W4A4_KV_INT8 ? pick_rows<W4A4_F16, W4A4_KV_INT8>(a, read, s)
+                                       : pick_rows<W4A4_F16, W4A4_KV_FP4>(a, read, s);
+}
+
+int launch_kv_append(const KvRowsArgs &a, int dtype, hipStream_t s) { return pick_rows(a, dtype, false, s); }
+int launch_kv_read(const KvRowsArgs &a, int dtype, hipStream_t s) { return pick_rows(a, dtype, true, s); }
+
+// ================================================================================================
+// Attention. A sequence's own tokens: tiles of one sequence go in equal runs to workgroups and there round-robin to
+// the waves, as over the 16-bit cache. The shared prefix: the query rows of all sequences that share a key/value head
+// are cut into row tiles of 16, and each wave takes RT of them over a run of the prefix, so that a tile of keys that
+// has been loaded and widened serves 16 RT rows. Each (sequence, head) then has parts, of the prefix and of its own
+// tokens, which k_join adds up in a fixed order.
+// ================================================================================================
+
+// The parts that a run of T tiles is cut into: `per` tiles each, used of them
+__device__ __forceinline__ int tiles_per_part(int T, int splits, int least) { return max((T + splits - 1) / splits, least); }
+
+// Pages of tile t. A half without a visible key may have no page any more and reads the other half's; a page that
+// does not exist reads page 0 and poisons the result.
+__device__ __forceinline__ KvPlace look_up(const KvPages &c, const int32_t *table, int key0, int n, int from, int sinks,
+                                           bool &bad)
+{
+    KvPlace p;
+    p.key0 = key0;
+    bool any[2];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int lo = key0 + 16 * hf;
+        any[hf] = lo < n && (min(lo + 15, n - 1) >= from || lo < sinks);
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int lo = key0 + 16 * (any[hf] ? hf : 1 - hf);
+        int pid = __builtin_amdgcn_readfirstlane(table[lo >> c.page_shift]);
+        if ((unsigned)pid >= (unsigned)c.num_pages) {
+            bad = true;
+            pid = 0;
+        }
+        p.page[hf] = pid;
+        p.at[hf] = lo & (c.page_size - 1);
+    }
+    return p;
+}
+
+template <int DT, int D, int F>
+__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
+{
+    typedef KvShape<D, F> S;
+    extern __shared__ float sm[];
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    // all heads of one (sequence, split) run on one XCD, and the sequences move on by one XCD from split to split
+    const int hts = a.kv_heads * a.head_tiles;
+    const int unit = blockIdx.x / (8 * hts) * 8 + blockIdx.x % 8, head = blockIdx.x / 8 % hts;
+    const int split = unit / a.B, b = (unit + split) % a.B;
+    const int kvh = head / a.head_tiles, ht = head % a.head_tiles;
+    if (split >= a.splits) return;
+    const int group = a.heads / a.kv_heads, G = min(16, group - ht * 16), h0 = kvh * group + ht * 16;
+    const int n = a.lens[b];
+    const int32_t *table = a.table + (int64_t)b * a.ldt;
+    const AttnTiles tl = attn_tiles(n, a);
+    const int per = tiles_per_part(tl.T, a.splits, a.tiles_per_split);
+    const int t0 = split * per, t1 = min(tl.T, t0 + per);
+    uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h0 * D;
+    if (tl.T == 0) {  // nothing visible: zeros, where no other part follows
+        if (split == 0 && !a.prefix_splits)
+            for (int e = threadIdx.x; e < G * D; e += blockDim.x) out[e] = 0;
+        return;
+    }
+    if (t0 >= t1) return;
+
+    AttnRows<DT, D, F, 1> rows;
+    rows.clear();
+    // operand rows past the group repeat its last head; their results are not used
+    rows.load_q(0, a.q + (int64_t)b * a.ldq + (int64_t)(h0 + min(r, G - 1)) * D, g);
+    bool bad = tl.over;
+    const int from = a.window > 0 ? n - a.window : 0;
+    auto key_of = [&](int t) { return (t < tl.ns ? t : tl.w0 + t - tl.ns) * 32; };
+
+    int t = tl.over ? t1 : t0 + wave;
+    KvTile<DT, D, F> tile;
+    KvPlace at, next;
+    if (t < t1) {
+        at = look_up(a.kv, table, key_of(t), n, from, a.sinks, bad);
+        tile.load(a.kv, at, kvh, lane);
+        if (t + waves < t1) next = look_up(a.kv, table, key_of(t + waves), n, from, a.sinks, bad);
+    }
+    for (; t < t1; t += waves) {
+        const int key0 = at.key0;
+        const bool whole = key0 <= n - 32 && (key0 >= from || key0 + 32 <= a.sinks);
+        KvTile<DT, D, F> cur = tile;
+        if (t + waves < t1) {  // the next tile's loads, and the pages of the one behind it
+            at = next;
+            tile.load(a.kv, at, kvh, lane);
+            if (t + 2 * waves < t1) next = look_up(a.kv, table, key_of(t + 2 * waves), n, from, a.sinks, bad);
+        }
+        bool ok[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int key = key0 + 16 * (e / 4) + 4 * g + e % 4;
+            ok[e] = key < n && (key >= from || key < a.sinks);
+        }
+        rows.add(cur, whole, ok, a.scale_log2);
+    }
+    float sum = rows.total(0);
+    if (__any(bad)) sum = NAN;
+
+    // ---- join the waves: maximum [W][16], sum [W][16], channels [W][G][D + pad] ----
+    float *wm = sm, *ws = sm + waves * 16, *wa = sm + waves * 32;
+    constexpr int LD = D + ATTN_PAD;
+    if (g == 0) {
+        wm[wave * 16 + r] = rows.mx[0];
+        ws[wave * 16 + r] = sum;
+    }
+    if (r < G) {
+        float *dst = wa + (wave * G + r) * LD;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (S::VE * 16 == D || S::VE * (4 * g + x) < D)
+#pragma unroll
+                for (int i = 0; i < S::VE; ++i) dst[S::VE * (4 * g + x) + i] = rows.acc[0][i][x];
+    }
+    __syncthreads();
+    const bool alone = !a.prefix_splits && tl.T <= per;
+    for (int e = threadIdx.x; e < G * (D / 4); e += blockDim.x) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
+        float top = wm[h];
+        for (int w = 1; w < waves; ++w) top = fmaxf(top, wm[w * 16 + h]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+        float l = 0.0f;
+        for (int w = 0; w < waves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(wm[w * 16 + h] - base);
+            o += f * *reinterpret_cast<const f4_t *>(wa + (w * G + h) * LD + d);
+            l += f * ws[w * 16 + h];
+        }
+        if (alone) {
+            const u2_t y = {pack16<DT>(o[0] / l, o[1] / l), pack16<DT>(o[2] / l, o[3] / l)};
+            *reinterpret_cast<any2_t *>(out + h * D + d) = y;
+        } else {
+            const int64_t part = ((int64_t)b * a.heads + h0 + h) * (a.prefix_splits + a.splits) + a.prefix_splits + split;
+            *reinterpret_cast<f4_t *>(a.part + part * D + d) = o;
+            if (d == 0) a.stat[part] = make_float2(top, l);
+        }
+    }
+}
+
+// Tiles of the prefix: none, or one logical tile that poisons where the table cannot hold it.
+__device__ __forceinline__ int prefix_tiles(const AttnArgs &a, bool &over)
+{
+    const int n = a.prefix_splits ? a.prefix_len[0] : 0;
+    over = (int64_t)n > (int64_t)a.prefix_width * a.kv.page_size;
+    return over ? 1 : n <= 0 ? 0 : (int)(((int64_t)n + 31) >> 5);
+}
+
+template <int DT, int D, int F, int RT>
+__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix(const AttnArgs a)
+{
+    typedef KvShape<D, F> S;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // wr waves on row tiles, the others on other keys; all row blocks of one (head, part) run on one XCD
+    const int wr = a.prefix_row_waves, wk = ATTN_WAVES / wr;
+    const int unit = blockIdx.x / (8 * a.prefix_row_blocks) * 8 + blockIdx.x % 8;
+    const int block = blockIdx.x / 8 % a.prefix_row_blocks;
+    const int parts = a.prefix_splits / wk;
+    const int kvh = unit / parts, split = unit % parts * wk + wave / wr;
+    if (kvh >= a.kv_heads) return;
+    const int group = a.heads / a.kv_heads;
+    const int64_t total = (int64_t)a.B * group, row0 = ((int64_t)block * wr + wave % wr) * 16 * RT;
+    if (row0 >= total) return;
+    bool bad;
+    const int T = prefix_tiles(a, bad), n = bad ? 0 : a.prefix_len[0];
+    const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+    const int t0 = split * per, t1 = min(T, t0 + per);
+    if (t0 >= t1) return;
+
+    AttnRows<DT, D, F, RT> rows;
+    rows.clear();
+    auto place = [&](int t, int64_t &b, int &h) {  // row r of row tile t
+        const int64_t row = min(row0 + 16 * t + r, total - 1);
+        b = row / group;
+        h = kvh * group + (int)(row - b * group);
+    };
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        int64_t b;
+        int h;
+        place(t, b, h);
+        rows.load_q(t, a.q + b * a.ldq + (int64_t)h * D, g);
+    }
+    if (!bad) {
+        KvTile<DT, D, F> tile;
+        for (int t = t0; t < t1; ++t) {
+            const int key0 = t * 32;
+            const KvPlace at = look_up(a.kv, a.prefix_table, key0, n, 0, 0, bad);
+            tile.load(a.kv, at, kvh, lane);
+            bool ok[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ok[e] = key0 + 16 * (e / 4) + 4 * g + e % 4 < n;
+            rows.add(tile, key0 <= n - 32, ok, a.scale_log2);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        float sum = rows.total(t);
+        if (__any(bad)) sum = NAN;
+        if (row0 + 16 * t + r >= total) continue;
+        int64_t b;
+        int h;
+        place(t, b, h);
+        const int64_t part = (b * a.heads + h) * (a.prefix_splits + a.splits) + split;
+        if (g == 0) a.stat[part] = make_float2(rows.mx[t], sum);
+        float *dst = a.part + part * D;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (S::VE * 16 == D || S::VE * (4 * g + x) < D)
+#pragma unroll
+                for (int i = 0; i < S::VE; ++i) dst[S::VE * (4 * g + x) + i] = rows.acc[t][i][x];
+    }
+}
+
+// out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the parts that had tiles, one workgroup per
+// (sequence, head): the prefix's parts come first, the sequence's own behind them.
+constexpr int JOIN_MAX = 256;
+template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const AttnArgs a)
+{
+    constexpr int TC = D / 4, ROWS = 256 / TC;  // threads over the channels, parts at a time
+    __shared__ float4 red[ROWS][TC];
+    __shared__ float weight[JOIN_MAX], wave_top[4], wave_sum[4];
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
+    const int c = tid % TC, row = tid / TC;
+    const int64_t at = ((int64_t)b * a.heads + h) * (a.prefix_splits + a.splits);
+    const float4 *p = reinterpret_cast<const float4 *>(a.part + at * D) + c;
+    bool over;
+    int used_p = 0, used_s = 0;
+    if (a.prefix_splits) {
+        const int T = prefix_tiles(a, over);
+        const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+        used_p = (T + per - 1) / per;
+    }
+    const AttnTiles tl = attn_tiles(a.lens[b], a);
+    const int per = tiles_per_part(tl.T, a.splits, a.tiles_per_split);
+    used_s = (tl.T + per - 1) / per;
+    if (!a.prefix_splits && used_s <= 1) return;  // written by its only workgroup
+    const int used = used_p + used_s;
+    auto place = [&](int i) { return i < used_p ? i : a.prefix_splits + i - used_p; };
+    uint16_t *out = a.out + (int64_t)b * a.ldo + (int64_t)h * D;
+    if (used == 0) {
+        for (int e = tid; e < D; e += 256) out[e] = 0;
+        return;
+    }
+    const float2 st = tid < used ? a.stat[at + place(tid)] : make_float2(-INFINITY, 0.0f);
+    float top = st.x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((tid & 63) == 0) wave_top[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    const float f = __builtin_amdgcn_exp2f(st.x - (top == -INFINITY ? 0.0f : top));
+    weight[tid] = f;
+    float l = f * st.y;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    if ((tid & 63) == 0) wave_sum[wave] = l;
+    __syncthreads();
+    l = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+    float4 o = make_float4(0, 0, 0, 0);
+    if (row < ROWS) {
+#pragma unroll 4
+        for (int s = row; s < used; s += ROWS) {
+            const float4 x = p[(int64_t)place(s) * TC];
+            const float w = weight[s];
+            o.x = fmaf(w, x.x, o.x);
+            o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z);
+            o.w = fmaf(w, x.w, o.w);
+        }
+        red[row][c] = o;
+    }
+    __syncthreads();
+    if (row == 0) {
+        for (int s = 1; s < ROWS; ++s) {
+            const float4 v = red[s][c];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        const u2_t y = {pack16<DT>(o.x / l, o.y / l), pack16<DT>(o.z / l, o.w / l)};
+        *reinterpret_cast<any2_t *>(out + 4 * c) = y;
+    }
+}
+
+PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
+{
+    PrefixPlan p;
+    const int64_t rows = (int64_t)std::max(B, 1) * (heads / kv_heads), row_tiles = (rows + 15) / 16;
+    const int64_t tiles = std::max<int64_t>(((int64_t)max_prefix + 31) / 32, 1);
+    p.rt = row_tiles > 4 ? 2 : 1;
+    const int64_t wave_rows = (row_tiles + p.rt - 1) / p.rt;
+    p.row_waves = wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;
+    p.row_blocks = (int)((wave_rows + p.row_waves - 1) / p.row_waves);
+    const int wk = ATTN_WAVES / p.row_waves;
+    const int64_t want = std::max<int64_t>(512 / (p.row_blocks * (int64_t)kv_heads), 1);  // workgroups of a head's keys
+    p.splits = (int)std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(want, (tiles + wk - 1) / wk), 1), 128 / wk) * wk;
+    p.tiles = 1;
+    return p;
+}
+
+template <int DT, int D, int F> static int run_kv_attn(const AttnArgs &a, int rt, hipStream_t s)
+{
+    int rc;
+    if (a.prefix_splits) {
+        const int wk = ATTN_WAVES / a.prefix_row_waves;
+        const int64_t units = (int64_t)a.kv_heads * (a.prefix_splits / wk);
+        const dim3 grid((unsigned)((units + 7) / 8 * 8 * a.prefix_row_blocks));
+        if (rt == 2) hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 2>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
+        else hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 1>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
+        if ((rc = check_launch("paged_attn prefix"))) return rc;
+    }
+    const int G = std::min(16, a.heads / a.kv_heads);
+    const size_t lds = (size_t)a.waves * (32 + G * (D + ATTN_PAD)) * sizeof(float);
+    if (lds > 65536 &&  // more than every kernel gets unasked
+        (rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_own<DT, D, F>), lds, "paged_attn")))
+        return rc;
+    const int64_t units = ((int64_t)a.B * a.splits + 7) / 8 * 8;
+    hipLaunchKernelGGL((k_attn_own<DT, D, F>), dim3((unsigned)(units * a.kv_heads * a.head_tiles)), dim3(64 * a.waves), lds,
+                       s, a);
+    if ((rc = check_launch("paged_attn")) || (a.splits == 1 && !a.prefix_splits)) return rc;
+    hipLaunchKernelGGL((k_join<DT, D>), dim3(a.heads, a.B), dim3(256), 0, s, a);
+    return check_launch("paged_attn join");
+}
+
+template <int DT, int D> static int pick_format(const AttnArgs &a, int rt, hipStream_t s)
+{
+    if (a.kv.format == W4A4_KV_INT8) return run_kv_attn<DT, D, W4A4_KV_INT8>(a, rt, s);
+    if (a.kv.format == W4A4_KV_FP4) return run_kv_attn<DT, D, W4A4_KV_FP4>(a, rt, s);
+    return run_kv_attn<DT, D, W4A4_KV_16BIT>(a, rt, s);
+}
+
+template <int DT> static int pick_dim(const AttnArgs &a, int D, int rt, hipStream_t s)
+{
+    switch (D) {
+    case 64: return pick_format<DT, 64>(a, rt, s);
+    case 96: return pick_format<DT, 96>(a, rt, s);
+    case 128: return pick_format<DT, 128>(a, rt, s);
+    case 192: return pick_format<DT, 192>(a, rt, s);
+    default: return pick_format<DT, 256>(a, rt, s);
+    }
+}
+
+int launch_kv_attn(AttnArgs a, int dtype, int D, int rt, hipStream_t s)
+{
+    a.head_tiles = (a.heads / a.kv_heads + 15) / 16;
+    return dtype == W4A4_BF16 ? pick_dim<W4A4_BF16>(a, D, rt, s) : pick_dim<W4A4_F16>(a, D, rt, s);
+}
+
+}  // namespace w4a4

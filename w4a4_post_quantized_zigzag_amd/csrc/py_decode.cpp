@@ -193,6 +193,68 @@ void dense(const at::Tensor &t, at::ScalarType dt, int64_t n, const char *name)
         TORCH_CHECK_VALUE(false, name, " must be contiguous ", dt, " [", n, "]");
 }
 
+// ---- a cache of any format -------------------------------------------------------------------------
+
+struct Kv {
+    at::Tensor k, v, ks, vs;  // scales undefined for 16 bits
+    int format, pages, page;
+    int64_t heads, stride, scale_stride;
+    void same(const Place &p) const { p.same(k), p.same(v), p.same(ks), p.same(vs); }
+};
+
+// (k, v) of the elements' type `dt`, where `sixteen`, or (k, v, k_scale, v_scale): int8 [pages, kv_heads, page_size, D] with
+// fp32 [pages, kv_heads, page_size], or uint8 [.., D / 2] with uint8 [pages, kv_heads, D / 32, page_size]
+Kv kv_of(PyObject *o, at::ScalarType dt, int64_t D, bool sixteen)
+{
+    if (!PyTuple_Check(o)) TORCH_CHECK_TYPE(false, "cache must be a tuple of tensors");
+    const Py_ssize_t n = PyTuple_GET_SIZE(o);
+    if (n != 4 && !(sixteen && n == 2))
+        TORCH_CHECK_VALUE(false, "cache must be (k, v, k_scale, v_scale)", sixteen ? " or (k, v)" : "");
+    Kv c;
+    c.k = tensor(PyTuple_GET_ITEM(o, 0), "k"), c.v = tensor(PyTuple_GET_ITEM(o, 1), "v");
+    want(c.k.dim() == 4, "cache must be [pages, kv_heads, page_size, ..]");
+    const int64_t P = c.k.size(0), page = c.k.size(2);
+    c.heads = c.k.size(1);
+    int64_t row = D;
+    if (n == 2) {
+        c.format = W4A4_KV_16BIT;
+        if (c.k.scalar_type() != dt) TORCH_CHECK_VALUE(false, "a cache of two tensors must be ", dt);
+    } else if (c.k.scalar_type() == at::kChar) {
+        c.format = W4A4_KV_INT8;
+    } else if (c.k.scalar_type() == at::kByte) {
+        c.format = W4A4_KV_FP4;
+        row = D / 2;
+    } else {
+        TORCH_CHECK_TYPE(false, "codes must be int8 or uint8, not ", c.k.scalar_type());
+    }
+    if (c.k.size(3) != row)
+        TORCH_CHECK_VALUE(false, "cache rows of ", c.k.size(3), " elements do not hold head_dim ", D);
+    want(c.v.scalar_type() == c.k.scalar_type() && c.v.sizes() == c.k.sizes() && c.v.strides() == c.k.strides(),
+         "keys and values must be laid out alike");
+    want(c.k.stride(3) == 1 && c.k.stride(2) == row && (c.k.stride(1) == page * row || c.heads == 1),
+         "a cache page must be dense");
+    c.pages = size(P, "pages"), c.page = size(page, "page_size"), c.stride = ld(c.k, c.heads * page * row);
+    c.scale_stride = 0;
+    if (n == 4) {
+        c.ks = tensor(PyTuple_GET_ITEM(o, 2), "k_scale"), c.vs = tensor(PyTuple_GET_ITEM(o, 3), "v_scale");
+        const bool fp4 = c.format == W4A4_KV_FP4;
+        const int64_t groups = fp4 ? D / 32 : 1;
+        const auto st = fp4 ? at::kByte : at::kFloat;
+        const auto shape = fp4 ? std::vector<int64_t>{P, c.heads, groups, page} : std::vector<int64_t>{P, c.heads, page};
+        for (const at::Tensor *t : {&c.ks, &c.vs}) {
+            if (t->scalar_type() != st || t->sizes() != at::IntArrayRef(shape))
+                TORCH_CHECK_VALUE(false, "scales must be ", st, " ", at::IntArrayRef(shape));
+            const int last = (int)t->dim() - 1;
+            want(t->stride(last) == 1 && (!fp4 || t->stride(2) == page || groups == 1) &&
+                     (t->stride(1) == groups * page || c.heads == 1),
+                 "a page's scales must be dense");
+        }
+        want(c.ks.strides() == c.vs.strides(), "keys' and values' scales must be laid out alike");
+        c.scale_stride = ld(c.ks, c.heads * groups * page);
+    }
+    return c;
+}
+
 // ---- norm_rope(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
 //                k_cache, v_cache, slots) ----------------------------------------------------------
 
@@ -251,6 +313,99 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- norm_rope_quant(q, k, v, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
+//                      cache, slots) ----------------------------------------------------------------
+
+PyObject *norm_rope_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 13);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+                     &slots = tensor(a[12], "slots");
+    const at::Tensor qw = optional(a[3], "q_weight"), kw = optional(a[4], "k_weight"), freq = optional(a[5], "inv_freq"),
+                     pos = optional(a[6], "positions"), ko = optional(a[10], "k_out");
+    at::Tensor qo = optional(a[9], "q_out");
+    const double eps = real(a[7]);
+    const int interleaved = PyObject_IsTrue(a[8]);
+    if (interleaved < 0) throw python_error();
+    const Heads hq = heads_of(q, "q"), hk = heads_of(k, "k");
+    if (hk.code != hq.code || hk.rows != hq.rows || hk.D != hq.D)
+        TORCH_CHECK_VALUE(false, "k must be [", hq.rows, ", kv_heads, ", hq.D, "] of the queries' dtype");
+    same_heads(v, "v", hk);
+    if (qo.defined()) same_heads(qo, "q_out", hq);
+    if (ko.defined()) same_heads(ko, "k_out", hk);
+    if (qw.defined()) dense(qw, at::kFloat, hq.D, "q_weight");
+    if (kw.defined()) dense(kw, at::kFloat, hq.D, "k_weight");
+    int64_t rot = 0;
+    if (freq.defined()) {
+        rot = 2 * freq.numel();
+        dense(freq, at::kDouble, freq.numel(), "inv_freq");
+        want(pos.defined(), "positions are required");
+        dense(pos, at::kLong, hq.rows, "positions");
+    }
+    dense(slots, at::kLong, hq.rows, "slots");
+    const Kv c = kv_of(a[11], q.scalar_type(), hq.D, false);
+    want(c.heads == hk.heads, "the cache has another number of heads than k");
+    const Place at_(q);
+    if (!qo.defined()) qo = at::empty({hq.rows, hq.heads, hq.D}, q.options());
+    at_.same(k), at_.same(v), at_.same(qw), at_.same(kw), at_.same(freq), at_.same(qo), at_.same(ko), at_.same(slots);
+    if (freq.defined()) at_.same(pos);
+    c.same(at_);
+    check(w4a4_qk_norm_rope_quant(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), hq.code, size(hq.rows, "rows"), size(hq.heads, "heads"),
+        size(hk.heads, "kv_heads"), size(hq.D, "head_dim"), ld(q, hq.width()), ld(k, hk.width()), ld(v, hk.width()),
+        (const float *)ptr(qw), (const float *)ptr(kw), (float)eps, (const double *)ptr(freq), size(rot, "rot_dim"),
+        interleaved, freq.defined() ? (const int64_t *)ptr(pos) : nullptr, qo.data_ptr(), ld(qo, hq.width()), ptr(ko),
+        ko.defined() ? ld(ko, hk.width()) : 0, c.format, ptr(c.k), ptr(c.v), ptr(c.ks), ptr(c.vs), c.pages, c.page,
+        c.stride, c.scale_stride, (const int64_t *)ptr(slots), at_.stream()));
+    return THPVariable_Wrap(std::move(qo));
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- kv_append(k, v, cache, slots) ------------------------------------------------------------------
+
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 4);
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &slots = tensor(a[3], "slots");
+    const Heads h = heads_of(k, "k");
+    same_heads(v, "v", h);
+    dense(slots, at::kLong, h.rows, "slots");
+    const Kv c = kv_of(a[2], k.scalar_type(), h.D, false);
+    want(c.heads == h.heads, "the cache has another number of heads than k");
+    const Place at_(k);
+    at_.same(v), at_.same(slots), c.same(at_);
+    check(w4a4_kv_append_quant(k.data_ptr(), v.data_ptr(), h.code, size(h.rows, "rows"), size(h.heads, "kv_heads"),
+                               size(h.D, "head_dim"), ld(k, h.width()), ld(v, h.width()), c.format, ptr(c.k), ptr(c.v),
+                               ptr(c.ks), ptr(c.vs), c.pages, c.page, c.stride, c.scale_stride,
+                               (const int64_t *)ptr(slots), at_.stream()));
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- kv_read(cache, slots, k_out, v_out) --------------------------------------------------------------
+
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 4);
+    const at::Tensor &slots = tensor(a[1], "slots"), &ko = tensor(a[2], "k_out"), &vo = tensor(a[3], "v_out");
+    const Heads h = heads_of(ko, "k_out");
+    same_heads(vo, "v_out", h);
+    dense(slots, at::kLong, h.rows, "slots");
+    const Kv c = kv_of(a[0], ko.scalar_type(), h.D, false);
+    want(c.heads == h.heads, "the cache has another number of heads than k_out");
+    const Place at_(ko);
+    at_.same(vo), at_.same(slots), c.same(at_);
+    check(w4a4_kv_read_quant(c.format, ptr(c.k), ptr(c.v), ptr(c.ks), ptr(c.vs), c.pages, c.page, c.stride,
+                             c.scale_stride, (const int64_t *)ptr(slots), size(h.rows, "rows"),
+                             size(h.heads, "kv_heads"), size(h.D, "head_dim"), h.code, ko.data_ptr(),
+                             ld(ko, h.width()), vo.data_ptr(), ld(vo, h.width()), at_.stream()));
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 // ---- paged_attn(q, k_cache, v_cache, table, lens, scale, window, sinks, max_len, out, ws) --------
 
 PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
@@ -294,6 +449,137 @@ PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- attn_quant(q, cache, table, lens, scale, window, sinks, max_len, out, ws) ------------------------
+
+// What both calls over a cache of any format make of their queries, tables and lengths
+struct AttnCall {
+    const at::Tensor &q, &table, &lens;
+    at::Tensor out, ws;
+    Heads h;
+    Kv c;
+    int width, B, H, KV, D, max_len;
+    float scale;
+
+    AttnCall(PyObject *q_, PyObject *cache, PyObject *table_, PyObject *lens_, PyObject *scale_, PyObject *max_len_,
+             PyObject *out_, PyObject *ws_, bool sixteen)
+        : q(tensor(q_, "q")), table(tensor(table_, "table")), lens(tensor(lens_, "lens")), out(optional(out_, "out")),
+          ws(optional(ws_, "ws")), h(heads_of(q, "q")), c(kv_of(cache, q.scalar_type(), h.D, sixteen))
+    {
+        want(table.scalar_type() == at::kInt && table.dim() == 2 && table.size(0) == h.rows &&
+                 (table.stride(1) == 1 || table.size(1) == 1),
+             "table must be int32 [B, width]");
+        dense(lens, at::kInt, h.rows, "lens");
+        width = size(table.size(1), "table width");
+        scale = (float)(scale_ == Py_None ? 1.0 / std::sqrt((double)std::max<int64_t>(h.D, 1)) : real(scale_));
+        max_len = max_len_ == Py_None ? (int)std::min<int64_t>((int64_t)width * c.page, 1 << 30)
+                                      : (int)integer(max_len_, "max_len");
+        if (out.defined()) same_heads(out, "out", h);
+        B = size(h.rows, "B"), H = size(h.heads, "heads"), KV = size(c.heads, "kv_heads"), D = size(h.D, "head_dim");
+    }
+    void finish(const Place &at_, size_t need)
+    {
+        if (!out.defined()) out = at::empty({h.rows, h.heads, h.D}, q.options());
+        if (!ws.defined()) {
+            if (need) ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
+        } else {
+            want(ws.is_contiguous(), "ws must be contiguous");
+        }
+        at_.same(table), at_.same(lens), at_.same(out), at_.same(ws), c.same(at_);
+    }
+};
+
+PyObject *attn_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    AttnCall x(a[0], a[1], a[2], a[3], a[4], a[7], a[8], a[9], false);
+    const int window = (int)integer(a[5], "window"), sinks = (int)integer(a[6], "sinks");
+    const Place at_(x.q);
+    x.finish(at_, w4a4_paged_attn_quant_workspace_bytes(x.B, x.H, x.KV, x.D, x.max_len, window, sinks));
+    check(w4a4_paged_attn_decode_quant(
+        x.q.data_ptr(), x.h.code, x.B, x.H, x.KV, x.D, ld(x.q, x.h.width()), x.c.format, ptr(x.c.k), ptr(x.c.v),
+        ptr(x.c.ks), ptr(x.c.vs), x.c.pages, x.c.page, x.c.stride, x.c.scale_stride,
+        (const int32_t *)x.table.data_ptr(), x.width, ld(x.table, x.width), (const int32_t *)x.lens.data_ptr(),
+        x.max_len, x.scale, window, sinks, x.out.data_ptr(), ld(x.out, x.h.width()), ptr(x.ws),
+        x.ws.defined() ? (size_t)x.ws.nbytes() : 0, at_.stream()));
+    return THPVariable_Wrap(std::move(x.out));
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- attn_shared(q, cache, prefix_table, prefix_len, table, lens, scale, max_prefix, max_len, out, ws) --
+
+PyObject *attn_shared(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 11);
+    AttnCall x(a[0], a[1], a[4], a[5], a[6], a[8], a[9], a[10], true);
+    const at::Tensor &pt = tensor(a[2], "prefix_table"), &pl = tensor(a[3], "prefix_len");
+    want(pt.dim() == 1, "prefix_table must be 1-D");
+    dense(pt, at::kInt, pt.size(0), "prefix_table");
+    dense(pl, at::kInt, 1, "prefix_len");
+    const int pw = size(pt.size(0), "prefix table width");
+    const int max_prefix = a[7] == Py_None ? (int)std::min<int64_t>((int64_t)pw * x.c.page, 1 << 30)
+                                           : (int)integer(a[7], "max_prefix");
+    const Place at_(x.q);
+    x.finish(at_, w4a4_paged_attn_shared_workspace_bytes(x.B, x.H, x.KV, x.D, max_prefix, x.max_len));
+    at_.same(pt), at_.same(pl);
+    check(w4a4_paged_attn_shared(
+        x.q.data_ptr(), x.h.code, x.B, x.H, x.KV, x.D, ld(x.q, x.h.width()), x.c.format, ptr(x.c.k), ptr(x.c.v),
+        ptr(x.c.ks), ptr(x.c.vs), x.c.pages, x.c.page, x.c.stride, x.c.scale_stride, (const int32_t *)pt.data_ptr(), pw,
+        (const int32_t *)pl.data_ptr(), max_prefix, (const int32_t *)x.table.data_ptr(), x.width, ld(x.table, x.width),
+        (const int32_t *)x.lens.data_ptr(), x.max_len, x.scale, x.out.data_ptr(), ld(x.out, x.h.width()), ptr(x.ws),
+        x.ws.defined() ? (size_t)x.ws.nbytes() : 0, at_.stream()));
+    return THPVariable_Wrap(std::move(x.out));
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- adapter_add(Y, X, A, B, ids, scale, epilogue, residual, out, ws) ------------------------------------
+
+PyObject *adapter_add(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    const at::Tensor &Y = tensor(a[0], "Y"), &X = tensor(a[1], "X"), &A = tensor(a[2], "A"), &B = tensor(a[3], "B"),
+                     &ids = tensor(a[4], "ids");
+    const at::Tensor scale = optional(a[5], "scale"), res = optional(a[7], "residual");
+    at::Tensor out = optional(a[8], "out"), ws = optional(a[9], "ws");
+    const int epilogue = (int)integer(a[6], "epilogue"), dt = code_of(X, "X", false);
+    want(X.dim() == 2 && A.dim() == 3 && B.dim() == 3, "X must be 2-D, A and B 3-D");
+    const int64_t M = X.size(0), K = X.size(1), na = A.size(0), R = A.size(1), N = B.size(1);
+    want(X.stride(1) == 1 || K == 1, "X must have unit column stride");
+    if (A.size(2) != K || B.size(0) != na || B.size(2) != R || A.scalar_type() != X.scalar_type() ||
+        B.scalar_type() != X.scalar_type())
+        TORCH_CHECK_VALUE(false, "A must be ", X.scalar_type(), " [n, R, ", K, "] and B [n, N, R]");
+    want(A.stride(2) == 1 && (A.stride(1) == K || R == 1) && B.stride(2) == 1 && (B.stride(1) == R || N == 1),
+         "an adapter must be dense");
+    dense(ids, at::kInt, M, "ids");
+    if (scale.defined()) dense(scale, at::kFloat, na, "scale");
+    auto like_y = [&](const at::Tensor &t, const char *name) {
+        if (t.scalar_type() != X.scalar_type() || t.dim() != 2 || t.size(0) != M || t.size(1) != N ||
+            (t.stride(1) != 1 && N != 1))
+            TORCH_CHECK_VALUE(false, name, " must be ", X.scalar_type(), " [", M, ", ", N, "] with unit column stride");
+    };
+    like_y(Y, "Y");
+    if (out.defined()) like_y(out, "out");
+    if (res.defined()) like_y(res, "residual");
+    const int m = size(M, "M"), k = size(K, "K"), r = size(R, "R");
+    const Place at_(X);
+    if (!out.defined()) out = at::empty({M, N}, X.options());
+    const size_t need = w4a4_adapter_workspace_bytes(m, k, r);
+    if (!ws.defined()) {
+        if (need) ws = at::empty({(int64_t)need}, X.options().dtype(at::kByte));
+    } else {
+        want(ws.is_contiguous(), "ws must be contiguous");
+    }
+    at_.same(Y), at_.same(A), at_.same(B), at_.same(ids), at_.same(scale), at_.same(res), at_.same(out), at_.same(ws);
+    check(w4a4_adapter_add(X.data_ptr(), dt, m, k, ld(X, K), A.data_ptr(), ld(A, R * K), B.data_ptr(), ld(B, N * R),
+                           size(na, "n"), r, (const int32_t *)ids.data_ptr(), (const float *)ptr(scale), size(N, "N"),
+                           Y.data_ptr(), ld(Y, N), epilogue, ptr(res), res.defined() ? ld(res, N) : 0, out.data_ptr(),
+                           ld(out, N), ptr(ws), ws.defined() ? (size_t)ws.nbytes() : 0, at_.stream()));
+    return THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
 // ---- init(W4A4Error) ------------------------------------------------------------------------------
 
 PyObject *init(PyObject *, PyObject *cls)
@@ -309,6 +595,12 @@ template <typename F> PyCFunction fast(F f) { return reinterpret_cast<PyCFunctio
 PyMethodDef methods[] = {{"gemv", fast(gemv), METH_FASTCALL, nullptr},
                          {"norm_rope", fast(norm_rope), METH_FASTCALL, nullptr},
                          {"paged_attn", fast(paged_attn), METH_FASTCALL, nullptr},
+                         {"norm_rope_quant", fast(norm_rope_quant), METH_FASTCALL, nullptr},
+                         {"kv_append", fast(kv_append), METH_FASTCALL, nullptr},
+                         {"kv_read", fast(kv_read), METH_FASTCALL, nullptr},
+                         {"attn_quant", fast(attn_quant), METH_FASTCALL, nullptr},
+                         {"attn_shared", fast(attn_shared), METH_FASTCALL, nullptr},
+                         {"adapter_add", fast(adapter_add), METH_FASTCALL, nullptr},
                          {"init", init, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

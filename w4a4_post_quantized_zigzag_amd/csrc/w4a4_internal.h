@@ -227,6 +227,17 @@ int launch_gemv_w4g(const void *X, int x_dtype, int M, int K, int64_t ldx, const
                     const uint16_t *w_scale, int gshift, int N, uint16_t *Y, int64_t ldy, int epilogue,
                     const uint16_t *residual, int64_t ldr, hipStream_t s);
 
+// Quantized key-value cache (kv_quant.h): codes [kv_heads][page_size][D] (int8; fp4: D / 2 bytes) of page p at p *
+// page_stride bytes, scales [kv_heads][page_size] fp32 (fp4: [kv_heads][D / 32][page_size] bytes) at p * scale_stride
+// elements.
+struct KvPages {
+    uint8_t *k, *v;
+    void *k_scale, *v_scale;
+    int64_t page_stride, scale_stride;
+    int format;  // W4A4_KV_*
+    int num_pages, page_size, page_shift;
+};
+
 // single-token path between two linears (k_decode.hip); 16-bit elements, strides in elements
 struct NormRopeArgs {
     const uint16_t *q, *k, *v;
@@ -242,6 +253,7 @@ struct NormRopeArgs {
     int num_pages, page_size;
     int64_t page_stride;
     const int64_t *slots;  // [M]
+    KvPages kv;  // format other than W4A4_KV_16BIT: the append goes here instead of to k_cache, v_cache
     int waves_per_token, page_shift;  // set by the launcher
 };
 int launch_norm_rope(NormRopeArgs a, int dtype, bool interleaved, hipStream_t s);
@@ -257,12 +269,51 @@ struct AttnArgs {
     float2 *stat;  // [B][heads][splits] (maximum, sum)
     float *part;   // [B][heads][splits][D]
     int head_tiles;  // set by the launcher
+    // attention over a quantized cache or behind a shared prefix (k_kvq.hip): the cache in either format, and the
+    // parts of each (sequence, head) in stat and part are then prefix_splits of the prefix and `splits` of its own
+    KvPages kv;
+    const int32_t *prefix_table, *prefix_len;
+    int prefix_width, prefix_splits, prefix_tiles, prefix_row_waves, prefix_row_blocks;
 };
+// rows as they are into the quantized cache, and back (k_kvq.hip)
+struct KvRowsArgs {
+    uint16_t *k, *v;  // [M][kv_heads][D]; read-back: either may be nullptr
+    int64_t M, ldk, ldv;
+    int kv_heads, D;
+    const int64_t *slots;
+    KvPages kv;
+};
+int launch_kv_append(const KvRowsArgs &a, int dtype, hipStream_t s);
+int launch_kv_read(const KvRowsArgs &a, int dtype, hipStream_t s);
+
 struct AttnPlan {
     int splits, tiles_per_split, waves;
 };
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks);
 int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s);
+// How a shared prefix is cut: row tiles of 16 per wave, waves of a workgroup on different rows, row blocks, parts of
+// the keys and the least tiles of a part.
+struct PrefixPlan {
+    int rt, row_waves, row_blocks, splits, tiles;
+};
+PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix);
+int launch_kv_attn(AttnArgs a, int dtype, int D, int rt, hipStream_t s);
+
+// low-rank adapters (k_adapter.hip); 16-bit elements, strides in elements
+struct AdapterArgs {
+    const uint16_t *X, *A, *B, *Y, *residual;  // residual may be nullptr
+    uint16_t *out;
+    int64_t M, ldx, ldy, ldr, ldo, stride_a, stride_b;
+    int K, N, R, n;
+    const int32_t *ids;  // [M]
+    const float *scale;  // [n] or nullptr: ones
+    int epilogue, parts;
+    float *T;  // [parts][M][R]
+    int leads;      // set by the launcher
+    int64_t tile0;
+};
+int adapter_parts(int64_t M, int K);
+int launch_adapter(const AdapterArgs &a, int dtype, hipStream_t s);
 
 // calibration (k_calib.hip)
 size_t zigzag_workspace(int K);
