@@ -17,7 +17,7 @@
 
 namespace w4a4 {
 
-constexpr int AD_WAVES = 4;
+constexpr int IN_WAVES = 4, OUT_WAVES = 4;
 
 // The adapters of a tile's rows, one after another in the order of their first rows; this workgroup takes the `lead`-th,
 // `lead + leads`-th, ... of them. Rows without an adapter count as one more, with id -1.
@@ -51,17 +51,17 @@ struct AdapterWalk {
     }
 };
 
-template <int DT, int RT> __global__ __launch_bounds__(64 * AD_WAVES) void k_adapter_in(const AdapterArgs a)
+// U: steps of 32 k in flight
+template <int DT, int RT, int U> __global__ __launch_bounds__(64 * IN_WAVES) void k_adapter_in(const AdapterArgs a)
 {
-    constexpr int U = RT == 1 ? 8 : 4;  // steps of 32 k in flight
-    __shared__ float red[AD_WAVES][RT][64][4];
+    __shared__ float red[IN_WAVES][RT][64][4];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = blockIdx.x % a.parts, lead = blockIdx.x / a.parts % a.leads, r0 = blockIdx.z * 16 * RT;
     const int64_t m0 = (int64_t)(blockIdx.y + a.tile0) * 16;
     const uint16_t *x = a.X + min(m0 + r, a.M - 1) * a.ldx + 8 * g;
-    const int steps = (a.K + 31) / 32, per = (steps + a.parts * AD_WAVES - 1) / (a.parts * AD_WAVES);
-    const int s0 = (part * AD_WAVES + wave) * per, s1 = min(steps, s0 + per);
+    const int steps = (a.K + 31) / 32, per = (steps + a.parts * IN_WAVES - 1) / (a.parts * IN_WAVES);
+    const int s0 = (part * IN_WAVES + wave) * per, s1 = min(steps, s0 + per);
     const int most = a.K - 8 - 8 * g;  // the last run's k
     AdapterWalk walk;
     walk.start(a, m0);
@@ -106,11 +106,11 @@ template <int DT, int RT> __global__ __launch_bounds__(64 * AD_WAVES) void k_ada
             for (int i = 0; i < 4; ++i) red[wave][t][lane][i] = acc[t][i];
         __syncthreads();
         // entry (t, l, i): rank r0 + 16 t + 4 (l / 16) + i of row l % 16; R is a multiple of 8
-        for (int e = threadIdx.x; e < RT * 64; e += 64 * AD_WAVES) {
+        for (int e = threadIdx.x; e < RT * 64; e += 64 * IN_WAVES) {
             const int l = e % 64, t = e / 64, rank = r0 + 16 * t + l / 16 * 4;
             f4_t v = *reinterpret_cast<const f4_t *>(red[0][t][l]);
 #pragma unroll
-            for (int u = 1; u < AD_WAVES; ++u) v += *reinterpret_cast<const f4_t *>(red[u][t][l]);
+            for (int u = 1; u < IN_WAVES; ++u) v += *reinterpret_cast<const f4_t *>(red[u][t][l]);
             if (rank < a.R && (walk.rows >> (l % 16) & 1))
                 *reinterpret_cast<f4_t *>(a.T + ((int64_t)part * a.M + m0 + l % 16) * a.R + rank) = v;
         }
@@ -119,66 +119,128 @@ template <int DT, int RT> __global__ __launch_bounds__(64 * AD_WAVES) void k_ada
 
 __device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
-// A wave has 16 rows and 16 NT channels: operand row r of product t is channel 4 NT (r / 4) + 4 t + r % 4 of them, so
-// that a lane's results are 4 NT neighbouring channels of its row. Every row's inner products are its own adapter's,
-// whichever adapter the pass is for: they are made into operands once, and each pass keeps its own rows' columns.
-// J: blocks of 32 ranks.
-template <int DT, int J, int NT> __global__ __launch_bounds__(64 * AD_WAVES) void k_adapter_out(const AdapterArgs a)
+// Orders one wave's LDS writes and reads of other lanes' data (the hardware keeps a wave's LDS accesses in order; this
+// keeps the compiler from moving them).
+__device__ __forceinline__ void lds_fence()
 {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A wave has 16 rows and a block of 16 NT channels at a time. What limits it is not the bytes but the lines that its
+// loads touch: the matrix operands want neighbouring lanes in neighbouring rows, which is a line per lane (20 million
+// line accesses for 1600 rows of 64 ranks through 4099 channels, 35 us). So the block's weights, which are one run of
+// memory, are loaded as they lie there, LP lanes to a row of ranks, and pass through a corner of LDS of the wave's own
+// (rows padded to an odd number of 16-byte slots, free of bank conflicts on both sides); the results go back through
+// it, so that Y, the residual and the output are touched row by row as well.
+// Every row's inner products are its own adapter's, whichever adapter a pass is for: they are made into operands once,
+// and each pass keeps its own rows' columns.
+//  - WALK: the wave walks run_blocks blocks of channels, with the next block's Y and first adapter's weights on their
+//    way: few adapters per tile of rows, many tiles.
+//  - else it has one block, and the next adapter's weights are on their way: many adapters, few tiles.
+// What is on its way is asked for without branches (the last one once more at the end), for a wait behind a branch is
+// a wait for everything. LP: lanes to a row of weights, 8 LP >= R. SMALL: N below 8.
+template <int DT, int LP, bool WALK, bool SMALL>
+__global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArgs a)
+{
+    constexpr int NT = LP <= 8 ? 4 : LP == 16 ? 2 : 1, C = 16 * NT, J = LP < 4 ? 1 : LP / 4;
+    constexpr int SLOTS = LP + 1, LOADS = C * LP / 64;     // of weights per block
+    constexpr int CL = C / 8, IO = 16 * CL / 64 > 0 ? 16 * CL / 64 : 1;  // lanes to a row of Y, loads of 16 rows
+    constexpr int RES = C + 4;                              // floats between the rows of the results
+    constexpr int AREA = C * SLOTS * 16 > 16 * RES * 4 ? C * SLOTS * 16 : 16 * RES * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t area[OUT_WAVES][AREA];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // the waves of a workgroup are row_waves tiles of rows by AD_WAVES / row_waves blocks of channels
-    const int64_t tile = (int64_t)(blockIdx.y * a.row_waves + wave % a.row_waves) + a.tile0;
-    const int64_t m0 = tile * 16, m = m0 + r, mc = min(m, a.M - 1);
-    const int lead = blockIdx.x % a.leads;
-    const int n0 = (blockIdx.x / a.leads * (AD_WAVES / a.row_waves) + wave / a.row_waves) * 16 * NT;
-    if (n0 >= a.N || m0 >= a.M) return;
-    const int c0 = n0 + 4 * NT * g, live = a.N - c0;  // the lane's first channel, and how many there are
-    AdapterWalk walk;
-    walk.start(a, m0);
+    // The waves of a workgroup are row_waves tiles of rows by OUT_WAVES / row_waves runs of blocks. Consecutive
+    // workgroups go to different XCDs: a run of channels stays on one, whose L2 then reads its part of each B once.
+    const int unit = blockIdx.x / 8, lead = unit % a.leads, runs8 = (a.out_runs + 7) / 8;
+    const int run = unit / a.leads % runs8 * 8 + blockIdx.x % 8;
+    const int64_t tile = (int64_t)(unit / a.leads / runs8) * a.row_waves + wave % a.row_waves + a.tile0;
+    const int64_t m0 = tile * 16, mc = min(m0 + r, a.M - 1);
+    const int first = (run * (OUT_WAVES / a.row_waves) + wave / a.row_waves) * a.run_blocks * C;
+    const int end = min(a.N, first + a.run_blocks * C);
+    if (run >= a.out_runs || first >= end || m0 >= a.M) return;
+    u4_t *slots = reinterpret_cast<u4_t *>(area[wave]);
+    float *results = reinterpret_cast<float *>(area[wave]);
 
-    // all that does not depend on the adapter is asked for first
+    // all that does not depend on the adapter is asked for first: the rows' inner products, their part of Y, their ids
     float v[J][8];
-    {
-        const float *tp = a.T + mc * a.R + 8 * g;
-        const int64_t next = a.M * a.R;
+    const float *tp = a.T + mc * a.R + 8 * g;
+    auto inner = [&](int j, const float *t) {
+        const f4_t *q = reinterpret_cast<const f4_t *>(t + min(32 * j, a.R - 8 - 8 * g));
+        const f4_t x = q[0], y = q[1];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const f4_t *q = reinterpret_cast<const f4_t *>(tp + min(32 * j, a.R - 8 - 8 * g));
-            const f4_t x = q[0], y = q[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][i] = x[i], v[j][4 + i] = y[i];
-        }
-        for (int p = 1; p < a.parts; ++p) {
-            tp += next;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const f4_t *q = reinterpret_cast<const f4_t *>(tp + min(32 * j, a.R - 8 - 8 * g));
-                const f4_t x = q[0], y = q[1];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[j][i] += x[i], v[j][4 + i] += y[i];
-            }
-        }
-    }
-    const bool whole = live >= 4 * NT;
-    any2_t base[NT], add[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) base[t] = add[t] = any2_t{0, 0};
-    const uint16_t *yp = a.Y + mc * a.ldy + c0, *rp = a.residual ? a.residual + mc * a.ldr + c0 : nullptr;
-    auto load4 = [&](const uint16_t *p, int t) {  // channels 4 t .. 4 t + 3
-        any2_t x = {0, 0};
-        if (whole) return *reinterpret_cast<const any2_t *>(p + 4 * t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * t + i < live) x[i / 2] |= (uint32_t)p[4 * t + i] << (16 * (i % 2));
-        return x;
+        for (int i = 0; i < 4; ++i) v[j][i] += x[i], v[j][4 + i] += y[i];
     };
 #pragma unroll
-    for (int t = 0; t < NT; ++t) base[t] = load4(yp, t);
-    if (rp)
+    for (int j = 0; j < J; ++j) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) add[t] = load4(rp, t);
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+        inner(j, tp);
+    }
+    // as holder of Y: row lane / CL of each 64 / CL, eight channels from 8 (lane % CL)
+    const int ch = lane % CL * 8;
+    int64_t row[IO];
+    int rid[IO];
+#pragma unroll
+    for (int i = 0; i < IO; ++i) {
+        row[i] = min(m0 + min(i * (64 / CL) + lane / CL, 15), a.M - 1);
+        rid[i] = a.ids[row[i]];
+    }
+    struct Rows {
+        u4_t y[IO], z[IO];
+    };
+    const bool residual = a.residual != nullptr;
+    const uint16_t *zbase = residual ? a.residual : a.Y;
+    const int64_t ldz = residual ? a.ldr : a.ldy;
+    auto load_rows = [&](int n0, Rows &d) {
+        if constexpr (!SMALL) {
+            const int c = min(n0 + ch, a.N - 8);  // what reaches past N is read again, element by element
+#pragma unroll
+            for (int i = 0; i < IO; ++i) d.y[i] = load8_any(a.Y + row[i] * a.ldy + c);
+            if (residual)
+#pragma unroll
+                for (int i = 0; i < IO; ++i) d.z[i] = load8_any(zbase + row[i] * ldz + c);
+        }
+    };
+    Rows rows;
+    load_rows(first, rows);
+    AdapterWalk walk;
+    walk.start(a, m0);
+    float rscale[IO];
+    bool rhas[IO];
+#pragma unroll
+    for (int i = 0; i < IO; ++i) {
+        rhas[i] = (unsigned)rid[i] < (unsigned)a.n;
+        rscale[i] = rhas[i] && a.scale ? a.scale[rid[i]] : 1.0f;
+    }
+    // rows without an adapter that are already what they shall be need no pass
+    const bool idle = a.Y == a.out && a.ldy == a.ldo && a.epilogue == W4A4_EPI_NONE;
+    auto next_adapter = [&]() {
+        while (walk.next(a, lead))
+            if (walk.who >= 0 || !idle) return true;
+        return false;
+    };
+    if (!next_adapter()) return;
+    // as loader of weights: row lane / LP of each 64 / LP, eight ranks from 8 (lane % LP)
+    struct Weights {
+        u4_t w[LOADS];
+    };
+    const int wrank = min(lane % LP * 8, a.R - 8);
+    auto load_weights = [&](int n0, int who, Weights &d) {  // without an adapter the first one's, unused
+        const uint16_t *w = a.B + (int64_t)max(who, 0) * a.stride_b + wrank;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            d.w[i] = load8_any(w + (int64_t)min(n0 + i * (64 / LP) + lane / LP, a.N - 1) * a.R);
+    };
+    Weights w;
+    load_weights(first, walk.who, w);
 
+    for (int p = 1; p < a.parts; ++p) {
+        tp += a.M * a.R;
+#pragma unroll
+        for (int j = 0; j < J; ++j) inner(j, tp);
+    }
     u4_t hi[J], lo[J];
     float f[J];
 #pragma unroll
@@ -201,118 +263,165 @@ template <int DT, int J, int NT> __global__ __launch_bounds__(64 * AD_WAVES) voi
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hi[j][i] = pack16<DT>(v[j][2 * i], v[j][2 * i + 1]);
-            const uint32_t w = hi[j][i];
-            const f2_t h = unpack16<DT>(w);
+            const uint32_t x = pack16<DT>(v[j][2 * i], v[j][2 * i + 1]);
+            hi[j][i] = x;
+            const f2_t h = unpack16<DT>(x);
             // an infinity is whole in the first part
             lo[j][i] = pack16<DT>(fabsf(h.x) == INFINITY ? 0.0f : v[j][2 * i] - h.x,
                                   fabsf(h.y) == INFINITY ? 0.0f : v[j][2 * i + 1] - h.y);
         }
     }
 
-    float sum[NT][4], s = 0.0f;
+    f4_t sum[NT];
+    uint32_t met = 0;  // rows of the passes so far
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) sum[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](int who, uint32_t of, const Weights &d) {
+        met |= of;
+        const bool mine = who >= 0 && (of >> r & 1);
+        lds_fence();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
-    uint32_t kept = 0;  // rows that are this workgroup's to write
-    bool has = false;   // the lane's row has an adapter
-    int64_t wrow[NT];
+        for (int i = 0; i < LOADS; ++i) slots[(i * (64 / LP) + lane / LP) * SLOTS + lane % LP] = d.w[i];
+        lds_fence();
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        wrow[t] = (int64_t)min(n0 + 4 * NT * (r / 4) + 4 * t + r % 4, a.N - 1) * a.R + 8 * g;
-    while (walk.next(a, lead)) {
-        if (walk.who < 0) {
-            // rows without an adapter that are already what they shall be
-            if (!(a.Y == a.out && a.ldy == a.ldo && a.epilogue == W4A4_EPI_NONE)) kept |= walk.rows;
-            continue;
-        }
-        kept |= walk.rows;
-        const bool mine = walk.rows >> r & 1;
-        const uint16_t *w = a.B + (int64_t)walk.who * a.stride_b;
-        u4_t wv[J][NT];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+                // runs past R are zeros on both sides
+                u4_t x = slots[(16 * t + r) * SLOTS + (LP < 4 ? g % LP : 4 * j + g)];
+                if (32 * j + 8 * g >= a.R) x = u4_t{0, 0, 0, 0};
+                f4_t q = mma32<DT>(x, lo[j], f4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                q = mma32<DT>(x, hi[j], q);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) wv[j][t] = load8_any(w + wrow[t] + min(32 * j, a.R - 8 - 8 * g));
-        const float sc = a.scale ? a.scale[walk.who] : 1.0f;
-        if (mine) {
-            s = sc;
-            has = true;
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (32 * j + 32 > a.R && 32 * j + 8 * g >= a.R) wv[j][t] = u4_t{0, 0, 0, 0};
-                f4_t p = mma32<DT>(wv[j][t], lo[j], f4_t{0.0f, 0.0f, 0.0f, 0.0f});
-                p = mma32<DT>(wv[j][t], hi[j], p);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[t][i] = mine ? fmaf(p[i], f[j], sum[t][i]) : sum[t][i];
+                for (int i = 0; i < 4; ++i) sum[t][i] = mine ? fmaf(q[i], f[j], sum[t][i]) : sum[t][i];
             }
-    }
-    if (!(kept >> r & 1) || live <= 0) return;
-    uint16_t *out = a.out + m * a.ldo + c0;
-    auto finish = [&](float y, float x, float z) {
-        y = has ? fmaf(x, s, y) : y;
-        return a.epilogue == W4A4_EPI_GELU ? gelu_erf(y) : y + z;
     };
+    auto finish = [&](int i, float y, float x, float z) {
+        y = rhas[i] ? fmaf(x, rscale[i], y) : y;
+        return a.epilogue == W4A4_EPI_GELU ? gelu_erf(y) : residual ? y + z : y;
+    };
+    auto store = [&](int n0, const Rows &d) {
+        lds_fence();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const f2_t y0 = unpack16<DT>(base[t][0]), y1 = unpack16<DT>(base[t][1]);
-        const f2_t z0 = unpack16<DT>(add[t][0]), z1 = unpack16<DT>(add[t][1]);
-        const any2_t o = {pack16<DT>(finish(y0.x, sum[t][0], z0.x), finish(y0.y, sum[t][1], z0.y)),
-                          pack16<DT>(finish(y1.x, sum[t][2], z1.x), finish(y1.y, sum[t][3], z1.y))};
-        if (whole) {
-            *reinterpret_cast<any2_t *>(out + 4 * t) = o;
-        } else {
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f4_t *>(results + r * RES + 16 * t + 4 * g) = sum[t];
+        lds_fence();
+        const int c = n0 + ch;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (4 * t + i < live) out[4 * t + i] = (uint16_t)(o[i / 2] >> (16 * (i % 2)));
+        for (int i = 0; i < IO; ++i) {
+            const int q = i * (64 / CL) + lane / CL;  // row of the tile
+            const float *x = results + min(q, 15) * RES + ch;
+            const f4_t x0 = reinterpret_cast<const f4_t *>(x)[0], x1 = reinterpret_cast<const f4_t *>(x)[1];
+            if (q > 15 || !(met >> q & 1)) continue;
+            uint16_t *out = a.out + row[i] * a.ldo + c;
+            if (!SMALL && c + 8 <= a.N) {
+                u4_t o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t yw = d.y[i][e], zw = residual ? d.z[i][e] : 0u;
+                    const f2_t y = unpack16<DT>(yw), z = unpack16<DT>(zw);
+                    o[e] = pack16<DT>(finish(i, y.x, e < 2 ? x0[2 * e] : x1[2 * e - 4], z.x),
+                                      finish(i, y.y, e < 2 ? x0[2 * e + 1] : x1[2 * e - 3], z.y));
+                }
+                store8_any(out, o);
+            } else {
+                const uint16_t *y = a.Y + row[i] * a.ldy + c, *z = zbase + row[i] * ldz + c;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < a.N)
+                        out[e] = (uint16_t)pack16<DT>(finish(i, unpack16<DT>(y[e]).x, e < 4 ? x0[e] : x1[e - 4],
+                                                             unpack16<DT>(z[e]).x), 0.0f);
+            }
         }
+    };
+    if constexpr (WALK) {
+        const int who = walk.who, behind_count = walk.count;
+        const uint32_t of = walk.rows, behind = walk.left;
+        for (int n0 = first; n0 < end; n0 += C) {
+            const int n1 = n0 + C < end ? n0 + C : n0;
+            Rows rn;
+            Weights wn;
+            load_rows(n1, rn);
+            load_weights(n1, who, wn);
+            multiply(who, of, w);
+            walk.left = behind;
+            walk.count = behind_count;
+            while (next_adapter()) {  // the tile's other adapters
+                Weights more;
+                load_weights(n0, walk.who, more);
+                multiply(walk.who, walk.rows, more);
+            }
+            store(n0, rows);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sum[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            rows = rn;
+            w = wn;
+        }
+    } else {
+        bool more = true;
+        while (more) {
+            const int who = walk.who;
+            const uint32_t of = walk.rows;
+            more = next_adapter();
+            Weights next;
+            load_weights(first, walk.who, next);
+            multiply(who, of, w);
+            w = next;
+        }
+        store(first, rows);
     }
 }
 
-// Parts of K: 1024 k for the four waves of a workgroup, all loads of a wave in flight at once, while that leaves few
-// enough workgroups; every part is read again by each workgroup of the second launch.
+// Parts of K for the first launch: up to 1024 workgroups of active tiles, each wave at least 64 k; every part is read
+// again by each wave of the second launch.
 int adapter_parts(int64_t M, int K)
 {
     const int64_t tiles = (M + 15) / 16;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({16, (K + 1023) / 1024, 64 / std::max<int64_t>(tiles, 1)}));
+    if (tiles <= 16) return (int)std::clamp<int64_t>((K + 1023) / 1024, 1, 16);
+    return (int)std::clamp<int64_t>(std::min<int64_t>(512 / tiles, K / 512), 1, 16);
 }
 
-template <int DT, int J, int NT> static void run_out(AdapterArgs a, int64_t tiles, hipStream_t s)
+template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool walk, hipStream_t s)
 {
-    const int across = AD_WAVES / a.row_waves, blocks = (a.N + 16 * NT * across - 1) / (16 * NT * across);
-    hipLaunchKernelGGL((k_adapter_out<DT, J, NT>), dim3(blocks * a.leads, (tiles + a.row_waves - 1) / a.row_waves),
-                       dim3(64 * AD_WAVES), 0, s, a);
+    constexpr int C = 16 * (LP <= 8 ? 4 : LP == 16 ? 2 : 1);
+    a.leads = walk ? 1 : 4;
+    a.row_waves = walk ? 4 : 1;
+    const int across = OUT_WAVES / a.row_waves, blocks = (a.N + C - 1) / C;
+    const int64_t groups = (tiles + a.row_waves - 1) / a.row_waves;
+    a.run_blocks = walk ? (int)std::clamp<int64_t>((int64_t)blocks * groups * a.row_waves / 3072, 1, 16) : 1;
+    a.out_runs = (blocks + a.run_blocks * across - 1) / (a.run_blocks * across);
+    const dim3 grid((unsigned)((a.out_runs + 7) / 8 * 8 * a.leads * groups)), block(64 * OUT_WAVES);
+    if (a.N < 8) hipLaunchKernelGGL((k_adapter_out<DT, LP, false, true>), grid, block, 0, s, a);
+    else if (walk) hipLaunchKernelGGL((k_adapter_out<DT, LP, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_adapter_out<DT, LP, false, false>), grid, block, 0, s, a);
 }
 
-template <int DT, int J> static void pick_out(const AdapterArgs &a, int64_t tiles, hipStream_t s)
+template <int DT, int RT> static void run_in(const AdapterArgs &a, int64_t tiles, hipStream_t s)
 {
-    run_out<DT, J, J >= 4 ? 2 : 4>(a, tiles, s);
+    const dim3 grid(a.parts * a.leads, (unsigned)tiles, (a.R + 16 * RT - 1) / (16 * RT)), block(64 * IN_WAVES);
+    const int per = ((a.K + 31) / 32 + a.parts * IN_WAVES - 1) / (a.parts * IN_WAVES);  // a wave's steps
+    if (per <= 2) hipLaunchKernelGGL((k_adapter_in<DT, RT, 2>), grid, block, 0, s, a);
+    else if (per <= 4) hipLaunchKernelGGL((k_adapter_in<DT, RT, 4>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_adapter_in<DT, RT, 8>), grid, block, 0, s, a);
 }
 
 template <int DT> static int run_adapter(AdapterArgs a, hipStream_t s)
 {
     const int64_t tiles = (a.M + 15) / 16;
-    const int leads = tiles <= 16 ? 16 : tiles <= 128 ? 4 : 1;
-    const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-    for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += 32768) {
-        const unsigned y = (unsigned)std::min<int64_t>(32768, tiles - a.tile0);
-        a.leads = leads;
-        a.row_waves = 1;
-        const dim3 in(a.parts * a.leads, y, (a.R + 16 * rt - 1) / (16 * rt)), block(64 * AD_WAVES);
-        if (rt == 1) hipLaunchKernelGGL((k_adapter_in<DT, 1>), in, block, 0, s, a);
-        else if (rt == 2) hipLaunchKernelGGL((k_adapter_in<DT, 2>), in, block, 0, s, a);
-        else hipLaunchKernelGGL((k_adapter_in<DT, 4>), in, block, 0, s, a);
+    const bool many = tiles > 16;
+    // a launch holds less than 2^32 threads: at most 2^23 workgroups of 256
+    const int64_t most = std::clamp<int64_t>(((int64_t)1 << 23) / ((int64_t)a.N / 16 + 64) / 4 * 4, 4, 32768);
+    for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += most) {
+        const int64_t y = std::min<int64_t>(most, tiles - a.tile0);
+        a.leads = many ? 1 : 16;
+        if (a.R <= 16) run_in<DT, 1>(a, y, s);
+        else run_in<DT, 2>(a, y, s);
         if (int rc = check_launch("adapter_add inner")) return rc;
-        a.leads = tiles <= 16 ? 4 : 1;
-        a.row_waves = tiles > 16 ? 4 : 1;
-        if (a.R <= 32) pick_out<DT, 1>(a, y, s);
-        else if (a.R <= 64) pick_out<DT, 2>(a, y, s);
-        else if (a.R <= 128) pick_out<DT, 4>(a, y, s);
-        else pick_out<DT, 8>(a, y, s);
+        const bool walk = many && a.N >= 8;
+        if (a.R <= 16) run_out<DT, 2>(a, y, walk, s);
+        else if (a.R <= 32) run_out<DT, 4>(a, y, walk, s);
+        else if (a.R <= 64) run_out<DT, 8>(a, y, walk, s);
+        else if (a.R <= 128) run_out<DT, 16>(a, y, walk, s);
+        else run_out<DT, 32>(a, y, walk, s);
         if (int rc = check_launch("adapter_add")) return rc;
     }
     return W4A4_OK;

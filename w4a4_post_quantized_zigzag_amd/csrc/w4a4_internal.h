@@ -309,7 +309,7 @@ struct AdapterArgs {
     const float *scale;  // [n] or nullptr: ones
     int epilogue, parts;
     float *T;  // [parts][M][R]
-    int leads, row_waves;  // set by the launcher
+    int leads, row_waves, out_runs, run_blocks;  // set by the launcher
     int64_t tile0;
 };
 int adapter_parts(int64_t M, int K);
