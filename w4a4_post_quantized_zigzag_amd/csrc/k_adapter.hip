@@ -141,7 +141,8 @@ __device__ __forceinline__ void lds_fence()
 // What is on its way is asked for without branches (the last one once more at the end), for a wait behind a branch is
 // a wait for everything. LP: lanes to a row of weights, 8 LP >= R. SMALL: N below 8.
 template <int DT, int LP, bool WALK, bool SMALL>
-__global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArgs a)
+__global__ __launch_bounds__(64 * OUT_WAVES) __attribute__((amdgpu_waves_per_eu(LP < 8 ? 4 : LP == 8 ? 3 : 2)))
+void k_adapter_out(const AdapterArgs a)
 {
     constexpr int NT = LP <= 8 ? 4 : LP == 16 ? 2 : 1, C = 16 * NT, J = LP < 4 ? 1 : LP / 4;
     constexpr int SLOTS = LP + 1, LOADS = C * LP / 64;     // of weights per block
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArg
         rid[i] = a.ids[row[i]];
     }
     struct Rows {
-        u4_t y[IO], z[IO];
+        u4_t y[IO];
     };
     const bool residual = a.residual != nullptr;
     const uint16_t *zbase = residual ? a.residual : a.Y;
@@ -198,9 +199,6 @@ __global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArg
             const int c = min(n0 + ch, a.N - 8);  // what reaches past N is read again, element by element
 #pragma unroll
             for (int i = 0; i < IO; ++i) d.y[i] = load8_any(a.Y + row[i] * a.ldy + c);
-            if (residual)
-#pragma unroll
-                for (int i = 0; i < IO; ++i) d.z[i] = load8_any(zbase + row[i] * ldz + c);
         }
     };
     Rows rows;
@@ -289,7 +287,7 @@ __global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArg
             for (int j = 0; j < J; ++j) {
                 // runs past R are zeros on both sides
                 u4_t x = slots[(16 * t + r) * SLOTS + (LP < 4 ? g % LP : 4 * j + g)];
-                if (32 * j + 8 * g >= a.R) x = u4_t{0, 0, 0, 0};
+                if ((LP < 4 || a.R != 8 * LP) && 32 * j + 8 * g >= a.R) x = u4_t{0, 0, 0, 0};
                 f4_t q = mma32<DT>(x, lo[j], f4_t{0.0f, 0.0f, 0.0f, 0.0f});
                 q = mma32<DT>(x, hi[j], q);
 #pragma unroll
@@ -301,6 +299,10 @@ __global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArg
         return a.epilogue == W4A4_EPI_GELU ? gelu_erf(y) : residual ? y + z : y;
     };
     auto store = [&](int n0, const Rows &d) {
+        u4_t res[IO];
+        if (!SMALL && residual)
+#pragma unroll
+            for (int i = 0; i < IO; ++i) res[i] = load8_any(zbase + row[i] * ldz + min(n0 + ch, a.N - 8));
         lds_fence();
 #pragma unroll
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f4_t *>(results + r * RES + 16 * t + 4 * g) = sum[t];
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(64 * OUT_WAVES) void k_adapter_out(const AdapterArg
                 u4_t o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t yw = d.y[i][e], zw = residual ? d.z[i][e] : 0u;
+                    const uint32_t yw = d.y[i][e], zw = residual ? res[i][e] : 0u;
                     const f2_t y = unpack16<DT>(yw), z = unpack16<DT>(zw);
                     o[e] = pack16<DT>(finish(i, y.x, e < 2 ? x0[2 * e] : x1[2 * e - 4], z.x),
                                       finish(i, y.y, e < 2 ? x0[2 * e + 1] : x1[2 * e - 3], z.y));
