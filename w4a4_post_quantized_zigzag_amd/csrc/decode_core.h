@@ -114,6 +114,14 @@ template <typename F> __device__ __forceinline__ float across_groups(float x, F 
 constexpr int ATTN_WAVES = 4;   // waves of a workgroup, or one where there is little to do
 constexpr int ATTN_PAD = 4;     // floats between the heads' rows in LDS, against bank conflicts
 
+// Orders one wave's LDS writes and reads of other lanes' data (the hardware keeps a wave's LDS accesses in order; this
+// keeps the compiler from moving them).
+__device__ __forceinline__ void lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // N dwords from a 4-byte aligned address
 template <int N> struct __attribute__((aligned(4))) DwordRun {
     uint32_t v[N];

@@ -119,14 +119,6 @@ template <int DT, int RT, int U> __global__ __launch_bounds__(64 * IN_WAVES) voi
 
 __device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
-// Orders one wave's LDS writes and reads of other lanes' data (the hardware keeps a wave's LDS accesses in order; this
-// keeps the compiler from moving them).
-__device__ __forceinline__ void lds_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // A wave has 16 rows and a block of 16 NT channels at a time. What limits it is not the bytes but the lines that its
 // loads touch: the matrix operands want neighbouring lanes in neighbouring rows, which is a line per lane (20 million
 // line accesses for 1600 rows of 64 ranks through 4099 channels, 35 us). So the block's weights, which are one run of

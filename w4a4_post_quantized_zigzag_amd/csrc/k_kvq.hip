@@ -114,33 +114,6 @@ int launch_kv_read(const KvRowsArgs &a, int dtype, hipStream_t s) { return pick_
 // The parts that a run of T tiles is cut into: `per` tiles each, used of them
 __device__ __forceinline__ int tiles_per_part(int T, int splits, int least) { return max((T + splits - 1) / splits, least); }
 
-// Pages of tile t. A half without a visible key may have no page any more and reads the other half's; a page that
-// does not exist reads page 0 and poisons the result.
-__device__ __forceinline__ KvPlace look_up(const KvPages &c, const int32_t *table, int key0, int n, int from, int sinks,
-                                           bool &bad)
-{
-    KvPlace p;
-    p.key0 = key0;
-    bool any[2];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        const int lo = key0 + 16 * hf;
-        any[hf] = lo < n && (min(lo + 15, n - 1) >= from || lo < sinks);
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        const int lo = key0 + 16 * (any[hf] ? hf : 1 - hf);
-        int pid = __builtin_amdgcn_readfirstlane(table[lo >> c.page_shift]);
-        if ((unsigned)pid >= (unsigned)c.num_pages) {
-            bad = true;
-            pid = 0;
-        }
-        p.page[hf] = pid;
-        p.at[hf] = lo & (c.page_size - 1);
-    }
-    return p;
-}
-
 template <int DT, int D, int F>
 __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
 {
@@ -171,40 +144,49 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
     AttnRows<DT, D, F, 1> rows;
     rows.clear();
     // operand rows past the group repeat its last head; their results are not used
-    rows.load_q(0, a.q + (int64_t)b * a.ldq + (int64_t)(h0 + min(r, G - 1)) * D, g);
+    const bool flip = a.scale_log2 < 0.0f;
+    rows.load_q(0, a.q + (int64_t)b * a.ldq + (int64_t)(h0 + min(r, G - 1)) * D, g, flip);
+    const float scale = AttnRows<DT, D, F, 1>::scale_of(a);
     bool bad = tl.over;
     const int from = a.window > 0 ? n - a.window : 0;
     auto key_of = [&](int t) { return (t < tl.ns ? t : tl.w0 + t - tl.ns) * 32; };
+    auto is_whole = [&](int key0) { return key0 <= n - 32 && (key0 >= from || key0 + 32 <= a.sinks); };
 
-    int t = tl.over ? t1 : t0 + wave;
-    KvTile<DT, D, F> tile;
-    KvPlace at, next;
-    if (t < t1) {
-        at = look_up(a.kv, table, key_of(t), n, from, a.sinks, bad);
-        tile.load(a.kv, at, kvh, lane);
-        if (t + waves < t1) next = look_up(a.kv, table, key_of(t + waves), n, from, a.sinks, bad);
-    }
-    for (; t < t1; t += waves) {
-        const int key0 = at.key0;
-        const bool whole = key0 <= n - 32 && (key0 >= from || key0 + 32 <= a.sinks);
-        KvTile<DT, D, F> cur = tile;
-        if (t + waves < t1) {  // the next tile's loads, and the pages of the one behind it
-            at = next;
-            tile.load(a.kv, at, kvh, lane);
-            if (t + 2 * waves < t1) next = look_up(a.kv, table, key_of(t + 2 * waves), n, from, a.sinks, bad);
+    typedef KvStage<D, F, 64> Stage;
+    uint8_t *stage = reinterpret_cast<uint8_t *>(sm) + wave * Stage::BYTES;
+    const int count = tl.over ? 0 : (t1 - t0 - wave + waves - 1) / waves;  // this wave's tiles
+    for (int base = 0; base < count; base += 64) {
+        const int some = min(64, count - base);
+        KvPlaces places;
+        places.look_up<D, F>(a.kv, table, key_of(t0 + wave + (base + min(lane, some - 1)) * waves), n, from, a.sinks, kvh, bad);
+        KvTile<DT, D, F> tile;
+        Stage keys;
+        KvPlace at = places.get<F>(0);
+        keys.load(a.kv.k, at, lane);
+        tile.template load<false>(a.kv, at, lane);
+        for (int i = 0; i < some; ++i) {
+            const int key0 = at.key0;
+            lds_fence();
+            keys.commit(stage, lane);
+            lds_fence();
+            KvTile<DT, D, F> cur = tile;
+            cur.keys_from(stage, lane);
+            // the next tile is asked for (the last one again), without a branch: behind one the wait for this tile would
+            // be a wait for that, too
+            at = places.get<F>(min(i + 1, some - 1));
+            keys.load(a.kv.k, at, lane);
+            tile.template load<false>(a.kv, at, lane);
+            rows.template add<true>(cur, is_whole(key0), [&](int e) {
+                const int key = key0 + 16 * (e / 4) + 4 * g + e % 4;
+                return key < n && (key >= from || key < a.sinks);
+            }, scale);
         }
-        bool ok[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int key = key0 + 16 * (e / 4) + 4 * g + e % 4;
-            ok[e] = key < n && (key >= from || key < a.sinks);
-        }
-        rows.add(cur, whole, ok, a.scale_log2);
     }
     float sum = rows.total(0);
     if (__any(bad)) sum = NAN;
 
     // ---- join the waves: maximum [W][16], sum [W][16], channels [W][G][D + pad] ----
+    __syncthreads();  // the keys' rows make room
     float *wm = sm, *ws = sm + waves * 16, *wa = sm + waves * 32;
     constexpr int LD = D + ATTN_PAD;
     if (g == 0) {
@@ -252,6 +234,145 @@ __device__ __forceinline__ int prefix_tiles(const AttnArgs &a, bool &over)
     return over ? 1 : n <= 0 ? 0 : (int)(((int64_t)n + 31) >> 5);
 }
 
+// The prefix for many rows: the four waves of a workgroup have RT row tiles each and share the tile of keys, which
+// passes through LDS, two tiles in turn. The scales of quantized rows come along: fp32 [2][32] of keys and values, or
+// bytes [2][D / 32][32].
+template <int DT, int D, int F, int RT>
+__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix_rows(const AttnArgs a)
+{
+    typedef KvShape<D, F> S;
+    typedef KvStage<D, F, 64 * ATTN_WAVES> Stage;
+    constexpr int SCALES = F == W4A4_KV_16BIT ? 0 : 2 * 32 * (F == W4A4_KV_INT8 ? 4 : D / 32);
+    constexpr int BUF = 2 * Stage::BYTES + SCALES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][BUF];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // all row blocks of one (head, part) run on one XCD
+    const int unit = blockIdx.x / (8 * a.prefix_row_blocks) * 8 + blockIdx.x % 8;
+    const int block = blockIdx.x / 8 % a.prefix_row_blocks;
+    const int kvh = unit / a.prefix_splits, split = unit % a.prefix_splits;
+    if (kvh >= a.kv_heads) return;
+    const int group = a.heads / a.kv_heads;
+    const int64_t total = (int64_t)a.B * group, row0 = ((int64_t)block * ATTN_WAVES + wave) * 16 * RT;
+    bool bad;
+    const int T = prefix_tiles(a, bad), n = bad ? 0 : a.prefix_len[0];
+    const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+    const int t0 = split * per, t1 = min(T, t0 + per);
+    if (t0 >= t1) return;
+
+    AttnRows<DT, D, F, RT> rows;
+    rows.clear();
+    auto place = [&](int t, int64_t &b, int &h) {  // row r of row tile t
+        const int64_t row = min(row0 + 16 * t + r, total - 1);
+        b = row / group;
+        h = kvh * group + (int)(row - b * group);
+    };
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        int64_t b;
+        int h;
+        place(t, b, h);
+        rows.load_q(t, a.q + b * a.ldq + (int64_t)h * D, g, a.scale_log2 < 0.0f);
+    }
+    const float scale = AttnRows<DT, D, F, 1>::scale_of(a);
+    if (!bad) {
+        Stage k, v;
+        uint32_t sc = 0;
+        // the thread's dword of the scales: key's or value's, group, first key (fp4: of four)
+        constexpr int PER = F == W4A4_KV_INT8 ? 32 : 8, GROUPS = F == W4A4_KV_INT8 ? 1 : D / 32;
+        const int sv = tid / (PER * GROUPS), sg = tid / PER % GROUPS, sk = tid % PER * (32 / PER);
+        auto load = [&](const KvPlace &at) {
+            k.load(a.kv.k, at, tid);
+            v.load(a.kv.v, at, tid);
+            if (F != W4A4_KV_16BIT && sv < 2) {
+                const void *p = sv ? a.kv.v_scale : a.kv.k_scale;
+                const int64_t i = (sk < 16 ? at.scales[0] : at.scales[1]) + sg * a.kv.page_size + sk % 16;
+                sc = F == W4A4_KV_INT8 ? reinterpret_cast<const uint32_t *>(p)[i]
+                                       : *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(p) + i);
+            }
+        };
+        // what is past the end becomes zeros; its scales finite, and a key's not 0, which would turn its -inf into a NaN
+        auto commit = [&](int t, uint8_t *to) {
+            const int live = n - t * 32;
+            if (live >= 32) {
+                k.commit(to, tid);
+                v.commit(to + Stage::BYTES, tid);
+            } else {
+                k.commit(to, tid, live);
+                v.commit(to + Stage::BYTES, tid, live);
+            }
+            if (F != W4A4_KV_16BIT && sv < 2) {
+                uint32_t x = sc;
+                if constexpr (F == W4A4_KV_INT8) {
+                    if (sk >= live) x = sv ? 0u : 0x3F800000u;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (sk + i >= live) x = (x & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
+                }
+                reinterpret_cast<uint32_t *>(to + 2 * Stage::BYTES)[tid] = x;
+            }
+        };
+        for (int base = t0; base < t1; base += 64) {
+        const int some = min(64, t1 - base);
+        KvPlaces places;
+        places.look_up<D, F>(a.kv, a.prefix_table, (base + min(lane, some - 1)) * 32, n, 0, 0, kvh, bad);
+        load(places.get<F>(0));
+        commit(base, lds[0]);
+        __syncthreads();
+        for (int i = 0; i < some; ++i) {
+            const int t = base + i;
+            const uint8_t *now = lds[i & 1];
+            load(places.get<F>(min(i + 1, some - 1)));
+            if (row0 < total) {
+                KvTile<DT, D, F> tile;
+                tile.keys_from(now, lane);
+                const uint8_t *scales = now + 2 * Stage::BYTES;
+                if constexpr (F == W4A4_KV_INT8) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        tile.ks[hf] = reinterpret_cast<const float4 *>(scales)[4 * hf + g];
+                        tile.vs[hf] = reinterpret_cast<const float4 *>(scales)[8 + 4 * hf + g];
+                    }
+                } else if constexpr (F == W4A4_KV_FP4) {
+                    const int vg = (S::VE * r < D ? S::VE * r : 0) / 32;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                        for (int l = 0; l < S::NL; ++l)
+                            tile.kb[hf][l] = scales[S::channel(l * S::NR, g) / 32 * 32 + 16 * hf + r];
+                        tile.vb[hf] = reinterpret_cast<const uint32_t *>(scales + D + vg * 32 + 16 * hf)[g];
+                    }
+                }
+                tile.values_from(now + Stage::BYTES, lane);
+                rows.template add<false>(tile, t * 32 <= n - 32,
+                                    [&](int e) { return t * 32 + 16 * (e / 4) + 4 * g + e % 4 < n; }, scale);
+            }
+            if (i + 1 < some) commit(t + 1, lds[(i + 1) & 1]);
+            __syncthreads();
+        }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        float sum = rows.total(t);
+        if (__any(bad)) sum = NAN;
+        if (row0 + 16 * t + r >= total) continue;
+        int64_t b;
+        int h;
+        place(t, b, h);
+        const int64_t part = (b * a.heads + h) * (a.prefix_splits + a.splits) + split;
+        if (g == 0) a.stat[part] = make_float2(rows.mx[t], sum);
+        float *dst = a.part + part * D;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (S::VE * 16 == D || S::VE * (4 * g + x) < D)
+#pragma unroll
+                for (int i = 0; i < S::VE; ++i) dst[S::VE * (4 * g + x) + i] = rows.acc[t][i][x];
+    }
+}
+
+// The prefix for few rows: each wave loads its own tiles.
 template <int DT, int D, int F, int RT>
 __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix(const AttnArgs a)
 {
@@ -286,18 +407,23 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix(const AttnArgs 
         int64_t b;
         int h;
         place(t, b, h);
-        rows.load_q(t, a.q + b * a.ldq + (int64_t)h * D, g);
+        rows.load_q(t, a.q + b * a.ldq + (int64_t)h * D, g, a.scale_log2 < 0.0f);
     }
+    const float scale = AttnRows<DT, D, F, 1>::scale_of(a);
     if (!bad) {
-        KvTile<DT, D, F> tile;
-        for (int t = t0; t < t1; ++t) {
-            const int key0 = t * 32;
-            const KvPlace at = look_up(a.kv, a.prefix_table, key0, n, 0, 0, bad);
-            tile.load(a.kv, at, kvh, lane);
-            bool ok[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ok[e] = key0 + 16 * (e / 4) + 4 * g + e % 4 < n;
-            rows.add(tile, key0 <= n - 32, ok, a.scale_log2);
+        for (int base = t0; base < t1; base += 64) {
+            const int some = min(64, t1 - base);
+            KvPlaces places;
+            places.look_up<D, F>(a.kv, a.prefix_table, (base + min(lane, some - 1)) * 32, n, 0, 0, kvh, bad);
+            KvTile<DT, D, F> tile;
+            tile.template load<true>(a.kv, places.get<F>(0), lane);
+            for (int i = 0; i < some; ++i) {
+                const int key0 = (base + i) * 32;
+                KvTile<DT, D, F> cur = tile;
+                tile.template load<true>(a.kv, places.get<F>(min(i + 1, some - 1)), lane);
+                rows.template add<true>(cur, key0 <= n - 32,
+                                        [&](int e) { return key0 + 16 * (e / 4) + 4 * g + e % 4 < n; }, scale);
+            }
         }
     }
 #pragma unroll
@@ -414,12 +540,14 @@ template <int DT, int D, int F> static int run_kv_attn(const AttnArgs &a, int rt
         const int wk = ATTN_WAVES / a.prefix_row_waves;
         const int64_t units = (int64_t)a.kv_heads * (a.prefix_splits / wk);
         const dim3 grid((unsigned)((units + 7) / 8 * 8 * a.prefix_row_blocks));
-        if (rt == 2) hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 2>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
-        else hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 1>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
+        const dim3 block(64 * ATTN_WAVES);
+        if (wk > 1) hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 1>), grid, block, 0, s, a);
+        else if (rt == 2) hipLaunchKernelGGL((k_attn_prefix_rows<DT, D, F, 2>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_attn_prefix_rows<DT, D, F, 1>), grid, block, 0, s, a);
         if ((rc = check_launch("paged_attn prefix"))) return rc;
     }
     const int G = std::min(16, a.heads / a.kv_heads);
-    const size_t lds = (size_t)a.waves * (32 + G * (D + ATTN_PAD)) * sizeof(float);
+    const size_t lds = a.waves * std::max<size_t>((32 + G * (D + ATTN_PAD)) * sizeof(float), KvStage<D, F, 64>::BYTES);
     if (lds > 65536 &&  // more than every kernel gets unasked
         (rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_own<DT, D, F>), lds, "paged_attn")))
         return rc;
