@@ -1431,7 +1431,7 @@ static KvAttnPlan kv_attn_plan(int B, int heads, int kv_heads, int head_dim, boo
                                int window, int sinks)
 {
     KvAttnPlan p{};
-    p.own = attn_plan(B, heads, kv_heads, max_len, window, sinks);
+    p.own = kv_plan(B, heads, kv_heads, max_len, window, sinks, shared);
     if (shared) {
         p.prefix = prefix_plan(B, heads, kv_heads, max_prefix);
         p.own.splits = std::min(p.own.splits, 128);  // the join weighs 256 parts at most

@@ -1,6 +1,7 @@
 // The quantized key-value cache: rows into it and back, the attention of one new token per sequence over it, and the
 // same attention behind a prefix that all sequences of a batch share (over a quantized or a 16-bit cache).
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kv_tile.h"
@@ -114,16 +115,16 @@ int launch_kv_read(const KvRowsArgs &a, int dtype, hipStream_t s) { return pick_
 // The parts that a run of T tiles is cut into: `per` tiles each, used of them
 __device__ __forceinline__ int tiles_per_part(int T, int splits, int least) { return max((T + splits - 1) / splits, least); }
 
+// A workgroup's part of one sequence's own tokens for up to 16 of the heads that share a key/value head.
 template <int DT, int D, int F>
-__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
+__device__ __forceinline__ void own_tokens(const AttnArgs &a, const int id, float *sm)
 {
     typedef KvShape<D, F> S;
-    extern __shared__ float sm[];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     // all heads of one (sequence, split) run on one XCD, and the sequences move on by one XCD from split to split
     const int hts = a.kv_heads * a.head_tiles;
-    const int unit = blockIdx.x / (8 * hts) * 8 + blockIdx.x % 8, head = blockIdx.x / 8 % hts;
+    const int unit = id / (8 * hts) * 8 + id % 8, head = id / 8 % hts;
     const int split = unit / a.B, b = (unit + split) % a.B;
     const int kvh = head / a.head_tiles, ht = head % a.head_tiles;
     if (split >= a.splits) return;
@@ -226,6 +227,12 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
     }
 }
 
+template <int DT, int D, int F> __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_own(const AttnArgs a)
+{
+    extern __shared__ float sm[];
+    own_tokens<DT, D, F>(a, blockIdx.x, sm);
+}
+
 // Tiles of the prefix: none, or one logical tile that poisons where the table cannot hold it.
 __device__ __forceinline__ int prefix_tiles(const AttnArgs &a, bool &over)
 {
@@ -237,19 +244,23 @@ __device__ __forceinline__ int prefix_tiles(const AttnArgs &a, bool &over)
 // The prefix for many rows: the four waves of a workgroup have RT row tiles each and share the tile of keys, which
 // passes through LDS, two tiles in turn. The scales of quantized rows come along: fp32 [2][32] of keys and values, or
 // bytes [2][D / 32][32].
+template <int D, int F> constexpr int prefix_buffer()
+{
+    return 2 * KvStage<D, F, 64 * ATTN_WAVES>::BYTES +
+           (F == W4A4_KV_16BIT ? 0 : 2 * 32 * (F == W4A4_KV_INT8 ? 4 : D / 32));
+}
+
 template <int DT, int D, int F, int RT>
-__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix_rows(const AttnArgs a)
+__device__ __forceinline__ void prefix_many(const AttnArgs &a, const int id, uint8_t *lds)
 {
     typedef KvShape<D, F> S;
     typedef KvStage<D, F, 64 * ATTN_WAVES> Stage;
-    constexpr int SCALES = F == W4A4_KV_16BIT ? 0 : 2 * 32 * (F == W4A4_KV_INT8 ? 4 : D / 32);
-    constexpr int BUF = 2 * Stage::BYTES + SCALES;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][BUF];
+    constexpr int BUF = prefix_buffer<D, F>();
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // all row blocks of one (head, part) run on one XCD
-    const int unit = blockIdx.x / (8 * a.prefix_row_blocks) * 8 + blockIdx.x % 8;
-    const int block = blockIdx.x / 8 % a.prefix_row_blocks;
+    const int unit = id / (8 * a.prefix_row_blocks) * 8 + id % 8;
+    const int block = id / 8 % a.prefix_row_blocks;
     const int kvh = unit / a.prefix_splits, split = unit % a.prefix_splits;
     if (kvh >= a.kv_heads) return;
     const int group = a.heads / a.kv_heads;
@@ -318,11 +329,11 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix_rows(const Attn
         KvPlaces places;
         places.look_up<D, F>(a.kv, a.prefix_table, (base + min(lane, some - 1)) * 32, n, 0, 0, kvh, bad);
         load(places.get<F>(0));
-        commit(base, lds[0]);
+        commit(base, lds);
         __syncthreads();
         for (int i = 0; i < some; ++i) {
             const int t = base + i;
-            const uint8_t *now = lds[i & 1];
+            const uint8_t *now = lds + (i & 1) * BUF;
             load(places.get<F>(min(i + 1, some - 1)));
             if (row0 < total) {
                 KvTile<DT, D, F> tile;
@@ -348,7 +359,7 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix_rows(const Attn
                 rows.template add<false>(tile, t * 32 <= n - 32,
                                     [&](int e) { return t * 32 + 16 * (e / 4) + 4 * g + e % 4 < n; }, scale);
             }
-            if (i + 1 < some) commit(t + 1, lds[(i + 1) & 1]);
+            if (i + 1 < some) commit(t + 1, lds + ((i + 1) & 1) * BUF);
             __syncthreads();
         }
         }
@@ -373,16 +384,15 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix_rows(const Attn
 }
 
 // The prefix for few rows: each wave loads its own tiles.
-template <int DT, int D, int F, int RT>
-__global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix(const AttnArgs a)
+template <int DT, int D, int F, int RT> __device__ __forceinline__ void prefix_few(const AttnArgs &a, const int id)
 {
     typedef KvShape<D, F> S;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // wr waves on row tiles, the others on other keys; all row blocks of one (head, part) run on one XCD
     const int wr = a.prefix_row_waves, wk = ATTN_WAVES / wr;
-    const int unit = blockIdx.x / (8 * a.prefix_row_blocks) * 8 + blockIdx.x % 8;
-    const int block = blockIdx.x / 8 % a.prefix_row_blocks;
+    const int unit = id / (8 * a.prefix_row_blocks) * 8 + id % 8;
+    const int block = id / 8 % a.prefix_row_blocks;
     const int parts = a.prefix_splits / wk;
     const int kvh = unit / parts, split = unit % parts * wk + wave / wr;
     if (kvh >= a.kv_heads) return;
@@ -443,6 +453,25 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_prefix(const AttnArgs 
 #pragma unroll
                 for (int i = 0; i < S::VE; ++i) dst[S::VE * (4 * g + x) + i] = rows.acc[t][i][x];
     }
+}
+
+// The prefix and the sequences' own tokens in one launch: the one is bound by the matrix cores, the other by memory. Eight
+// workgroups (one on each XCD) of the one and of the other take turns, and change places after every 32 turns, so that
+// neither keeps to the same CUs. RT 0: few rows.
+template <int DT, int D, int F, int RT> __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_shared(const AttnArgs a)
+{
+    extern __shared__ float sm[];
+    const int turn = blockIdx.x / 8, xcd = blockIdx.x % 8, both = 2 * min(a.prefix_turns, a.own_turns);
+    bool prefix = a.prefix_turns > a.own_turns;
+    int id = turn - both / 2;
+    if (turn < both) {
+        prefix = ((turn + (turn / 2 / 16)) & 1) == 0;
+        id = turn / 2;
+    }
+    id = id * 8 + xcd;
+    if (!prefix) own_tokens<DT, D, F>(a, id, sm);
+    else if constexpr (RT == 0) prefix_few<DT, D, F, 1>(a, id);
+    else prefix_many<DT, D, F, RT>(a, id, reinterpret_cast<uint8_t *>(sm));
 }
 
 // out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the parts that had tiles, one workgroup per
@@ -517,44 +546,76 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const Att
     }
 }
 
+static int envi(const char*n,int d){const char*e=getenv(n);return e?atoi(e):d;}
+AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks, bool shared)
+{
+    const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;
+    int64_t tiles = ((int64_t)max_len + 31) / 32;
+    if ((int64_t)window + sinks >= max_len) window = 0;  // it hides nothing
+    if (window > 0)  // a run of w keys touches at most w / 32 + 2 tiles
+        tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
+    tiles = std::max<int64_t>(tiles, 1);
+    const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
+    if (tiles <= std::clamp<int64_t>(rows / 4, 8, envi("KV_ALONE",32))) return {1, (int)tiles, ATTN_WAVES};
+    AttnPlan p;
+    p.waves = !shared && rows * tiles <= envi("KV_ONE",512) && tiles <= 96 ? 1 : ATTN_WAVES;
+    int64_t want = tiles;
+    if (p.waves > 1) {
+        const int workgroups = shared ? envi("SH_WANT", 1024) : envi("KV_WANT", window > 0 ? 1024 : B <= 2 ? 512 : 2048);
+        want = std::min<int64_t>(std::max<int64_t>(workgroups / rows, 1), 256);
+    }
+    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, p.waves * (p.waves > 1 ? envi("KV_MIN", 2) : 1));
+    p.splits = (int)((tiles + p.tiles_per_split - 1) / p.tiles_per_split);
+    p.tiles_per_split = std::min(p.tiles_per_split, envi("KV_LEAST", 1<<30));
+    return p;
+}
+
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
 {
     PrefixPlan p;
     const int64_t rows = (int64_t)std::max(B, 1) * (heads / kv_heads), row_tiles = (rows + 15) / 16;
     const int64_t tiles = std::max<int64_t>(((int64_t)max_prefix + 31) / 32, 1);
-    p.rt = row_tiles > 4 ? 2 : 1;
+    p.rt = row_tiles > envi("PF_RT",4) ? 2 : 1;
     const int64_t wave_rows = (row_tiles + p.rt - 1) / p.rt;
     p.row_waves = wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;
     p.row_blocks = (int)((wave_rows + p.row_waves - 1) / p.row_waves);
     const int wk = ATTN_WAVES / p.row_waves;
-    const int64_t want = std::max<int64_t>(512 / (p.row_blocks * (int64_t)kv_heads), 1);  // workgroups of a head's keys
+    const int64_t want = std::max<int64_t>(envi("PF_WANT",256) / (p.row_blocks * (int64_t)kv_heads), 1);  // workgroups of a head's keys
     p.splits = (int)std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(want, (tiles + wk - 1) / wk), 1), 128 / wk) * wk;
     p.tiles = 1;
     return p;
 }
 
-template <int DT, int D, int F> static int run_kv_attn(const AttnArgs &a, int rt, hipStream_t s)
+template <int DT, int D, int F, int RT> static int run_shared(const AttnArgs &a, size_t lds, hipStream_t s)
+{
+    if constexpr (RT > 0) lds = std::max<size_t>(lds, 2 * prefix_buffer<D, F>());
+    if (lds > 65536)  // more than every kernel gets unasked
+        if (int rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_shared<DT, D, F, RT>), lds, "paged_attn_shared"))
+            return rc;
+    hipLaunchKernelGGL((k_attn_shared<DT, D, F, RT>), dim3(8 * (unsigned)(a.prefix_turns + a.own_turns)),
+                       dim3(64 * ATTN_WAVES), lds, s, a);
+    return check_launch("paged_attn_shared");
+}
+
+template <int DT, int D, int F> static int run_kv_attn(AttnArgs a, int rt, hipStream_t s)
 {
     int rc;
-    if (a.prefix_splits) {
-        const int wk = ATTN_WAVES / a.prefix_row_waves;
-        const int64_t units = (int64_t)a.kv_heads * (a.prefix_splits / wk);
-        const dim3 grid((unsigned)((units + 7) / 8 * 8 * a.prefix_row_blocks));
-        const dim3 block(64 * ATTN_WAVES);
-        if (wk > 1) hipLaunchKernelGGL((k_attn_prefix<DT, D, F, 1>), grid, block, 0, s, a);
-        else if (rt == 2) hipLaunchKernelGGL((k_attn_prefix_rows<DT, D, F, 2>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_attn_prefix_rows<DT, D, F, 1>), grid, block, 0, s, a);
-        if ((rc = check_launch("paged_attn prefix"))) return rc;
-    }
     const int G = std::min(16, a.heads / a.kv_heads);
     const size_t lds = a.waves * std::max<size_t>((32 + G * (D + ATTN_PAD)) * sizeof(float), KvStage<D, F, 64>::BYTES);
-    if (lds > 65536 &&  // more than every kernel gets unasked
-        (rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_own<DT, D, F>), lds, "paged_attn")))
-        return rc;
-    const int64_t units = ((int64_t)a.B * a.splits + 7) / 8 * 8;
-    hipLaunchKernelGGL((k_attn_own<DT, D, F>), dim3((unsigned)(units * a.kv_heads * a.head_tiles)), dim3(64 * a.waves), lds,
-                       s, a);
-    if ((rc = check_launch("paged_attn")) || (a.splits == 1 && !a.prefix_splits)) return rc;
+    a.own_turns = (int)(((int64_t)a.B * a.splits + 7) / 8 * a.kv_heads * a.head_tiles);
+    if (a.prefix_splits) {
+        const int wk = ATTN_WAVES / a.prefix_row_waves;
+        a.prefix_turns = (int)(((int64_t)a.kv_heads * (a.prefix_splits / wk) + 7) / 8 * a.prefix_row_blocks);
+        rc = wk > 1    ? run_shared<DT, D, F, 0>(a, lds, s)
+             : rt == 2 ? run_shared<DT, D, F, 2>(a, lds, s)
+                       : run_shared<DT, D, F, 1>(a, lds, s);
+        if (rc) return rc;
+    } else {
+        if (lds > 65536 && (rc = ensure_dynamic_lds(reinterpret_cast<const void *>(&k_attn_own<DT, D, F>), lds, "paged_attn")))
+            return rc;
+        hipLaunchKernelGGL((k_attn_own<DT, D, F>), dim3(8 * (unsigned)a.own_turns), dim3(64 * a.waves), lds, s, a);
+        if ((rc = check_launch("paged_attn")) || a.splits == 1) return rc;
+    }
     hipLaunchKernelGGL((k_join<DT, D>), dim3(a.heads, a.B), dim3(256), 0, s, a);
     return check_launch("paged_attn join");
 }
@@ -563,7 +624,7 @@ template <int DT, int D> static int pick_format(const AttnArgs &a, int rt, hipSt
 {
     if (a.kv.format == W4A4_KV_INT8) return run_kv_attn<DT, D, W4A4_KV_INT8>(a, rt, s);
     if (a.kv.format == W4A4_KV_FP4) return run_kv_attn<DT, D, W4A4_KV_FP4>(a, rt, s);
-    return run_kv_attn<DT, D, W4A4_KV_16BIT>(a, rt, s);
+    return run_kv_attn<DT, D, W4A4_KV_16BIT>(a, rt, s);  // behind a prefix only
 }
 
 template <int DT> static int pick_dim(const AttnArgs &a, int D, int rt, hipStream_t s)

@@ -357,16 +357,15 @@ template <int DT, int D, int F, int RT> struct AttnRows {
     {
         f4_t s[RT][2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int t = 0; t < RT; ++t) s[t][0] = s[t][1] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int t = 0; t < RT; ++t) s[t][hf] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < S::KJ; ++j)
 #pragma unroll
-            for (int j = 0; j < S::KJ; ++j) {
+            for (int hf = 0; hf < 2; ++hf) {
                 const u4_t k = tile.key(hf, j);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) s[t][hf] = mma32<DT>(k, q[t][j], s[t][hf]);
             }
-        }
         if (!whole) {
             asm volatile("");  // a branch that most tiles skip, not 40 selects for all of them
             bool ok[8];
@@ -395,32 +394,40 @@ template <int DT, int D, int F, int RT> struct AttnRows {
                 vscale[4 * hf + 3] = b.w;
             }
         }
-        u4_t hi[RT], lo[RT];
+        float p[RT][8], top[RT];
+        bool grown = false;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            float p[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                p[e] = s[t][e / 4][e % 4];
-                if constexpr (EACH) p[e] *= kscale[e];
+                p[t][e] = s[t][e / 4][e % 4];
+                if constexpr (EACH) p[t][e] *= kscale[e];
             }
-            float top = p[0];
+            top[t] = p[t][0];
 #pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
-            top = across_groups(top, [](float x, float y) { return fmaxf(x, y); });
-            if constexpr (!EACH) top *= scale;
-            // The reference is moved only when the maximum has grown by more than 2^SLACK: sums and results are then
-            // relative to one that is at most so much too small, and most tiles leave the results alone.
-            if (__any(top > mx[t] + SLACK)) {
-                const float to = fmaxf(mx[t], top), f = to > mx[t] ? __builtin_amdgcn_exp2f(mx[t] - to) : 1.0f;
+            for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], p[t][e]);
+            top[t] = across_groups(top[t], [](float x, float y) { return fmaxf(x, y); });
+            if constexpr (!EACH) top[t] *= scale;
+            grown = grown || top[t] > mx[t] + SLACK;
+        }
+        // The reference is moved only when a maximum has grown by more than 2^SLACK: sums and results are then relative
+        // to one that is at most so much too small, and most tiles leave the results alone.
+        if (__any(grown)) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const float to = fmaxf(mx[t], top[t]), f = to > mx[t] ? __builtin_amdgcn_exp2f(mx[t] - to) : 1.0f;
 #pragma unroll
                 for (int i = 0; i < S::VE; ++i) acc[t][i] *= f;
                 sum[t] *= f;
                 mx[t] = to;
             }
+        }
+        u4_t hi[RT], lo[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
             const float from = (mx[t] == -INFINITY ? 0.0f : mx[t]) - OFF;
             auto weight = [&](int e) {
-                return __builtin_amdgcn_exp2f(EACH ? p[e] - from : fmaf(p[e], scale, -from));
+                return __builtin_amdgcn_exp2f(EACH ? p[t][e] - from : fmaf(p[t][e], scale, -from));
             };
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
@@ -436,17 +443,26 @@ template <int DT, int D, int F, int RT> struct AttnRows {
                 lo[t][e / 2] = pack16<PDT>(x - h.x, y - h.y);
             }
         }
+        u4_t v[S::VE];
 #pragma unroll
-        for (int i = 0; i < S::VE / 2; ++i) {
-            u4_t even, odd;
-            tile.values(i, even, odd);
+        for (int i = 0; i < S::VE / 2; ++i) tile.values(i, v[2 * i], v[2 * i + 1]);
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                acc[t][2 * i] = mma32<PDT>(even, lo[t], acc[t][2 * i]);
-                acc[t][2 * i + 1] = mma32<PDT>(odd, lo[t], acc[t][2 * i + 1]);
-                acc[t][2 * i] = mma32<PDT>(even, hi[t], acc[t][2 * i]);
-                acc[t][2 * i + 1] = mma32<PDT>(odd, hi[t], acc[t][2 * i + 1]);
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+            for (int i = 0; i < S::VE; ++i) acc[t][i] = mma32<PDT>(v[i], lo[t], acc[t][i]);
+#pragma unroll
+            for (int i = 0; i < S::VE; ++i) acc[t][i] = mma32<PDT>(v[i], hi[t], acc[t][i]);
+        }
+        if constexpr (RT > 1) {
+#ifdef SCHED
+            // the first rows' products go with the second rows' exponents
+            __builtin_amdgcn_sched_group_barrier(0x2 | 0x400, 60, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * S::VE; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2 | 0x400, 4, 0);
             }
+#endif
         }
     }
 

@@ -274,6 +274,7 @@ struct AttnArgs {
     KvPages kv;
     const int32_t *prefix_table, *prefix_len;
     int prefix_width, prefix_splits, prefix_tiles, prefix_row_waves, prefix_row_blocks;
+    int prefix_turns, own_turns;  // set by the launcher
 };
 // rows as they are into the quantized cache, and back (k_kvq.hip)
 struct KvRowsArgs {
@@ -296,6 +297,7 @@ int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s);
 struct PrefixPlan {
     int rt, row_waves, row_blocks, splits, tiles;
 };
+AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks, bool shared);
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix);
 int launch_kv_attn(AttnArgs a, int dtype, int D, int rt, hipStream_t s);
 
