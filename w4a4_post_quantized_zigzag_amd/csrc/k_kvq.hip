@@ -1,7 +1,6 @@
 // The quantized key-value cache: rows into it and back, the attention of one new token per sequence over it, and the
 // same attention behind a prefix that all sequences of a batch share (over a quantized or a 16-bit cache).
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kv_tile.h"
@@ -455,23 +454,15 @@ template <int DT, int D, int F, int RT> __device__ __forceinline__ void prefix_f
     }
 }
 
-// The prefix and the sequences' own tokens in one launch: the one is bound by the matrix cores, the other by memory. Eight
-// workgroups (one on each XCD) of the one and of the other take turns, and change places after every 32 turns, so that
-// neither keeps to the same CUs. RT 0: few rows.
+// The prefix and the sequences' own tokens in one launch: the one is bound by the matrix cores, the other by memory. The
+// prefix's workgroups come first, one or two for each CU, and the own tokens' fill in beside and behind them. RT 0: few rows.
 template <int DT, int D, int F, int RT> __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_shared(const AttnArgs a)
 {
     extern __shared__ float sm[];
-    const int turn = blockIdx.x / 8, xcd = blockIdx.x % 8, both = 2 * min(a.prefix_turns, a.own_turns);
-    bool prefix = a.prefix_turns > a.own_turns;
-    int id = turn - both / 2;
-    if (turn < both) {
-        prefix = ((turn + (turn / 2 / 16)) & 1) == 0;
-        id = turn / 2;
-    }
-    id = id * 8 + xcd;
-    if (!prefix) own_tokens<DT, D, F>(a, id, sm);
-    else if constexpr (RT == 0) prefix_few<DT, D, F, 1>(a, id);
-    else prefix_many<DT, D, F, RT>(a, id, reinterpret_cast<uint8_t *>(sm));
+    const int own = blockIdx.x - 8 * a.prefix_turns;
+    if (own >= 0) own_tokens<DT, D, F>(a, own, sm);
+    else if constexpr (RT == 0) prefix_few<DT, D, F, 1>(a, blockIdx.x);
+    else prefix_many<DT, D, F, RT>(a, blockIdx.x, reinterpret_cast<uint8_t *>(sm));
 }
 
 // out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the parts that had tiles, one workgroup per
@@ -546,7 +537,13 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const Att
     }
 }
 
-static int envi(const char*n,int d){const char*e=getenv(n);return e?atoi(e):d;}
+// How the own tokens are split, by sizes known on the host alone. A sequence short enough for one workgroup, or one of
+// so many that each CU has several, is not split: its result needs no join. The smallest parts are two tiles a wave: with
+// one, partials and their join cost more than the keys (64 sequences of 4000 int8 keys, one key head: 20.3 us against
+// 15.3; one of 8192: 13.2 against 12.4). Few short rows take a wave each, which waits for no other. Between them: about
+// two workgroups a CU for one or two sequences and eight for many, whose lengths differ and fill each other's gaps (16
+// ragged ones up to 16384 keys: 54 us at 2048 workgroups, 60 at 512; two of 65536 in 4 bits: 52.3 at 512, 55 at 2048);
+// behind a prefix two a CU, since the prefix's products fill the rest.
 AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks, bool shared)
 {
     const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;
@@ -556,32 +553,36 @@ AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int si
         tiles = std::min<int64_t>(tiles, (int64_t)window / 32 + 2 + ((int64_t)sinks + 31) / 32);
     tiles = std::max<int64_t>(tiles, 1);
     const int64_t rows = (int64_t)std::max(B, 1) * kv_heads * head_tiles;
-    if (tiles <= std::clamp<int64_t>(rows / 4, 8, envi("KV_ALONE",32))) return {1, (int)tiles, ATTN_WAVES};
+    if (tiles <= std::clamp<int64_t>(rows / 4, 8, 32)) return {1, (int)tiles, ATTN_WAVES};
     AttnPlan p;
-    p.waves = !shared && rows * tiles <= envi("KV_ONE",512) && tiles <= 96 ? 1 : ATTN_WAVES;
-    int64_t want = tiles;
+    p.waves = !shared && rows * tiles <= 512 && tiles <= 96 ? 1 : ATTN_WAVES;
+    int64_t want = tiles, least = 1;
     if (p.waves > 1) {
-        const int workgroups = shared ? envi("SH_WANT", 1024) : envi("KV_WANT", window > 0 ? 1024 : B <= 2 ? 512 : 2048);
+        const int workgroups = shared || (B <= 2 && window <= 0) ? 512 : window > 0 ? 1024 : 2048;
         want = std::min<int64_t>(std::max<int64_t>(workgroups / rows, 1), 256);
+        least = 2 * p.waves;
     }
-    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, p.waves * (p.waves > 1 ? envi("KV_MIN", 2) : 1));
+    p.tiles_per_split = (int)std::max<int64_t>((tiles + want - 1) / want, least);
     p.splits = (int)((tiles + p.tiles_per_split - 1) / p.tiles_per_split);
-    p.tiles_per_split = std::min(p.tiles_per_split, envi("KV_LEAST", 1<<30));
     return p;
 }
 
+// How the prefix is split: at most one workgroup for each CU, those counted that only fill a turn of eight, since a CU
+// with two takes twice as long while others wait (2 key heads of 384 rows, 4000 int8 keys: 51.3 us with 240 workgroups,
+// 66.2 with 264). More than 4 row tiles go two to a wave: each key read from LDS serves both (64 sequences of 8 heads
+// a key head, 16384 keys: 56.2 us against 70.4 with one).
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
 {
     PrefixPlan p;
     const int64_t rows = (int64_t)std::max(B, 1) * (heads / kv_heads), row_tiles = (rows + 15) / 16;
     const int64_t tiles = std::max<int64_t>(((int64_t)max_prefix + 31) / 32, 1);
-    p.rt = row_tiles > envi("PF_RT",4) ? 2 : 1;
+    p.rt = row_tiles > 4 ? 2 : 1;
     const int64_t wave_rows = (row_tiles + p.rt - 1) / p.rt;
     p.row_waves = wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;
     p.row_blocks = (int)((wave_rows + p.row_waves - 1) / p.row_waves);
     const int wk = ATTN_WAVES / p.row_waves;
-    const int64_t want = std::max<int64_t>(envi("PF_WANT",256) / (p.row_blocks * (int64_t)kv_heads), 1);  // workgroups of a head's keys
-    p.splits = (int)std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(want, (tiles + wk - 1) / wk), 1), 128 / wk) * wk;
+    const int64_t want = std::max<int64_t>(8 * (32 / p.row_blocks) / kv_heads, 1);  // workgroups on a head's keys
+    p.splits = (int)std::min<int64_t>({want, (tiles + wk - 1) / wk, 128 / wk}) * wk;
     p.tiles = 1;
     return p;
 }

@@ -454,15 +454,6 @@ template <int DT, int D, int F, int RT> struct AttnRows {
             for (int i = 0; i < S::VE; ++i) acc[t][i] = mma32<PDT>(v[i], hi[t], acc[t][i]);
         }
         if constexpr (RT > 1) {
-#ifdef SCHED
-            // the first rows' products go with the second rows' exponents
-            __builtin_amdgcn_sched_group_barrier(0x2 | 0x400, 60, 0);
-#pragma unroll
-            for (int i = 0; i < 2 * S::VE; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x2 | 0x400, 4, 0);
-            }
-#endif
         }
     }
 
