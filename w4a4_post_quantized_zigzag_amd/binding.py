@@ -642,16 +642,7 @@ def kv_append_quant(k, v, cache, slots):
 def kv_read_quant(cache, slots, dtype=None, k_out=None, v_out=None):
     """The rows at slots int64 [M] of a quantized cache as 16-bit rows (k, v), each [M, kv_heads, D]; zeros for a
     slot outside it. dtype: fp16 unless k_out or v_out say otherwise."""
-    torch = _torch()
-    if k_out is None or v_out is None:
-        given = k_out if k_out is not None else v_out
-        codes = cache[0]
-        D = codes.shape[-1] * (2 if codes.dtype == torch.uint8 else 1)
-        dt = given.dtype if given is not None else dtype or torch.float16
-        e = lambda: torch.empty((slots.shape[0], codes.shape[1], D), dtype=dt, device=codes.device)  # noqa: E731
-        k_out, v_out = e() if k_out is None else k_out, e() if v_out is None else v_out
-    (_native or _decode()).kv_read(cache, slots, k_out, v_out)
-    return k_out, v_out
+    return (_native or _decode()).kv_read(cache, slots, dtype, k_out, v_out)
 
 
 def paged_attn_decode_quant(q, cache, table, lens, scale: float | None = None, window: int = 0, sinks: int = 0,

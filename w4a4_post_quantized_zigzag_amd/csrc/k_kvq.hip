@@ -541,9 +541,10 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const Att
 // so many that each CU has several, is not split: its result needs no join. The smallest parts are two tiles a wave: with
 // one, partials and their join cost more than the keys (64 sequences of 4000 int8 keys, one key head: 20.3 us against
 // 15.3; one of 8192: 13.2 against 12.4). Few short rows take a wave each, which waits for no other. Between them: about
-// two workgroups a CU for one or two sequences and eight for many, whose lengths differ and fill each other's gaps (16
-// ragged ones up to 16384 keys: 54 us at 2048 workgroups, 60 at 512; two of 65536 in 4 bits: 52.3 at 512, 55 at 2048);
-// behind a prefix two a CU, since the prefix's products fill the rest.
+// two workgroups a CU for one or two sequences and eight for many, whose lengths differ and fill each other's gaps (the
+// ragged int8 batch: 54.5 us at 2048 workgroups, 69.5 at 512; two of 65536 keys in 4 bits: 53.2 at 512, 61.2 at 2048);
+// four behind a window, where lengths differ less (30.4 us at 1024, 35.9 at 2048); two behind a prefix, whose products
+// fill the rest.
 AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks, bool shared)
 {
     const int64_t head_tiles = ((int64_t)heads / kv_heads + 15) / 16;

@@ -3,6 +3,7 @@
 // output and workspace allocations and the current stream. These calls take a few microseconds on
 // the GPU, and the same steps in Python take longer than that (16 us for the norm + rotation).
 // Host code only; all arithmetic is behind the C ABI of libw4a4.so.
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
@@ -198,12 +199,13 @@ void dense(const at::Tensor &t, at::ScalarType dt, int64_t n, const char *name)
 struct Kv {
     at::Tensor k, v, ks, vs;  // scales undefined for 16 bits
     int format, pages, page;
-    int64_t heads, stride, scale_stride;
+    int64_t heads, D, stride, scale_stride;
     void same(const Place &p) const { p.same(k), p.same(v), p.same(ks), p.same(vs); }
 };
 
 // (k, v) of the elements' type `dt`, where `sixteen`, or (k, v, k_scale, v_scale): int8 [pages, kv_heads, page_size, D] with
-// fp32 [pages, kv_heads, page_size], or uint8 [.., D / 2] with uint8 [pages, kv_heads, D / 32, page_size]
+// fp32 [pages, kv_heads, page_size], or uint8 [.., D / 2] with uint8 [pages, kv_heads, D / 32, page_size].
+// D < 0: as the codes say
 Kv kv_of(PyObject *o, at::ScalarType dt, int64_t D, bool sixteen)
 {
     if (!PyTuple_Check(o)) TORCH_CHECK_TYPE(false, "cache must be a tuple of tensors");
@@ -215,15 +217,17 @@ Kv kv_of(PyObject *o, at::ScalarType dt, int64_t D, bool sixteen)
     want(c.k.dim() == 4, "cache must be [pages, kv_heads, page_size, ..]");
     const int64_t P = c.k.size(0), page = c.k.size(2);
     c.heads = c.k.size(1);
-    int64_t row = D;
+    const bool fp4 = n == 4 && c.k.scalar_type() == at::kByte;
+    if (D < 0) D = c.k.size(3) * (fp4 ? 2 : 1);
+    const int64_t row = fp4 ? D / 2 : D;
+    c.D = D;
     if (n == 2) {
         c.format = W4A4_KV_16BIT;
         if (c.k.scalar_type() != dt) TORCH_CHECK_VALUE(false, "a cache of two tensors must be ", dt);
     } else if (c.k.scalar_type() == at::kChar) {
         c.format = W4A4_KV_INT8;
-    } else if (c.k.scalar_type() == at::kByte) {
+    } else if (fp4) {
         c.format = W4A4_KV_FP4;
-        row = D / 2;
     } else {
         TORCH_CHECK_TYPE(false, "codes must be int8 or uint8, not ", c.k.scalar_type());
     }
@@ -237,13 +241,12 @@ Kv kv_of(PyObject *o, at::ScalarType dt, int64_t D, bool sixteen)
     c.scale_stride = 0;
     if (n == 4) {
         c.ks = tensor(PyTuple_GET_ITEM(o, 2), "k_scale"), c.vs = tensor(PyTuple_GET_ITEM(o, 3), "v_scale");
-        const bool fp4 = c.format == W4A4_KV_FP4;
-        const int64_t groups = fp4 ? D / 32 : 1;
+        const int64_t groups = fp4 ? D / 32 : 1, sizes[4] = {P, c.heads, fp4 ? groups : page, page};
         const auto st = fp4 ? at::kByte : at::kFloat;
-        const auto shape = fp4 ? std::vector<int64_t>{P, c.heads, groups, page} : std::vector<int64_t>{P, c.heads, page};
+        const at::IntArrayRef shape(sizes, fp4 ? 4 : 3);
         for (const at::Tensor *t : {&c.ks, &c.vs}) {
-            if (t->scalar_type() != st || t->sizes() != at::IntArrayRef(shape))
-                TORCH_CHECK_VALUE(false, "scales must be ", st, " ", at::IntArrayRef(shape));
+            if (t->scalar_type() != st || t->sizes() != shape)
+                TORCH_CHECK_VALUE(false, "scales must be ", st, " ", shape);
             const int last = (int)t->dim() - 1;
             want(t->stride(last) == 1 && (!fp4 || t->stride(2) == page || groups == 1) &&
                      (t->stride(1) == groups * page || c.heads == 1),
@@ -384,25 +387,44 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// ---- kv_read(cache, slots, k_out, v_out) --------------------------------------------------------------
+// ---- kv_read(cache, slots, dtype, k_out, v_out) -------------------------------------------------------
 
 PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    arity(n, 4);
-    const at::Tensor &slots = tensor(a[1], "slots"), &ko = tensor(a[2], "k_out"), &vo = tensor(a[3], "v_out");
+    arity(n, 5);
+    const at::Tensor &slots = tensor(a[1], "slots");
+    at::Tensor ko = optional(a[3], "k_out"), vo = optional(a[4], "v_out");
+    at::ScalarType dt = ko.defined() ? ko.scalar_type() : vo.defined() ? vo.scalar_type() : at::kHalf;
+    if (a[2] != Py_None) {
+        if (!THPDtype_Check(a[2])) TORCH_CHECK_TYPE(false, "dtype must be a torch.dtype");
+        const at::ScalarType asked = reinterpret_cast<THPDtype *>(a[2])->scalar_type;
+        if ((ko.defined() || vo.defined()) && asked != dt)
+            TORCH_CHECK_VALUE(false, "dtype ", asked, " for outputs of ", dt);
+        dt = asked;
+    }
+    want(slots.dim() == 1, "slots must be 1-D");
+    const Kv c = kv_of(a[0], dt, -1, false);
+    const Place at_(slots);
+    auto out = [&](at::Tensor &t) {
+        if (!t.defined()) t = at::empty({slots.size(0), c.heads, c.D}, c.k.options().dtype(dt));
+    };
+    out(ko), out(vo);
     const Heads h = heads_of(ko, "k_out");
+    if (h.rows != slots.size(0) || h.heads != c.heads || h.D != c.D)
+        TORCH_CHECK_VALUE(false, "k_out must be [", slots.size(0), ", ", c.heads, ", ", c.D, "]");
     same_heads(vo, "v_out", h);
     dense(slots, at::kLong, h.rows, "slots");
-    const Kv c = kv_of(a[0], ko.scalar_type(), h.D, false);
-    want(c.heads == h.heads, "the cache has another number of heads than k_out");
-    const Place at_(ko);
-    at_.same(vo), at_.same(slots), c.same(at_);
+    at_.same(ko), at_.same(vo), c.same(at_);
     check(w4a4_kv_read_quant(c.format, ptr(c.k), ptr(c.v), ptr(c.ks), ptr(c.vs), c.pages, c.page, c.stride,
                              c.scale_stride, (const int64_t *)ptr(slots), size(h.rows, "rows"),
                              size(h.heads, "kv_heads"), size(h.D, "head_dim"), h.code, ko.data_ptr(),
                              ld(ko, h.width()), vo.data_ptr(), ld(vo, h.width()), at_.stream()));
-    Py_RETURN_NONE;
+    PyObject *pair = PyTuple_New(2);
+    if (!pair) throw python_error();
+    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(ko)));
+    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(vo)));
+    return pair;
     END_HANDLE_TH_ERRORS
 }
 

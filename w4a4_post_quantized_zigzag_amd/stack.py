@@ -5,7 +5,9 @@ configuration keeps the attention-output and FFN-down projections at W8A8) with 
 permutation, block SVD factor, packed weights and per-step act_scale_table. For the language
 backbone's single tokens the same stack can keep its activations in 16 bits (the linears named in
 w4g: group-scaled 4-bit weights) and put attention where the identity was (attention=, with a
-PagedCache): per-head norm and rotation, append, attention over the cache. This module only
+PagedCache): per-head norm and rotation, append, attention over the cache. The cache may be kept in 8 or 4
+bits and its sequences may begin with the same tokens, kept and read once; each row may bring a
+low-rank adapter of its own to the linears (adapters=). This module only
 sequences library calls and owns buffers; all arithmetic runs in libw4a4.so.
 
 Per-step tables follow the pages' per-step scaling (vnrobo "Y tuong paper": the runtime looks up the
@@ -105,19 +107,33 @@ class Attention:
 
 class PagedCache:
     """Keys and values of `batch` sequences in pages shared by all of them, one pair of arrays per
-    layer, fp16. advance() makes room for one new token per sequence and sets the device tensors that run()
-    reads (table, lens, slots, positions) in place, so a captured run() can be replayed after it; its four
-    copies wait for the stream. Page bookkeeping is on the host. max_len is the longest that a sequence may
-    get, and what run() splits its attention for: the closer to the real lengths, the faster."""
+    layer, fp16, or quantized to 8 or 4 bits (kv="int8" or "fp4"). advance() makes room for one new token per sequence
+    and sets the device tensors that run() reads (table, lens, slots, positions) in place, so a captured run() can be
+    replayed after it; its copies wait for the stream. Page bookkeeping is on the host. max_len is the longest that a
+    sequence may get, and what run() splits its attention for: the closer to the real lengths, the faster.
+
+    max_prefix > 0: every sequence may begin with the same tokens, up to max_prefix of them, kept once and read once
+    per pass. advance_prefix() or extend(None, n) make room for them before the sequences get tokens of their own;
+    a sequence's own tokens (lens, max_len) are then counted behind the prefix, its positions through both."""
 
     def __init__(self, layers: int, attention: Attention, batch: int, pages: int, page_size: int = 16,
-                 max_len: int | None = None):
+                 max_len: int | None = None, kv: str = "fp16", max_prefix: int = 0):
         torch = _torch()
-        self.page_size, self.batch = page_size, batch
+        if kv not in ("fp16", "int8", "fp4"):
+            raise ValueError(f"kv must be fp16, int8 or fp4, not {kv!r}")
+        if max_prefix and attention.window > 0:
+            raise ValueError("a shared prefix goes with attention without a window")
+        self.page_size, self.batch, self.kind = page_size, batch, kv
         self.max_len = pages * page_size if max_len is None else max_len
-        shape = (pages, attention.kv_heads, page_size, attention.head_dim)
-        e = lambda: torch.zeros(shape, dtype=torch.float16, device="cuda")  # noqa: E731
-        self.k, self.v = [e() for _ in range(layers)], [e() for _ in range(layers)]
+        self.max_prefix = max_prefix
+        if kv == "fp16":
+            shape = (pages, attention.kv_heads, page_size, attention.head_dim)
+            e = lambda: torch.zeros(shape, dtype=torch.float16, device="cuda")  # noqa: E731
+            self.kv = [(e(), e()) for _ in range(layers)]
+        else:
+            self.kv = [bd.quant_pages(pages, attention.kv_heads, page_size, attention.head_dim, kv)
+                       for _ in range(layers)]
+        self.k, self.v = [c[0] for c in self.kv], [c[1] for c in self.kv]
         width = -(-self.max_len // page_size)
         self._table = torch.full((batch, width), -1, dtype=torch.int32)
         self._len = [0] * batch
@@ -126,37 +142,124 @@ class PagedCache:
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.slots = torch.full((batch,), -1, dtype=torch.int64, device="cuda")
         self.positions = torch.zeros(batch, dtype=torch.int64, device="cuda")
+        self._prefix = 0
+        self._prefix_table = torch.full((-(-max_prefix // page_size),), -1, dtype=torch.int32)
+        self.prefix_table = self._prefix_table.cuda()
+        self.prefix_len = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def _room(self, owners, n: int):
+        """Pages for n more tokens of every owner (a sequence, None for the prefix), none if there are too few;
+        the slots of those tokens, an owner's after another's."""
+        page = self.page_size
+        length = lambda b: self._prefix if b is None else self._len[b]  # noqa: E731
+        for b in owners:
+            if b is None and length(b) + n > self.max_prefix:
+                raise RuntimeError(f"the prefix is at max_prefix {self.max_prefix}")
+            if b is not None and length(b) + n > self.max_len:
+                raise RuntimeError(f"sequence {b} is at max_len {self.max_len}")
+        if sum(-(-(length(b) + n) // page) - -(-length(b) // page) for b in owners) > len(self._free):
+            raise RuntimeError("no free pages")
+        slots = []
+        for b in owners:
+            row = self._prefix_table if b is None else self._table[b]
+            for i in range(length(b), length(b) + n):
+                if i % page == 0:
+                    row[i // page] = self._free.pop()
+                slots.append(int(row[i // page]) * page + i % page)
+            if b is None:
+                self._prefix += n
+            else:
+                self._len[b] += n
+        return slots
+
+    def _publish(self, slots):
+        torch = _torch()
+        first = self._prefix
+        self.slots.copy_(torch.tensor(slots, dtype=torch.int64))
+        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+        self.positions.copy_(torch.tensor([max(first + n - 1, 0) for n in self._len], dtype=torch.int64))
+        self.table.copy_(self._table)
+        if self.max_prefix:
+            self.prefix_len.copy_(torch.tensor([first], dtype=torch.int32))
+            self.prefix_table.copy_(self._prefix_table)
 
     def advance(self, active=None):
         """Room for one more token of every sequence (of those whose entry in `active` is true): a
         sequence that does not take part keeps its length, and its row is not appended."""
-        torch = _torch()
         on = [b for b in range(self.batch) if active is None or active[b]]
-        for b in on:
-            if self._len[b] >= self.max_len:
-                raise RuntimeError(f"sequence {b} is at max_len {self.max_len}")
-        if sum(self._len[b] % self.page_size == 0 for b in on) > len(self._free):
-            raise RuntimeError("no free pages")
         slots = [-1] * self.batch
-        for b in on:
-            n = self._len[b]
-            if n % self.page_size == 0:
-                self._table[b, n // self.page_size] = self._free.pop()
-            slots[b] = int(self._table[b, n // self.page_size]) * self.page_size + n % self.page_size
-            self._len[b] = n + 1
-        self.slots.copy_(torch.tensor(slots, dtype=torch.int64))
-        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
-        self.positions.copy_(torch.tensor([max(n - 1, 0) for n in self._len], dtype=torch.int64))
-        self.table.copy_(self._table)
+        for b, slot in zip(on, self._room(on, 1)):
+            slots[b] = slot
+        self._publish(slots)
+
+    def advance_prefix(self, row: int = 0):
+        """Room for one more token of the prefix: run()'s row `row` is that token, the other rows of that pass are not
+        appended and their results are of no use."""
+        slots = [-1] * self.batch
+        row = range(self.batch)[row]
+        slots[row] = self._prefix_room(1)[0]
+        self._publish(slots)
+
+    def _prefix_room(self, n: int):
+        if any(self._len):
+            raise RuntimeError("the prefix is complete once a sequence has tokens of its own")
+        return self._room([None], n)
+
+    def extend(self, b, n: int):
+        """Room for n more tokens of sequence b (None: of the prefix) whose keys and values write() brings; returns
+        their slots, int64 [n] on the device."""
+        if n < 0:
+            raise ValueError(f"{n} tokens")
+        slots = self._prefix_room(n) if b is None else self._room([range(self.batch)[b]], n)
+        self._publish([-1] * self.batch)
+        return _torch().tensor(slots, dtype=_torch().int64, device="cuda")
+
+    def slots_of(self, b):
+        """The slots of all that sequence b sees, the prefix first (None: of the prefix), int64 on the device."""
+        torch, page = _torch(), self.page_size
+        place = lambda row, n: (row[torch.arange(n) // page].to(torch.int64) * page  # noqa: E731
+                                + torch.arange(n) % page)
+        parts = [place(self._prefix_table, self._prefix)]
+        if b is not None:
+            parts.append(place(self._table[b], self._len[b]))
+        return torch.cat(parts).cuda()
+
+    def write(self, li: int, k, v, slots):
+        """Rows k, v fp16 [n, kv_heads, head_dim], normed and rotated, as layer li's tokens at `slots` (-1: skipped)."""
+        if self.kind != "fp16":
+            bd.kv_append_quant(k, v, self.kv[li], slots)
+            return
+        on = slots >= 0
+        at = slots[on]
+        for cache, rows in zip(self.kv[li], (k, v)):
+            cache[at // self.page_size, :, at % self.page_size] = rows[on]
+
+    def read(self, li: int, slots):
+        """Layer li's keys and values at `slots` as fp16 rows (k, v), each [n, kv_heads, head_dim]; zeros for -1."""
+        if self.kind != "fp16":
+            return bd.kv_read_quant(self.kv[li], slots)
+        at = slots.clamp(min=0)
+        off = (slots < 0).view(-1, 1, 1)
+        return tuple(c[at // self.page_size, :, at % self.page_size].masked_fill_(off, 0) for c in self.kv[li])
 
     def release(self, b: int):
-        """Give sequence b's pages back and start it over."""
+        """Give sequence b's pages back and start it over (behind the prefix)."""
         used = -(-self._len[b] // self.page_size)
         self._free += self._table[b, :used].tolist()
         self._table[b] = -1
         self._len[b] = 0
         self.lens[b] = 0
         self.table.copy_(self._table)
+
+    def release_prefix(self):
+        """Give the prefix's pages back; every sequence has to be released before."""
+        if any(self._len):
+            raise RuntimeError("sequences still go on from the prefix")
+        used = -(-self._prefix // self.page_size)
+        self._free += self._prefix_table[:used].tolist()
+        self._prefix_table[:] = -1
+        self._prefix = 0
+        self._publish([-1] * self.batch)
 
 
 def _gather_order(cols):
@@ -216,14 +319,26 @@ class _PlainBuffers:
         if attention is not None:
             A = attention
             self.q, self.att = e((rows, A.heads, A.head_dim)), e((rows, A.heads, A.head_dim))
-            self.aws = {}  # attention workspaces by max_len
+            self.aws = {}  # attention workspaces by the call and what it is split for
+        self.rows, self.lws = rows, {}  # adapters' workspaces by (K, ranks)
 
-    def attn_ws(self, A: Attention, rows: int, max_len: int):
-        if max_len not in self.aws:
-            n = bd.lib().w4a4_paged_attn_workspace_bytes(rows, A.heads, A.kv_heads, A.head_dim, max_len,
-                                                         A.window, A.sinks)
-            self.aws[max_len] = _torch().empty(max(256, n), dtype=_torch().uint8, device="cuda")
-        return self.aws[max_len]
+    def attn_ws(self, A: Attention, rows: int, cache: PagedCache):
+        key = (cache.max_prefix, cache.kind != "fp16", cache.max_len)
+        if key not in self.aws:
+            L, size = bd.lib(), (rows, A.heads, A.kv_heads, A.head_dim)
+            if cache.max_prefix:
+                n = L.w4a4_paged_attn_shared_workspace_bytes(*size, cache.max_prefix, cache.max_len)
+            else:
+                f = L.w4a4_paged_attn_quant_workspace_bytes if key[1] else L.w4a4_paged_attn_workspace_bytes
+                n = f(*size, cache.max_len, A.window, A.sinks)
+            self.aws[key] = _torch().empty(max(256, n), dtype=_torch().uint8, device="cuda")
+        return self.aws[key]
+
+    def adapter_ws(self, K: int, R: int):
+        if (K, R) not in self.lws:
+            n = bd.lib().w4a4_adapter_workspace_bytes(self.rows, K, R)
+            self.lws[K, R] = _torch().empty(max(256, n), dtype=_torch().uint8, device="cuda")
+        return self.lws[K, R]
 
 
 class _Buffers:
@@ -273,17 +388,19 @@ class DeviceStack:
     w4g: names of the linears that run with group-scaled 4-bit weights (`group` consecutive k per
     scale) on unquantized activations. attention: an Attention instead of the identity; qkv is then
     [(heads + 2 kv_heads) head_dim, h], o [h, heads head_dim], a layer's dict may hold q_norm and k_norm
-    (fp32 [head_dim]), and run() takes a PagedCache whose batch is the rows. With either, nothing is
-    folded."""
+    (fp32 [head_dim]), and run() takes a PagedCache whose batch is the rows. adapters: one dict per layer from a
+    linear's name to its low-rank adapters (A [n, R, K], B [n, N, R]) or (A, B, scale [n]), the same n everywhere;
+    run() then takes the rows' ids. With any of the three, nothing is folded."""
 
     def __init__(self, weights, block: int, steps: int, calib=None, w8=(), fold_perms: bool = True, w4g=(),
-                 group: int = 128, attention: Attention | None = None):
+                 group: int = 128, attention: Attention | None = None, adapters=None):
         torch = _torch()
         self.block, self.steps = block, steps
         self.h = weights[0]["o"].shape[0]
         self.f = weights[0]["up"].shape[0]
         self.attention = attention
-        self.plain = attention is not None or bool(w4g)
+        self.plain = attention is not None or bool(w4g) or adapters is not None
+        self.adapters = None if adapters is None else self._check_adapters(weights, adapters)
         self._bufs = {}
         if self.plain:
             self._init_plain(weights, steps, calib, w8, w4g, group)
@@ -361,6 +478,37 @@ class DeviceStack:
             self.layers.append({n: (GroupLinear(lw[n], group) if n in w4g else
                                     DeviceLinear(lw[n], self.block, steps, *pu(n), bits=8 if n in w8 else 4)
                                     ).pack() for n in LINEARS})
+
+    @staticmethod
+    def _check_adapters(weights, adapters):
+        """The adapters as (A, B, scale or None) on the device, per layer and linear."""
+        torch = _torch()
+        if len(adapters) != len(weights):
+            raise ValueError(f"adapters for {len(adapters)} layers of {len(weights)}")
+        half = lambda t: torch.as_tensor(t, dtype=torch.float16, device="cuda").contiguous()  # noqa: E731
+        out, counts = [], set()
+        for lw, la in zip(weights, adapters):
+            if any(n not in LINEARS for n in la):
+                raise ValueError(f"adapters for {tuple(la)}, but the linears are {LINEARS}")
+            layer = {}
+            for name, (A, B, *rest) in la.items():
+                A, B = half(A), half(B)
+                N, K = lw[name].shape
+                n, R = A.shape[:2]
+                if A.shape != (n, R, K) or B.shape != (n, N, R) or R % 8 or not 0 < R <= 256 or len(rest) > 1:
+                    raise ValueError(f"adapters of {name} must be A [n, R, {K}], B [n, {N}, R] and a scale at most, R a "
+                                     f"multiple of 8 up to 256: A {tuple(A.shape)}, B {tuple(B.shape)}")
+                scale = None
+                if rest and rest[0] is not None:
+                    scale = torch.as_tensor(rest[0], dtype=torch.float32, device="cuda").contiguous()
+                    if scale.shape != (n,):
+                        raise ValueError(f"adapters of {name}: a scale of {tuple(scale.shape)} for {n}")
+                counts.add(n)
+                layer[name] = (A, B, scale)
+            out.append(layer)
+        if len(counts) > 1:
+            raise ValueError(f"linears have {sorted(counts)} adapters each: the ids are the same for all")
+        return out
 
     def bufs(self, rows: int):
         if rows not in self._bufs:
@@ -452,6 +600,13 @@ class DeviceStack:
     def gemm_call(self, e, step: int, calib: bool, bufs: _Buffers):
         """The linear's GEMM with its epilogue (and, with e["nxt"], the next linear's codes)."""
         lin, nxt, rmap = e["lin"], e.get("nxt"), e.get("res_map")
+        if e.get("adapter") is not None:
+            # the shared projection alone, rounded to fp16, then the rows' adapters with its epilogue
+            self.gemm_call({**e, "adapter": None, "epi": bd.EPI_NONE, "res": None}, step, calib, bufs)
+            A, B, scale = e["adapter"]
+            bd.adapter_add(e["Y"], e["X"], A, B, e["ids"], scale, epilogue=e["epi"], residual=e["res"], out=e["Y"],
+                           ws=bufs.adapter_ws(lin.K, A.shape[1]))
+            return
         if isinstance(lin, GroupLinear):
             bd.gemv_w4g(e["X"], lin.wt, lin.w_scale, Y=e["Y"], epilogue=e["epi"], residual=e["res"])
             return
@@ -476,13 +631,24 @@ class DeviceStack:
         A, n = self.attention, bufs.qkv.shape[0]
         qkv = bufs.qkv.view(n, A.heads + 2 * A.kv_heads, A.head_dim)
         q, k, v = qkv.split((A.heads, A.kv_heads, A.kv_heads), dim=1)
-        bd.qk_norm_rope_append(q, k, v, *self.norms[li], self.inv_freq, cache.positions, cache.k[li],
-                               cache.v[li], cache.slots, eps=A.eps, interleaved=A.interleaved, q_out=bufs.q)
-        bd.paged_attn_decode(bufs.q, cache.k[li], cache.v[li], cache.table, cache.lens, window=A.window,
-                             sinks=A.sinks, max_len=cache.max_len, out=bufs.att,
-                             ws=bufs.attn_ws(A, n, cache.max_len))
+        rope = (q, k, v, *self.norms[li], self.inv_freq, cache.positions)
+        how = dict(eps=A.eps, interleaved=A.interleaved, q_out=bufs.q)
+        if cache.kind == "fp16":
+            bd.qk_norm_rope_append(*rope, cache.k[li], cache.v[li], cache.slots, **how)
+        else:
+            bd.qk_norm_rope_append_quant(*rope, cache.kv[li], cache.slots, **how)
+        own = (cache.table, cache.lens)
+        how = dict(max_len=cache.max_len, out=bufs.att, ws=bufs.attn_ws(A, n, cache))
+        if cache.max_prefix:
+            bd.paged_attn_shared(bufs.q, cache.kv[li], cache.prefix_table, cache.prefix_len, *own,
+                                 max_prefix=cache.max_prefix, **how)
+        elif cache.kind == "fp16":
+            bd.paged_attn_decode(bufs.q, cache.k[li], cache.v[li], *own, window=A.window, sinks=A.sinks, **how)
+        else:
+            bd.paged_attn_decode_quant(bufs.q, cache.kv[li], *own, window=A.window, sinks=A.sinks, **how)
 
-    def run(self, X, step: int, calib: bool = False, outputs=None, codes=None, rows=None, cache=None):
+    def run(self, X, step: int, calib: bool = False, outputs=None, codes=None, rows=None, cache=None,
+            adapters=None):
         """One pass of the stack for denoising step `step` on X fp16 [rows, h] (device); returns the
         last layer's output in natural channel order. In calib mode the linears quantize per token
         and record their table entry for `step`. Test hooks: if `outputs` is a list, each linear's
@@ -490,13 +656,18 @@ class DeviceStack:
         residual or None); if `codes` is a list, each linear's activation codes and scale are
         appended as (codes, x_scale). `rows` (device int64 index) keeps only those token rows in
         what the hooks record. cache: the PagedCache of a stack with attention, advanced for this pass;
-        row b is sequence b's new token."""
+        row b is sequence b's new token. adapters: the rows' adapters, int32 [rows] on the device, of a stack that has
+        some; a row whose id is none of them, or a pass without ids, takes the linears as they are."""
         if (cache is not None) != (self.attention is not None):
             raise ValueError("a cache goes with attention, and attention needs one")
         if cache is not None and cache.batch != X.shape[0]:
             raise ValueError(f"{X.shape[0]} rows for a cache of {cache.batch} sequences")
         if cache is not None and len(cache.k) < len(self.layers):
             raise ValueError(f"a cache of {len(cache.k)} layers for a stack of {len(self.layers)}")
+        if cache is not None and cache.max_prefix and self.attention.window > 0:
+            raise ValueError("a shared prefix goes with attention without a window")
+        if adapters is not None and self.adapters is None:
+            raise ValueError("ids of adapters for a stack that has none")
         if codes is not None and self.plain:
             raise ValueError("codes are recorded by fully quantized stacks only")
         bufs = self.bufs(X.shape[0])
@@ -508,6 +679,8 @@ class DeviceStack:
         for li in range(len(self.layers)):
             out = bufs.hs[li % 2]
             for e in self.layer_plan(li, cur, out, calib, bufs, keep):
+                if adapters is not None:
+                    e.update(adapter=self.adapters[li].get(e["name"]), ids=adapters)
                 if cache is not None and e["name"] == "o":
                     self.attention_call(li, cache, bufs)
                 self.rotate_quant_call(e, step, calib, bufs)
