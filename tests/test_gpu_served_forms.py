@@ -1,0 +1,83 @@
+"""Every form of the serving kernels at the sizes where one gives way to another: how many rows a prefix's waves share, more
+tiles than one look at the page table covers, shared memory past 64 KB, and the adapters' walks and parts. Oracle and
+tolerances as in test_gpu_kv_attn.py and test_gpu_adapter.py."""
+import numpy as np
+import pytest
+
+from parity_util import dev
+from test_gpu_adapter import Case
+from test_gpu_kv_attn import Batch
+from test_gpu_norm_rope import tdt
+
+pytestmark = pytest.mark.gpu
+ALL = ["none", "int8", "fp4"]
+
+
+# rows a key head: 2, 3 and 4 tiles of 16 (two, two and four waves on rows), 5 and 9 (two tiles a wave)
+@pytest.mark.parametrize("B,group", [(9, 2), (33, 1), (32, 2), (40, 2), (13, 11)])
+@pytest.mark.parametrize("kind", ALL)
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+def test_prefix_rows(D, kind, B, group):
+    lens = [(7 * b) % 130 for b in range(B)]
+    b = Batch(lens, 2 * group, 2, D, 16, "bf16" if D in (96, 256) else "fp16", kind, prefix=1003, seed=B + D)
+    b.check(b.run(), rows=sorted({0, 1, B // 2, B - 2, B - 1}))
+
+
+@pytest.mark.parametrize("prefix", [1, 31, 33, 2049])
+@pytest.mark.parametrize("kind", ALL)
+def test_prefix_lengths_many_rows(kind, prefix):
+    b = Batch([3] * 70, 4, 2, 128, 32, "fp16", kind, prefix=prefix, seed=prefix)
+    b.check(b.run(), rows=[0, 31, 69])
+
+
+@pytest.mark.parametrize("kind", ["none", "int8"])
+@pytest.mark.parametrize("B", [33, 52])
+def test_prefix_of_more_tiles_than_a_look(B, kind):
+    """32 key heads leave each part of the prefix more than 64 tiles."""
+    b = Batch([5] * B, 32, 32, 64, 64, "fp16", kind, prefix=20011, seed=B)
+    b.check(b.run(), rows=[0, B - 1])
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp4"])
+def test_own_tokens_of_more_tiles_than_a_look(kind):
+    """300 sequences of one long table row leave each wave more than 64 tiles."""
+    import torch
+    n, B = 25003, 300
+    b = Batch([n], 2, 2, 64, 64, "fp16", kind, seed=1)
+    b.table = b.table.repeat(B, 1)
+    b.lens = [n - 100 * i for i in range(B)]
+    b.lens[-2:] = [0, n]
+    b.ld = dev(np.array(b.lens, np.int32))
+    b.q = torch.from_numpy(np.random.default_rng(2).standard_normal((B, 2, 64)).astype(np.float32)).to(tdt("fp16")).cuda()
+    b.check(b.run(), rows=[0, 1, 150, B - 2, B - 1])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [16, 256, 257, 700])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128, 136, 256])
+def test_adapter_ranks(R, M, dtype):
+    c = Case(M, 1032, 203, R, 5, dtype, seed=M + R)
+    c.check(c.run("residual"), "residual")
+
+
+@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("N", [1, 3, 7, 8, 9, 63, 64, 71, 129, 1030])
+def test_adapter_channels(N, M):
+    for R in (16, 48, 200):
+        c = Case(M, 136, N, R, 4, "fp16", seed=N + M)
+        for epi in ("none", "gelu", "residual"):
+            c.check(c.run(epi), epi)
+
+
+@pytest.mark.parametrize("M,K", [(1, 40), (1, 5000), (20, 16376), (280, 8200), (280, 504), (1000, 3336), (9000, 72)])
+def test_adapter_parts(M, K):
+    c = Case(M, K, 40, 16, 3, "bf16", seed=K)
+    c.check(c.run(), rows=slice(0, None) if M < 2000 else slice(M - 300, None))
+
+
+def test_adapters_of_a_tile_all_different():
+    """Sixteen adapters and none in each tile of rows, in the walk over many rows too."""
+    for M in (32, 400):
+        ids = np.arange(M) * 7 % 17 - 1
+        c = Case(M, 128, 300, 24, 16, "fp16", seed=M, ids=ids)
+        c.check(c.run("gelu"), "gelu")

@@ -579,7 +579,7 @@ PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
     const int64_t tiles = std::max<int64_t>(((int64_t)max_prefix + 31) / 32, 1);
     p.rt = row_tiles > 4 ? 2 : 1;
     const int64_t wave_rows = (row_tiles + p.rt - 1) / p.rt;
-    p.row_waves = wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;
+    p.row_waves = p.rt == 2 || wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;  // fewer than 4: a tile's rows in each wave
     p.row_blocks = (int)((wave_rows + p.row_waves - 1) / p.row_waves);
     const int wk = ATTN_WAVES / p.row_waves;
     const int64_t want = std::max<int64_t>(8 * (32 / p.row_blocks) / kv_heads, 1);  // workgroups on a head's keys
