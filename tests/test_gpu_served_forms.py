@@ -81,3 +81,22 @@ def test_adapters_of_a_tile_all_different():
         ids = np.arange(M) * 7 % 17 - 1
         c = Case(M, 128, 300, 24, 16, "fp16", seed=M, ids=ids)
         c.check(c.run("gelu"), "gelu")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("K", [8, 40, 1024, 1032, 2048, 2056])
+@pytest.mark.parametrize("R", [8, 16, 24])
+@pytest.mark.parametrize("M", [1, 2, 4, 5])
+def test_adapters_of_few_rows(M, R, K, dtype):
+    """On both sides of where one launch does for both products; a row's bits are the same beside others or alone."""
+    import torch
+    for ids in (None, [1, -1, 1, 0, 2][:M], [2] * M):
+        c = Case(M, K, 75, R, 3, dtype, seed=M + K, ids=ids)
+        out = c.run("residual")
+        c.check(out, "residual")
+        if ids is not None:
+            first = c.run("residual", Y=c.Y[:1], X=c.X[:1], ids=c.ids[:1], residual=c.res[:1])
+            assert torch.equal(first, out[:1])
+            y = c.Y.clone()
+            c.run(Y=y, out=y)
+            c.check(y)

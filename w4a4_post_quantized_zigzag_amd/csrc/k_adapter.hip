@@ -10,6 +10,8 @@
 //    order by the readers) and over the waves of each.
 //  - outer: [channels x rows] = B (A operand) . t^T. t stays fp32 in effect: it enters the product as two 16-bit parts,
 //    in fp16 scaled by a power of two per 32 ranks, so that neither part leaves fp16's range.
+// For up to four rows of up to 16 ranks and 2048 k one launch does both: each workgroup of the second makes the inner
+// products it needs itself, in the same order.
 #include <algorithm>
 #include <type_traits>
 
@@ -51,7 +53,39 @@ struct AdapterWalk {
     }
 };
 
-// U: steps of 32 k in flight
+// One wave's steps s0 .. s1 of 32 k each: [ranks x rows] into acc. x and w point at the lane's row and 8 k of each; U
+// steps are in flight; most: the lane's last run of 8 k.
+template <int DT, int RT, int U>
+__device__ __forceinline__ void inner_steps(const uint16_t *x, const uint16_t *const (&w)[RT], int s0, int s1, int most,
+                                            f4_t (&acc)[RT])
+{
+    auto block = [&](int s, auto last) {  // steps s .. s + U - 1; the last ones may reach past K or s1
+        u4_t xv[U], wv[U][RT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = last.value ? min(32 * (s + u), most) : 32 * (s + u);
+            xv[u] = load8_any(x + k);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) wv[u][t] = load8_any(w[t] + k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (last.value) {  // what is past the end is zeros on both sides
+                const bool on = s + u < s1 && 32 * (s + u) <= most;
+                const u4_t zero = {0, 0, 0, 0};
+                xv[u] = on ? xv[u] : zero;
+#pragma unroll
+                for (int t = 0; t < RT; ++t) wv[u][t] = on ? wv[u][t] : zero;
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[t] = mma32<DT>(wv[u][t], xv[u], acc[t]);
+        }
+    };
+    int s = s0;
+    for (; s + U < s1; s += U) block(s, std::false_type());
+    if (s < s1) block(s, std::true_type());
+}
+
 template <int DT, int RT, int U> __global__ __launch_bounds__(64 * IN_WAVES) void k_adapter_in(const AdapterArgs a)
 {
     __shared__ float red[IN_WAVES][RT][64][4];
@@ -74,31 +108,7 @@ template <int DT, int RT, int U> __global__ __launch_bounds__(64 * IN_WAVES) voi
         f4_t acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        auto block = [&](int s, auto last) {  // steps s .. s + U - 1; the last ones may reach past K or s1
-            u4_t xv[U], wv[U][RT];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = last.value ? min(32 * (s + u), most) : 32 * (s + u);
-                xv[u] = load8_any(x + k);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) wv[u][t] = load8_any(w[t] + k);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (last.value) {  // what is past the end is zeros on both sides
-                    const bool on = s + u < s1 && 32 * (s + u) <= most;
-                    const u4_t zero = {0, 0, 0, 0};
-                    xv[u] = on ? xv[u] : zero;
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) wv[u][t] = on ? wv[u][t] : zero;
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) acc[t] = mma32<DT>(wv[u][t], xv[u], acc[t]);
-            }
-        };
-        int s = s0;
-        for (; s + U < s1; s += U) block(s, std::false_type());
-        if (s < s1) block(s, std::true_type());
+        inner_steps<DT, RT, U>(x, w, s0, s1, most, acc);
         __syncthreads();  // of the pass before this
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -131,8 +141,8 @@ __device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(v *
 //    way: few adapters per tile of rows, many tiles.
 //  - else it has one block, and the next adapter's weights are on their way: many adapters, few tiles.
 // What is on its way is asked for without branches (the last one once more at the end), for a wait behind a branch is
-// a wait for everything. LP: lanes to a row of weights, 8 LP >= R. SMALL: N below 8.
-template <int DT, int LP, bool WALK, bool SMALL>
+// a wait for everything. LP: lanes to a row of weights, 8 LP >= R. SMALL: N below 8. ONE: there was no first launch.
+template <int DT, int LP, bool WALK, bool SMALL, bool ONE = false>
 __global__ __launch_bounds__(64 * OUT_WAVES) __attribute__((amdgpu_waves_per_eu(LP < 8 ? 4 : LP == 8 ? 3 : 2)))
 void k_adapter_out(const AdapterArgs a)
 {
@@ -152,7 +162,7 @@ void k_adapter_out(const AdapterArgs a)
     const int64_t m0 = tile * 16, mc = min(m0 + r, a.M - 1);
     const int first = (run * (OUT_WAVES / a.row_waves) + wave / a.row_waves) * a.run_blocks * C;
     const int end = min(a.N, first + a.run_blocks * C);
-    if (run >= a.out_runs || first >= end || m0 >= a.M) return;
+    if (run >= a.out_runs || (!ONE && (first >= end || m0 >= a.M))) return;
     u4_t *slots = reinterpret_cast<u4_t *>(area[wave]);
     float *results = reinterpret_cast<float *>(area[wave]);
 
@@ -169,7 +179,7 @@ void k_adapter_out(const AdapterArgs a)
     for (int j = 0; j < J; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-        inner(j, tp);
+        if (!ONE) inner(j, tp);
     }
     // as holder of Y: row lane / CL of each 64 / CL, eight channels from 8 (lane % CL)
     const int ch = lane % CL * 8;
@@ -226,10 +236,55 @@ void k_adapter_out(const AdapterArgs a)
     Weights w;
     load_weights(first, walk.who, w);
 
-    for (int p = 1; p < a.parts; ++p) {
-        tp += a.M * a.R;
+    if constexpr (ONE) {  // the sums of k_adapter_in, in its order, by all waves of the workgroup
+        constexpr int RT = LP < 4 ? 1 : 2;
+        __shared__ __attribute__((aligned(16))) float products[16][8 * LP + 4];
+        static_assert(AREA >= RT * 1024, "");
+        const int steps = (a.K + 31) / 32, per = (steps + a.parts * OUT_WAVES - 1) / (a.parts * OUT_WAVES);
+        AdapterWalk again;
+        again.start(a, m0);
+        while (again.next(a, lead)) {
+            if (again.who < 0) continue;
+            for (int r0 = 0; r0 < a.R; r0 += 16 * RT) {
+                const uint16_t *wi[RT];
 #pragma unroll
-        for (int j = 0; j < J; ++j) inner(j, tp);
+                for (int t = 0; t < RT; ++t)
+                    wi[t] = a.A + (int64_t)again.who * a.stride_a + (int64_t)min(r0 + 16 * t + r, a.R - 1) * a.K + 8 * g;
+                for (int part = 0; part < a.parts; ++part) {
+                    f4_t acc[RT];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) acc[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    const int s0 = (part * OUT_WAVES + wave) * per;
+                    inner_steps<DT, RT, 8>(a.X + mc * a.ldx + 8 * g, wi, s0, min(steps, s0 + per), a.K - 8 - 8 * g, acc);
+                    __syncthreads();  // of the part before this
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) reinterpret_cast<f4_t *>(area[wave])[64 * t + lane] = acc[t];
+                    __syncthreads();
+                    const int e = threadIdx.x, l = e % 64, rank = r0 + e / 64 * 16 + l / 16 * 4;
+                    if (e < RT * 64 && rank < a.R && (again.rows >> (l % 16) & 1)) {
+                        f4_t q = reinterpret_cast<const f4_t *>(area[0])[e];
+#pragma unroll
+                        for (int u = 1; u < OUT_WAVES; ++u) q += reinterpret_cast<const f4_t *>(area[u])[e];
+                        f4_t *to = reinterpret_cast<f4_t *>(&products[l % 16][rank]);
+                        *to = part ? *to + q : q;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (first >= end) return;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const f4_t *q = reinterpret_cast<const f4_t *>(&products[r][min(32 * j + 8 * g, a.R - 8)]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] = q[0][i], v[j][4 + i] = q[1][i];
+        }
+    } else {
+        for (int p = 1; p < a.parts; ++p) {
+            tp += a.M * a.R;
+#pragma unroll
+            for (int j = 0; j < J; ++j) inner(j, tp);
+        }
     }
     u4_t hi[J], lo[J];
     float f[J];
@@ -374,16 +429,22 @@ int adapter_parts(int64_t M, int K)
     return (int)std::clamp<int64_t>(std::min<int64_t>(512 / tiles, K / 512), 1, 16);
 }
 
-template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool walk, hipStream_t s)
+template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool walk, bool one, hipStream_t s)
 {
     constexpr int C = 16 * (LP <= 8 ? 4 : LP == 16 ? 2 : 1);
-    a.leads = walk ? 1 : 4;
+    a.leads = walk ? 1 : (int)std::min<int64_t>(4, a.M);
     a.row_waves = walk ? 4 : 1;
     const int across = OUT_WAVES / a.row_waves, blocks = (a.N + C - 1) / C;
     const int64_t groups = (tiles + a.row_waves - 1) / a.row_waves;
     a.run_blocks = walk ? (int)std::clamp<int64_t>((int64_t)blocks * groups * a.row_waves / 3072, 1, 16) : 1;
     a.out_runs = (blocks + a.run_blocks * across - 1) / (a.run_blocks * across);
     const dim3 grid((unsigned)((a.out_runs + 7) / 8 * 8 * a.leads * groups)), block(64 * OUT_WAVES);
+    if constexpr (LP == 2) {
+        if (one) {
+            hipLaunchKernelGGL((k_adapter_out<DT, LP, false, false, true>), grid, block, 0, s, a);
+            return;
+        }
+    }
     if (a.N < 8) hipLaunchKernelGGL((k_adapter_out<DT, LP, false, true>), grid, block, 0, s, a);
     else if (walk) hipLaunchKernelGGL((k_adapter_out<DT, LP, true, false>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_adapter_out<DT, LP, false, false>), grid, block, 0, s, a);
@@ -406,16 +467,22 @@ template <int DT> static int run_adapter(AdapterArgs a, hipStream_t s)
     const int64_t most = std::clamp<int64_t>(((int64_t)1 << 23) / ((int64_t)a.N / 16 + 64) / 4 * 4, 4, 32768);
     for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += most) {
         const int64_t y = std::min<int64_t>(most, tiles - a.tile0);
-        a.leads = many ? 1 : 16;
-        if (a.R <= 16) run_in<DT, 1>(a, y, s);
-        else run_in<DT, 2>(a, y, s);
-        if (int rc = check_launch("adapter_add inner")) return rc;
+        a.leads = many ? 1 : (int)std::min<int64_t>(16, a.M);
+        // A launch less for a few short rows (a row of 16 ranks, 1024x1024: 5.5 us in a graph against 6.8; 2048x2048: 7.0
+        // against 7.1, and 9.8 against 7.5 with four parts, 10.2 against 8.6 with 64 ranks). Up to 4 rows no workgroup
+        // has more than one adapter.
+        const bool one = a.M <= 4 && a.R <= 16 && a.N >= 8 && a.parts <= 2;
+        if (!one) {
+            if (a.R <= 16) run_in<DT, 1>(a, y, s);
+            else run_in<DT, 2>(a, y, s);
+            if (int rc = check_launch("adapter_add inner")) return rc;
+        }
         const bool walk = many && a.N >= 8;
-        if (a.R <= 16) run_out<DT, 2>(a, y, walk, s);
-        else if (a.R <= 32) run_out<DT, 4>(a, y, walk, s);
-        else if (a.R <= 64) run_out<DT, 8>(a, y, walk, s);
-        else if (a.R <= 128) run_out<DT, 16>(a, y, walk, s);
-        else run_out<DT, 32>(a, y, walk, s);
+        if (a.R <= 16) run_out<DT, 2>(a, y, walk, one, s);
+        else if (a.R <= 32) run_out<DT, 4>(a, y, walk, one, s);
+        else if (a.R <= 64) run_out<DT, 8>(a, y, walk, one, s);
+        else if (a.R <= 128) run_out<DT, 16>(a, y, walk, one, s);
+        else run_out<DT, 32>(a, y, walk, one, s);
         if (int rc = check_launch("adapter_add")) return rc;
     }
     return W4A4_OK;
