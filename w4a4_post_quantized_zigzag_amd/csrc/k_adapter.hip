@@ -432,12 +432,16 @@ int adapter_parts(int64_t M, int K)
 template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool walk, bool one, hipStream_t s)
 {
     constexpr int C = 16 * (LP <= 8 ? 4 : LP == 16 ? 2 : 1);
-    a.leads = walk ? 1 : (int)std::min<int64_t>(4, a.M);
     a.row_waves = walk ? 4 : 1;
     const int across = OUT_WAVES / a.row_waves, blocks = (a.N + C - 1) / C;
     const int64_t groups = (tiles + a.row_waves - 1) / a.row_waves;
     a.run_blocks = walk ? (int)std::clamp<int64_t>((int64_t)blocks * groups * a.row_waves / 3072, 1, 16) : 1;
     a.out_runs = (blocks + a.run_blocks * across - 1) / (a.run_blocks * across);
+    // A tile's adapters are dealt to enough workgroups for one on each CU: fewer wait for one adapter after another, more
+    // wait to start (32 rows of 24 adapters, 16384 channels: 14.5 us at 256 workgroups, 16.4 at 128, 16.2 at 512, 19.3 at
+    // 1024; 64 rows of 32 adapters of 64 ranks, 4096: 19.7, 21.2, 20.4, 26.7).
+    const int64_t alone = a.out_runs * tiles;
+    a.leads = walk ? 1 : (int)std::min<int64_t>({(255 + alone) / alone, 16, a.M});
     const dim3 grid((unsigned)((a.out_runs + 7) / 8 * 8 * a.leads * groups)), block(64 * OUT_WAVES);
     if constexpr (LP == 2) {
         if (one) {
@@ -469,8 +473,8 @@ template <int DT> static int run_adapter(AdapterArgs a, hipStream_t s)
         const int64_t y = std::min<int64_t>(most, tiles - a.tile0);
         a.leads = many ? 1 : (int)std::min<int64_t>(16, a.M);
         // A launch less for a few short rows (a row of 16 ranks, 1024x1024: 5.5 us in a graph against 6.8; 2048x2048: 7.0
-        // against 7.1, and 9.8 against 7.5 with four parts, 10.2 against 8.6 with 64 ranks). Up to 4 rows no workgroup
-        // has more than one adapter.
+        // against 7.1, and 9.8 against 7.5 with four parts, 10.2 against 8.6 with 64 ranks; 16 rows of 16 adapters 13.3
+        // against 10.4: the workgroups make one adapter's products after another's).
         const bool one = a.M <= 4 && a.R <= 16 && a.N >= 8 && a.parts <= 2;
         if (!one) {
             if (a.R <= 16) run_in<DT, 1>(a, y, s);
