@@ -12,6 +12,10 @@
 //    in fp16 scaled by a power of two per 32 ranks, so that neither part leaves fp16's range.
 // For up to four rows of up to 16 ranks and 2048 k one launch does both: each workgroup of the second makes the inner
 // products it needs itself, in the same order.
+// Measured (MI355X): 32 rows of 24 adapters, 16 ranks, 2048 -> 16384 channels: 4.6 us inner, 8.9 outer, bound by the launches
+// and by one adapter's weights after another (12.6 MB at 1.4 TB/s); 1600 rows of 64 ranks, 1024 -> 4099, one adapter for 50
+// rows: 9.0 inner (a tile's rows and one or two adapters are 64 to 96 KB, read by few waves), 21.0 outer (26 MB of Y in and
+// out at 1.8 TB/s, vector units 28 % busy); one row, 1024 -> 1024, in one launch: 5.1.
 #include <algorithm>
 #include <type_traits>
 

@@ -9,7 +9,10 @@ namespace w4a4 {
 
 // ================================================================================================
 // Rows as they are into the cache, and back. A lane takes eight channels of one head of one token, a head is LH
-// lanes. Bound by the bytes.
+// lanes, so that the largest of a head (or of 32 channels) is found by a few moves between neighbouring lanes, and each
+// access is 16 bytes of a row. Bound by the bytes: 8191 tokens of 8 + 8 heads of 128 are read back from 4 bits in 11.2 us
+// (9 MB in, 34 MB out: 3.8 TB/s), 1600 of 16 + 16 heads of 64 from 8 bits in 3.4; small calls by their launch (1.6 us).
+// The fused write is k_norm_rope's (8191 tokens of 32 + 8 heads of 128: 36.0 us, as with a 16-bit cache).
 // ================================================================================================
 template <int DT, int F, int LH> __global__ __launch_bounds__(256) void k_kv_append(const KvRowsArgs a)
 {
@@ -109,6 +112,13 @@ int launch_kv_read(const KvRowsArgs &a, int dtype, hipStream_t s) { return pick_
 // are cut into row tiles of 16, and each wave takes RT of them over a run of the prefix, so that a tile of keys that
 // has been loaded and widened serves 16 RT rows. Each (sequence, head) then has parts, of the prefix and of its own
 // tokens, which k_join adds up in a fixed order.
+//  - Own tokens are bound by memory: 32 ragged sequences up to 8191 int8 keys (32 heads over 8 of 128) 48.1 us, 4.4 TB/s;
+//    two of 131071 and fewer fp4 keys 47.8 us, 5.0 TB/s, with the vector units busy 45 % of the time and the matrix cores 17 %
+//    (counted; 4 heads to a key head use a quarter of a product's columns). One short sequence is bound by the chain of
+//    length, page, keys, values: 7.8 us.
+//  - The prefix is bound by how few waves there are to hide each other's waits: 64 sequences behind 16384 16-bit tokens
+//    52.0 us, own tokens included; the matrix cores are busy a fifth of that, the vector units a third (counted), 1.2 waves
+//    on a SIMD on average. Twice as many prefix workgroups write twice as many parts, and lose more (68 us).
 // ================================================================================================
 
 // The parts that a run of T tiles is cut into: `per` tiles each, used of them
@@ -466,7 +476,8 @@ template <int DT, int D, int F, int RT> __global__ __launch_bounds__(64 * ATTN_W
 }
 
 // out = sum_s exp2(m_s - M) o_s / sum_s exp2(m_s - M) l_s over the parts that had tiles, one workgroup per
-// (sequence, head): the prefix's parts come first, the sequence's own behind them.
+// (sequence, head): the prefix's parts come first, the sequence's own behind them. Bound by its launch and the parts' bytes
+// (64 sequences of 32 heads, 16 parts of 128 channels of the prefix: 6.7 us; one of 8 heads, 32 parts of 256: 3.5).
 constexpr int JOIN_MAX = 256;
 template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const AttnArgs a)
 {
@@ -569,7 +580,7 @@ AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int si
 }
 
 // How the prefix is split: at most one workgroup for each CU, those counted that only fill a turn of eight, since a CU
-// with two takes twice as long while others wait (2 key heads of 384 rows, 4000 int8 keys: 51.3 us with 240 workgroups,
+// with two takes twice as long while others wait (2 key heads of 384 rows, 30011 int8 keys: 51.3 us with 240 workgroups,
 // 66.2 with 264). More than 4 row tiles go two to a wave: each key read from LDS serves both (64 sequences of 8 heads
 // a key head, 16384 keys: 56.2 us against 70.4 with one).
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
