@@ -14,8 +14,8 @@
 // products it needs itself, in the same order.
 // Measured (MI355X): 32 rows of 24 adapters, 16 ranks, 2048 -> 16384 channels: 4.6 us inner, 8.9 outer, bound by the launches
 // and by one adapter's weights after another (12.6 MB at 1.4 TB/s); 1600 rows of 64 ranks, 1024 -> 4099, one adapter for 50
-// rows: 9.0 inner (a tile's rows and one or two adapters are 64 to 96 KB, read by few waves), 21.0 outer (26 MB of Y in and
-// out at 1.8 TB/s, vector units 28 % busy); one row, 1024 -> 1024, in one launch: 5.1.
+// rows: 8.9 inner (a tile's rows and one or two adapters, one after the other, read by few waves), 19.9 outer (37 MB in and
+// out at 1.9 TB/s, vector units 26 % busy); one row, 1024 -> 1024, in one launch: 5.1.
 #include <algorithm>
 #include <type_traits>
 
@@ -439,7 +439,10 @@ template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool
     a.row_waves = walk ? 4 : 1;
     const int across = OUT_WAVES / a.row_waves, blocks = (a.N + C - 1) / C;
     const int64_t groups = (tiles + a.row_waves - 1) / a.row_waves;
-    a.run_blocks = walk ? (int)std::clamp<int64_t>((int64_t)blocks * groups * a.row_waves / 3072, 1, 16) : 1;
+    // A walk is long enough to leave 8 waves a CU, 12 where a wave needs few registers (1600 rows of 64 ranks, 4099 channels:
+    // 28.5 us with 8, 29.9 with 12, 32.0 with 16; 16 ranks, 16384 channels: 45.1, 37.8 and 41.4).
+    constexpr int WAVES = 256 * (LP == 2 ? 12 : 8);
+    a.run_blocks = walk ? (int)std::clamp<int64_t>((int64_t)blocks * groups * a.row_waves / WAVES, 1, 16) : 1;
     a.out_runs = (blocks + a.run_blocks * across - 1) / (a.run_blocks * across);
     // A tile's adapters are dealt to enough workgroups for one on each CU: fewer wait for one adapter after another, more
     // wait to start (32 rows of 24 adapters, 16384 channels: 14.5 us at 256 workgroups, 16.4 at 128, 16.2 at 512, 19.3 at
