@@ -100,3 +100,64 @@ def test_adapters_of_few_rows(M, R, K, dtype):
             y = c.Y.clone()
             c.run(Y=y, out=y)
             c.check(y)
+
+
+def calls():
+    """One of each kind, in sizes that need a workspace."""
+    from w4a4_post_quantized_zigzag_amd import binding as bd
+    own = Batch([900, 17, 0, 2500], 8, 2, 128, 16, "bf16", "int8", seed=1)
+    own4 = Batch([1200, 640, 33], 6, 2, 64, 32, "fp16", "fp4", seed=2)
+    behind = Batch([5 * i for i in range(40)], 8, 2, 128, 16, "fp16", "none", prefix=3001, seed=3)
+    few = Batch([9, 200], 4, 4, 64, 16, "bf16", "int8", prefix=700, seed=4)
+    ad, rows = Case(40, 1032, 515, 24, 6, "fp16", seed=5), Case(600, 520, 130, 64, 3, "bf16", seed=6)
+    size = lambda b, *n: (len(b.lens), b.H, b.KV, b.D, *n)  # noqa: E731
+    L = bd.lib()
+    return [(lambda ws: own.run(max_len=2500, ws=ws), L.w4a4_paged_attn_quant_workspace_bytes(*size(own, 2500, 0, 0))),
+            (lambda ws: own4.run(max_len=1200, ws=ws), L.w4a4_paged_attn_quant_workspace_bytes(*size(own4, 1200, 0, 0))),
+            (lambda ws: behind.run(max_prefix=3001, max_len=200, ws=ws),
+             L.w4a4_paged_attn_shared_workspace_bytes(*size(behind, 3001, 200))),
+            (lambda ws: few.run(max_prefix=700, max_len=200, ws=ws),
+             L.w4a4_paged_attn_shared_workspace_bytes(*size(few, 700, 200))),
+            (lambda ws: ad.run("gelu", ws=ws), L.w4a4_adapter_workspace_bytes(40, 1032, 24)),
+            (lambda ws: rows.run("residual", ws=ws), L.w4a4_adapter_workspace_bytes(600, 520, 64))]
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    every = calls()
+    buf = lambda n: torch.full((max(n, 256),), 0xFF, dtype=torch.uint8, device="cuda")  # noqa: E731
+    want = [f(buf(n)) for f, n in every]
+    ws = [[buf(n) for _, n in every] for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for turn in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                at = (turn + 2 * i) % len(every)       # another call beside it each time
+                got[i].append((at, every[at][0](ws[i][at])))
+    torch.cuda.synchronize()
+    for some in got:
+        for at, out in some:
+            assert torch.equal(out, want[at]), at
+
+
+def test_graphs_that_share_a_workspace():
+    """Captured one by one with one workspace, replayed in any order, with eager calls between the replays."""
+    import torch
+    every = calls()
+    ws = torch.full((max(n for _, n in every),), 0xFF, dtype=torch.uint8, device="cuda")
+    want = [f(ws).clone() for f, _ in every]
+    graphs, outs = [], []
+    for f, _ in every:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f(ws))
+        graphs.append(g)
+    for turn in range(4):
+        for at in (3 * turn + np.arange(len(every)) * (5 if turn % 2 else 1)) % len(every):
+            outs[at].zero_()
+            graphs[at].replay()
+            assert torch.equal(outs[at], want[at]), (turn, at)
+            assert torch.equal(every[(at + turn) % len(every)][0](ws), want[(at + turn) % len(every)])
+        torch.cuda.synchronize()

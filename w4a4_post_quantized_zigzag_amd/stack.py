@@ -390,7 +390,8 @@ class DeviceStack:
     [(heads + 2 kv_heads) head_dim, h], o [h, heads head_dim], a layer's dict may hold q_norm and k_norm
     (fp32 [head_dim]), and run() takes a PagedCache whose batch is the rows. adapters: one dict per layer from a
     linear's name to its low-rank adapters (A [n, R, K], B [n, N, R]) or (A, B, scale [n]), the same n everywhere;
-    run() then takes the rows' ids. With any of the three, nothing is folded."""
+    run() then takes the rows' ids; fp16 tensors that are on the device already are kept, not copied. With any of the
+    three, nothing is folded."""
 
     def __init__(self, weights, block: int, steps: int, calib=None, w8=(), fold_perms: bool = True, w4g=(),
                  group: int = 128, attention: Attention | None = None, adapters=None):
