@@ -448,7 +448,7 @@ template <int DT, int LP> static void run_out(AdapterArgs a, int64_t tiles, bool
     // wait to start (32 rows of 24 adapters, 16384 channels: 14.5 us at 256 workgroups, 16.4 at 128, 16.2 at 512, 19.3 at
     // 1024; 64 rows of 32 adapters of 64 ranks, 4096: 19.7, 21.2, 20.4, 26.7).
     const int64_t alone = a.out_runs * tiles;
-    a.leads = walk ? 1 : (int)std::min<int64_t>({(255 + alone) / alone, 16, a.M});
+    a.leads = walk ? 1 : (int)std::min<int64_t>({(255 + alone) / alone, 16, a.n + 1, a.M});
     const dim3 grid((unsigned)((a.out_runs + 7) / 8 * 8 * a.leads * groups)), block(64 * OUT_WAVES);
     if constexpr (LP == 2) {
         if (one) {
@@ -478,7 +478,11 @@ template <int DT> static int run_adapter(AdapterArgs a, hipStream_t s)
     const int64_t most = std::clamp<int64_t>(((int64_t)1 << 23) / ((int64_t)a.N / 16 + 64) / 4 * 4, 4, 32768);
     for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += most) {
         const int64_t y = std::min<int64_t>(most, tiles - a.tile0);
-        a.leads = many ? 1 : (int)std::min<int64_t>(16, a.M);
+        // A tile's adapters go to workgroups of their own while those are few; where they are many, those without one cost
+        // more than the others wait (307 mixed rows of 27 adapters of 16 ranks, 328 k: 18.8 us dealt out, 26.9 not; 2048
+        // rows, one adapter for 400, 4096 k: 27.6 and 22.4).
+        const int64_t room = tiles > 32 ? 1 : many ? 1024 / (tiles * a.parts * ((a.R + 31) / 32)) : 16;
+        a.leads = (int)std::min<int64_t>({std::max<int64_t>(room, 1), 16, a.n, a.M});
         // A launch less for a few short rows (a row of 16 ranks, 1024x1024: 5.5 us in a graph against 6.8; 2048x2048: 7.0
         // against 7.1, and 9.8 against 7.5 with four parts, 10.2 against 8.6 with 64 ranks; 16 rows of 16 adapters 13.3
         // against 10.4: the workgroups make one adapter's products after another's).
