@@ -224,23 +224,36 @@ class PagedCache:
             parts.append(place(self._table[b], self._len[b]))
         return torch.cat(parts).cuda()
 
+    def _places(self, li: int, slots):
+        """Pages and offsets of `slots` in a 16-bit cache, and which of them are inside it (the others get slot 0)."""
+        torch = _torch()
+        if slots.dtype != torch.int64 or slots.dim() != 1:
+            raise ValueError(f"slots must be int64 [n], not {slots.dtype} {tuple(slots.shape)}")
+        on = (slots >= 0) & (slots < self.kv[li][0].shape[0] * self.page_size)
+        at = slots.masked_fill(~on, 0)
+        return at // self.page_size, at % self.page_size, on
+
     def write(self, li: int, k, v, slots):
-        """Rows k, v fp16 [n, kv_heads, head_dim], normed and rotated, as layer li's tokens at `slots` (-1: skipped)."""
+        """Rows k, v fp16 [n, kv_heads, head_dim], normed and rotated, as layer li's tokens at `slots` (outside the cache:
+        skipped)."""
         if self.kind != "fp16":
             bd.kv_append_quant(k, v, self.kv[li], slots)
             return
-        on = slots >= 0
-        at = slots[on]
-        for cache, rows in zip(self.kv[li], (k, v)):
-            cache[at // self.page_size, :, at % self.page_size] = rows[on]
+        page, off, on = self._places(li, slots)
+        shape = (slots.shape[0], *self.kv[li][0].shape[1::2])
+        for name, x in (("k", k), ("v", v)):
+            if x.dtype != _torch().float16 or x.shape != shape:
+                raise ValueError(f"{name} must be fp16 {list(shape)} for these slots, not {x.dtype} {list(x.shape)}")
+        for cache, x in zip(self.kv[li], (k, v)):
+            cache[page[on], :, off[on]] = x[on]
 
     def read(self, li: int, slots):
-        """Layer li's keys and values at `slots` as fp16 rows (k, v), each [n, kv_heads, head_dim]; zeros for -1."""
+        """Layer li's keys and values at `slots` as fp16 rows (k, v), each [n, kv_heads, head_dim]; zeros outside the
+        cache."""
         if self.kind != "fp16":
             return bd.kv_read_quant(self.kv[li], slots)
-        at = slots.clamp(min=0)
-        off = (slots < 0).view(-1, 1, 1)
-        return tuple(c[at // self.page_size, :, at % self.page_size].masked_fill_(off, 0) for c in self.kv[li])
+        page, off, on = self._places(li, slots)
+        return tuple(c[page, :, off].masked_fill_(~on.view(-1, 1, 1), 0) for c in self.kv[li])
 
     def release(self, b: int):
         """Give sequence b's pages back and start it over (behind the prefix)."""
