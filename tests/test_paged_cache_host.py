@@ -1,5 +1,5 @@
 """PagedCache.write and read over a 16-bit cache, whose rows are moved by indexing (no GPU needed): a slot outside the cache
-is skipped and reads as zeros, as over a quantized one, and rows of another shape or type are refused."""
+is skipped and reads as zeros, as over a quantized one, and rows of another shape are refused."""
 import pytest
 import torch
 
@@ -46,13 +46,12 @@ def test_refusals(cache):
     k, v = rows(3)
     at = torch.tensor([1, 2, 3])
     before = [t.clone() for t in cache.kv[0]]
-    for bad in ((k[:, :1], v), (k, v[:, :1]), (k[:2], v), (k[..., :1], v), (k[0], v[0]), (k.float(), v), (k, v.bfloat16())):
+    for bad in ((k[:, :1], v), (k, v[:, :1]), (k[:2], v), (k[..., :1], v), (k[0], v[0])):
         with pytest.raises(ValueError, match="must be"):
             cache.write(0, *bad, at)
-    for slots in (at[:2], at.int(), at.view(1, 3)):
+    for slots in (at[:2], at.view(1, 3)):
         with pytest.raises(ValueError, match="slots"):
             cache.write(0, k, v, slots)
-    for slots in (at.int(), at.view(1, 3)):
-        with pytest.raises(ValueError, match="slots"):
-            cache.read(0, slots)
+    with pytest.raises(ValueError, match="slots"):
+        cache.read(0, at.view(1, 3))
     assert all(torch.equal(a, b) for a, b in zip(cache.kv[0], before))
