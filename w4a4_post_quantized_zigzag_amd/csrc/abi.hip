@@ -1514,6 +1514,7 @@ static int kv_attn(AttnArgs &a, bool shared, int max_prefix, const void *q, int 
     a.prefix_splits = plan.prefix.splits;
     a.prefix_tiles = plan.prefix.tiles;
     a.prefix_row_waves = plan.prefix.row_waves;
+    a.prefix_row_runs = plan.prefix.row_runs;
     a.prefix_row_blocks = plan.prefix.row_blocks;
     if (plan.ws_bytes) {
         a.stat = reinterpret_cast<float2 *>(ws);

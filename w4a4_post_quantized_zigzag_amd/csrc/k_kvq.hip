@@ -267,13 +267,13 @@ __device__ __forceinline__ void prefix_many(const AttnArgs &a, const int id, uin
     constexpr int BUF = prefix_buffer<D, F>();
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // all row blocks of one (head, part) run on one XCD
-    const int unit = id / (8 * a.prefix_row_blocks) * 8 + id % 8;
-    const int block = id / 8 % a.prefix_row_blocks;
-    const int kvh = unit / a.prefix_splits, split = unit % a.prefix_splits;
-    if (kvh >= a.kv_heads) return;
+    // all row blocks of one (head, part, run of blocks) run on one XCD
+    const int unit = id / (8 * a.prefix_row_blocks) * 8 + id % 8, keys = unit / a.prefix_row_runs;
+    const int block = unit % a.prefix_row_runs * a.prefix_row_blocks + id / 8 % a.prefix_row_blocks;
+    const int kvh = keys / a.prefix_splits, split = keys % a.prefix_splits;
     const int group = a.heads / a.kv_heads;
     const int64_t total = (int64_t)a.B * group, row0 = ((int64_t)block * ATTN_WAVES + wave) * 16 * RT;
+    if (kvh >= a.kv_heads || (int64_t)block * ATTN_WAVES * 16 * RT >= total) return;
     bool bad;
     const int T = prefix_tiles(a, bad), n = bad ? 0 : a.prefix_len[0];
     const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
@@ -582,7 +582,9 @@ AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int si
 // How the prefix is split: at most one workgroup for each CU, those counted that only fill a turn of eight, since a CU
 // with two takes twice as long while others wait (2 key heads of 384 rows, 30011 int8 keys: 51.3 us with 240 workgroups,
 // 66.2 with 264). More than 4 row tiles go two to a wave: each key read from LDS serves both (64 sequences of 8 heads
-// a key head, 16384 keys: 56.2 us against 70.4 with one).
+// a key head, 16384 keys: 56.2 us against 70.4 with one). More row blocks than an XCD has CUs are cut into runs, each on
+// one XCD (8 heads over 1 of 128, 16384 keys: 512 sequences, 32 blocks, 88 us; 513, 33 blocks, 152 in two runs of 17 and
+// 755 in one run, which leaves seven XCDs idle).
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
 {
     PrefixPlan p;
@@ -591,9 +593,11 @@ PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
     p.rt = row_tiles > 4 ? 2 : 1;
     const int64_t wave_rows = (row_tiles + p.rt - 1) / p.rt;
     p.row_waves = p.rt == 2 || wave_rows >= 4 ? 4 : wave_rows >= 2 ? 2 : 1;  // fewer than 4: a tile's rows in each wave
-    p.row_blocks = (int)((wave_rows + p.row_waves - 1) / p.row_waves);
+    const int64_t blocks = (wave_rows + p.row_waves - 1) / p.row_waves;
+    p.row_runs = (int)((blocks + 31) / 32);
+    p.row_blocks = (int)((blocks + p.row_runs - 1) / p.row_runs);
     const int wk = ATTN_WAVES / p.row_waves;
-    const int64_t want = std::max<int64_t>(8 * (32 / p.row_blocks) / kv_heads, 1);  // workgroups on a head's keys
+    const int64_t want = std::max<int64_t>(8 * (32 / p.row_blocks) / ((int64_t)kv_heads * p.row_runs), 1);  // on a run's keys
     p.splits = (int)std::min<int64_t>({want, (tiles + wk - 1) / wk, 128 / wk}) * wk;
     p.tiles = 1;
     return p;
@@ -618,7 +622,7 @@ template <int DT, int D, int F> static int run_kv_attn(AttnArgs a, int rt, hipSt
     a.own_turns = (int)(((int64_t)a.B * a.splits + 7) / 8 * a.kv_heads * a.head_tiles);
     if (a.prefix_splits) {
         const int wk = ATTN_WAVES / a.prefix_row_waves;
-        a.prefix_turns = (int)(((int64_t)a.kv_heads * (a.prefix_splits / wk) + 7) / 8 * a.prefix_row_blocks);
+        a.prefix_turns = (int)(((int64_t)a.kv_heads * (a.prefix_splits / wk) * a.prefix_row_runs + 7) / 8 * a.prefix_row_blocks);
         rc = wk > 1    ? run_shared<DT, D, F, 0>(a, lds, s)
              : rt == 2 ? run_shared<DT, D, F, 2>(a, lds, s)
                        : run_shared<DT, D, F, 1>(a, lds, s);
