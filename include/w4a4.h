@@ -489,7 +489,8 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
  * w4a4_kv_read_quant: slots back to rows of `dtype`, one rounding of c * s; a slot outside the cache gives zeros.
  * k_out or v_out may be NULL. (fp4 written as bf16 and read as fp16 may leave fp16's range.)
  * w4a4_paged_attn_decode_quant: w4a4_paged_attn_decode over such a cache: the values above in the same formula, sums in
- * fp32, nothing rounded before the end but the weights p (to two 16-bit parts, 2^-17 of each). Workspace:
+ * fp32, nothing rounded before the end but the weights p, which go in as two 16-bit parts: 2^-17 of each is dropped over
+ * int8 and for bf16; for fp16 over the other formats 2^-22 of each, and up to 2^-39 of the sequence's largest. Workspace:
  * w4a4_paged_attn_quant_workspace_bytes. What is not visible may hold anything, scales included.
  *
  * w4a4_paged_attn_shared: the attention of one new token per sequence for a batch whose sequences all begin with the
@@ -540,7 +541,8 @@ int w4a4_paged_attn_shared(const void *q, int dtype, int B, int heads, int kv_he
  * (NULL: ones). A row whose id is outside [0, n) has no adapter and gets epilogue(Y[m]). X, A, B, Y, residual and out
  * are all of `dtype` (fp16 or bf16), at any element's address and row stride; Y is the shared projection's output
  * (with no epilogue of its own), out may be Y. Epilogues as in w4a4_gemm, after the sum. The inner products are fp32
- * and enter the second product as two 16-bit parts (2^-17 of each is dropped), sums are fp32, one rounding at the end.
+ * and enter the second product as two 16-bit parts: in bf16 2^-17 of each is dropped; in fp16 2^-22 of each, and up to
+ * 2^-39 of the largest among the 32 of its ranks 32 i to 32 i + 31. Sums are fp32, one rounding at the end.
  * Rows are independent of each other: another row's adapter, whatever it holds, does not touch them. K and R multiples
  * of 8 (W4A4_ERR_SHAPE), R up to 256, M up to 2^25, K up to 2^23, N up to 2^24 (W4A4_ERR_UNSUPPORTED). X may not
  * overlap out. ws: w4a4_adapter_workspace_bytes(M, K, R) bytes, 256-byte aligned. Results do not depend on timing.

@@ -1,9 +1,13 @@
 """Edges of the serving calls that sizes and arguments allow. Oracle and tolerances as in the tests of each call."""
+import numpy as np
 import pytest
 
+from oracle import served as osv
 from w4a4_post_quantized_zigzag_amd.stack import Attention, PagedCache
 
+from test_gpu_adapter import HALF_STEP, Case
 from test_gpu_kv_attn import Batch
+from test_gpu_norm_rope import f64
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +34,32 @@ def test_prefix_for_more_rows_than_an_xcd_has_workgroups(B, H, KV, D, kind):
     lens = [(5 * b) % 37 for b in range(B)]
     b = Batch(lens, H, KV, D, 16, "fp16" if B == 513 else "bf16", kind, prefix=1003, seed=B)
     b.check(b.run(max_len=36), rows=[0, 1, 127, 255, B // 2, B - 2, B - 1])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("R", [16, 64])
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("up,down", [(2.0 ** 14, 2.0 ** -8), (2.0 ** 16, 2.0 ** -14)])
+def test_a_rank_far_above_the_others(up, down, M, R, dtype):
+    """A rank 2^22 or 2^30 above the others that no channel takes anything from. In fp16 the second part of an inner product
+    that is far below the largest of its 32 is a subnormal number: at the scale that takes the largest to 2^14 or above its
+    half step is 2^-25, 2^-39 of the largest."""
+    c = Case(M, 256, 90, R, 3, dtype, seed=R)
+    c.A *= down
+    c.A[:, 3] *= up / down
+    c.B *= 1 / down
+    c.B[:, :, 3] = 0
+    c.Y *= 0
+    assert bool(c.A.isfinite().all()) and bool(c.B.isfinite().all())
+    X, A, B, ids, scale = f64(c.X), f64(c.A), f64(c.B), c.ids.tolist(), f64(c.scale)
+    y, inner, outer, _ = osv.adapter_add(f64(c.Y), X, A, B, ids, scale, "none", None)
+    tol = (256 + 64) * 2.0 ** -23 * inner + (2.0 ** -17 + (R + 9) * 2.0 ** -23) * outer
+    if dtype == "fp16":
+        for m, i in enumerate(ids):
+            for g in range(0, R if i >= 0 else 0, 32):
+                top = np.abs(A[i, g:g + 32] @ X[m]).max() * (1 + 2.0 ** -10)
+                tol[m] += 2.0 ** -39 * top * scale[i] * np.abs(B[i, :, g:g + 32]).sum(1)
+    tol = tol + 2.0 ** -23 * np.abs(y)
+    tol = tol + HALF_STEP[dtype] * (np.abs(y) + tol) + 2.0 ** -25
+    err = np.abs(f64(c.run()) - y)
+    assert np.all(err <= tol), float((err / tol).max())

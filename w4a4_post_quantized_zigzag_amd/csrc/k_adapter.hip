@@ -8,8 +8,10 @@
 // for all rows pays for one pass.
 //  - inner: [ranks x rows] = A (A operand) . X^T, K cut over workgroups (parts of t are fp32 and are added in a fixed
 //    order by the readers) and over the waves of each.
-//  - outer: [channels x rows] = B (A operand) . t^T. t stays fp32 in effect: it enters the product as two 16-bit parts,
-//    in fp16 scaled by a power of two per 32 ranks, so that neither part leaves fp16's range.
+//  - outer: [channels x rows] = B (A operand) . t^T. t enters the product as two 16-bit parts, which in bf16 drop 2^-17 of
+//    it. In fp16 they are scaled by a power of two per 32 ranks that takes the largest of them to 2^14 or above, so that
+//    neither part leaves fp16's range; they drop 2^-22 of t, and where the second is subnormal half its step, 2^-39 of that
+//    largest.
 // For up to four rows of up to 16 ranks and 2048 k one launch does both: each workgroup of the second makes the inner
 // products it needs itself, in the same order.
 // Measured (MI355X): 32 rows of 24 adapters, 16 ranks, 2048 -> 16384 channels: 4.6 us inner, 8.9 outer, bound by the launches
