@@ -481,7 +481,8 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
  * Arrays (keys and values each): codes int8 [kv_heads][page_size][D], or uint8 [kv_heads][page_size][D / 2], page p at
  * p * page_stride elements; scales fp32 [kv_heads][page_size], or uint8 [kv_heads][D / 32][page_size], page p at p *
  * scale_stride elements. Bases and pages start at multiples of 16 bytes (W4A4_ERR_ALIGN). Pages, slots, tables and
- * limits as for the 16-bit cache above.
+ * limits as for the 16-bit cache above, but the kept slots of one call must differ: of two rows with one slot, codes of
+ * either and a scale of either stay there, which need not stand for the values of either (no other slot is touched).
  *
  * w4a4_qk_norm_rope_quant: w4a4_qk_norm_rope with the append into such a cache (required here). Keys are rounded to
  * `dtype` first, so that the cache holds what w4a4_kv_append_quant makes of k_out and v, bit for bit.

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from oracle import served as osv
+from w4a4_post_quantized_zigzag_amd import binding as bd
 from w4a4_post_quantized_zigzag_amd.stack import Attention, PagedCache
 
 from test_gpu_adapter import HALF_STEP, Case
@@ -63,3 +64,25 @@ def test_a_rank_far_above_the_others(up, down, M, R, dtype):
     tol = tol + HALF_STEP[dtype] * (np.abs(y) + tol) + 2.0 ** -25
     err = np.abs(f64(c.run()) - y)
     assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp4"])
+@pytest.mark.parametrize("M", [4, 700])
+def test_two_rows_with_one_slot(M, kind):
+    """Every code and scale there is one of the two rows', every other slot as without them."""
+    import torch
+    KV, D, page, pages = 2, 128, 16, 50
+    k, v = (torch.randn(M, KV, D, device="cuda").half() * s for s in (1.0, 40.0))
+    q = torch.randn(M, 4, D, device="cuda").half()
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(M))[:M].cuda()
+    for append in (lambda c, at: bd.kv_append_quant(k, v, c, at),
+                   lambda c, at: bd.qk_norm_rope_append_quant(q, k, v, None, None, None, None, c, at)):
+        caches = [bd.quant_pages(pages, KV, page, D, kind) for _ in range(3)]
+        twice, first, second = slots.clone(), slots.clone(), slots.clone()
+        twice[1] = slots[M - 1]
+        first[1], first[M - 1] = slots[M - 1], -1
+        second[1] = -1
+        for cache, at in zip(caches, (twice, first, second)):
+            append(cache, at)
+        for got, a, b in zip(*caches):
+            assert bool(((got.view(torch.uint8) == a.view(torch.uint8)) | (got.view(torch.uint8) == b.view(torch.uint8))).all())

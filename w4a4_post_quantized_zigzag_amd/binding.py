@@ -629,13 +629,14 @@ def quant_pages(pages: int, kv_heads: int, page_size: int, head_dim: int, kind: 
 def qk_norm_rope_append_quant(q, k, v, q_weight, k_weight, inv_freq, positions, cache, slots, eps: float = 1e-6,
                               interleaved: bool = False, q_out=None, k_out=None):
     """qk_norm_rope_append into a quantized cache (QuantPages): it then holds what kv_append_quant makes of the
-    16-bit keys and values. Returns q_out."""
+    16-bit keys and values. Kept slots must differ from each other. Returns q_out."""
     return (_native or _decode()).norm_rope_quant(q, k, v, q_weight, k_weight, inv_freq, positions, eps,
                                                   interleaved, q_out, k_out, cache, slots)
 
 
 def kv_append_quant(k, v, cache, slots):
-    """Rows k, v [M, kv_heads, D] as they are into slots int64 [M] of a quantized cache (-1: skipped)."""
+    """Rows k, v [M, kv_heads, D] as they are into slots int64 [M] of a quantized cache (-1: skipped; the others must
+    differ from each other)."""
     (_native or _decode()).kv_append(k, v, cache, slots)
 
 

@@ -234,7 +234,7 @@ class PagedCache:
 
     def write(self, li: int, k, v, slots):
         """Rows k, v fp16 [n, kv_heads, head_dim], normed and rotated, as layer li's tokens at `slots` (outside the cache:
-        skipped)."""
+        skipped; the others must differ from each other)."""
         if self.kind != "fp16":
             bd.kv_append_quant(k, v, self.kv[li], slots)
             return
