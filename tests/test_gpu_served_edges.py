@@ -6,7 +6,7 @@ from oracle import served as osv
 from w4a4_post_quantized_zigzag_amd import binding as bd
 from w4a4_post_quantized_zigzag_amd.stack import Attention, PagedCache
 
-from test_gpu_adapter import HALF_STEP, Case
+from test_gpu_adapter import EPIS, HALF_STEP, Case
 from test_gpu_kv_attn import Batch
 from test_gpu_norm_rope import f64
 
@@ -86,3 +86,46 @@ def test_two_rows_with_one_slot(M, kind):
             append(cache, at)
         for got, a, b in zip(*caches):
             assert bool(((got.view(torch.uint8) == a.view(torch.uint8)) | (got.view(torch.uint8) == b.view(torch.uint8))).all())
+
+
+@pytest.mark.parametrize("epi", list(EPIS))
+@pytest.mark.parametrize("M,N,R,n", [(300, 333, 24, 4), (700, 1030, 64, 20), (1030, 77, 16, 3)])
+def test_in_place_over_many_rows(M, N, R, n, epi):
+    """More than 256 rows, as the stack calls it: the next block's Y is on its way while this one is stored, and rows
+    without an adapter are left alone."""
+    import torch
+    c = Case(M, 264, N, R, n, "bf16", seed=M)
+    assert -1 in c.ids.tolist()
+    want = c.run(epi)
+    c.check(want, epi)
+    y = torch.full((M + 1, N + 3), 7.0, dtype=c.Y.dtype, device="cuda")
+    out = y[:M, 2:2 + N]
+    for _ in range(3):
+        out.copy_(c.Y)
+        c.run(epi, Y=out, out=out)
+        assert torch.equal(out, want)
+    out.fill_(7.0)
+    assert bool((y == 7.0).all())
+    if epi == "residual":
+        r = c.res.clone()
+        c.run(epi, residual=r, out=r)
+        assert torch.equal(r, want)
+
+
+@pytest.mark.parametrize("M,R", [(500, 8), (65, 16)])
+def test_adapters_in_several_launches(M, R):
+    """2^22 channels and more take several launches of some tiles of rows each: the same bits as on slices of the channels,
+    whose calls are one launch."""
+    import torch
+    N, K, n, part = (1 << 22) + 13 if M > 256 else (1 << 24) - 3, 40, 2, 4096
+    t = lambda *s: torch.randn(*s, dtype=torch.bfloat16, device="cuda", generator=g)  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(M)
+    X, A, B, Y = t(M, K), t(n, R, K), t(n, N, R), t(M, N)
+    ids = torch.randint(-1, n, (M,), dtype=torch.int32, device="cuda", generator=g)
+    out = bd.adapter_add(Y, X, A, B, ids)
+    for at in (0, 1 << 20, N // 2 + 1, N - part):
+        want = bd.adapter_add(Y[:, at:at + part].contiguous(), X, A, B[:, at:at + part].contiguous(), ids)
+        assert torch.equal(out[:, at:at + part], want), at
+    for rows in (slice(0, 64), slice(M - 64, M)):
+        none = ids[rows] < 0
+        assert torch.equal(out[rows][none], Y[rows][none]) and not torch.equal(out[rows][~none], Y[rows][~none])
