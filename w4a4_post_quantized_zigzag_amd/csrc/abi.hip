@@ -1512,7 +1512,6 @@ static int kv_attn(AttnArgs &a, bool shared, int max_prefix, const void *q, int 
     a.tiles_per_split = plan.own.tiles_per_split;
     a.waves = plan.own.waves;
     a.prefix_splits = plan.prefix.splits;
-    a.prefix_tiles = plan.prefix.tiles;
     a.prefix_row_waves = plan.prefix.row_waves;
     a.prefix_row_runs = plan.prefix.row_runs;
     a.prefix_row_blocks = plan.prefix.row_blocks;

@@ -14,10 +14,10 @@
 //    largest.
 // For up to four rows of up to 16 ranks and 2048 k one launch does both: each workgroup of the second makes the inner
 // products it needs itself, in the same order.
-// Measured (MI355X): 32 rows of 24 adapters, 16 ranks, 2048 -> 16384 channels: 4.6 us inner, 8.9 outer, bound by the launches
+// Measured (MI355X): 32 rows of 24 adapters, 16 ranks, 2048 -> 16384 channels: 5.0 us inner, 9.0 outer, bound by the launches
 // and by one adapter's weights after another (12.6 MB at 1.4 TB/s); 1600 rows of 64 ranks, 1024 -> 4099, one adapter for 50
 // rows: 8.9 inner (a tile's rows and one or two adapters, one after the other, read by few waves), 19.9 outer (37 MB in and
-// out at 1.9 TB/s, vector units 26 % busy); one row, 1024 -> 1024, in one launch: 5.1.
+// out at 1.9 TB/s, vector units 26 % busy); one row, 1024 -> 1024, in one launch: 5.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -480,9 +480,11 @@ template <int DT> static int run_adapter(AdapterArgs a, hipStream_t s)
     const int64_t most = std::clamp<int64_t>(((int64_t)1 << 23) / ((int64_t)a.N / 16 + 64) / 4 * 4, 4, 32768);
     for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += most) {
         const int64_t y = std::min<int64_t>(most, tiles - a.tile0);
-        // A tile's adapters go to workgroups of their own while those are few; where they are many, those without one cost
-        // more than the others wait (307 mixed rows of 27 adapters of 16 ranks, 328 k: 18.8 us dealt out, 26.9 not; 2048
-        // rows, one adapter for 400, 4096 k: 27.6 and 22.4).
+        // A tile's adapters go to workgroups of their own while those are few. Where they are many, those without one cost
+        // rows in runs more than the others wait (dealt out and not: 2048 rows, one adapter for 400, 4096 k 27.6 and 22.4 us;
+        // 2000 rows of 17 adapters of 32 ranks, 1024 k, 21.5 and 17.9; 600 such rows 11.2 and 10.7). Mixed rows gain at any
+        // count (307 of 27 adapters 18.8 and 26.9; 600 of 17 25.0 and 39.4; 2000 of 17 71.3 and 76.1), which only the ids,
+        // on the device, could tell.
         const int64_t room = tiles > 32 ? 1 : many ? 1024 / (tiles * a.parts * ((a.R + 31) / 32)) : 16;
         a.leads = (int)std::min<int64_t>({std::max<int64_t>(room, 1), 16, a.n, a.M});
         // A launch less for a few short rows (a row of 16 ranks, 1024x1024: 5.5 us in a graph against 6.8; 2048x2048: 7.0

@@ -276,7 +276,7 @@ __device__ __forceinline__ void prefix_many(const AttnArgs &a, const int id, uin
     if (kvh >= a.kv_heads || (int64_t)block * ATTN_WAVES * 16 * RT >= total) return;
     bool bad;
     const int T = prefix_tiles(a, bad), n = bad ? 0 : a.prefix_len[0];
-    const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+    const int per = tiles_per_part(T, a.prefix_splits, 1);
     const int t0 = split * per, t1 = min(T, t0 + per);
     if (t0 >= t1) return;
 
@@ -334,43 +334,43 @@ __device__ __forceinline__ void prefix_many(const AttnArgs &a, const int id, uin
             }
         };
         for (int base = t0; base < t1; base += 64) {
-        const int some = min(64, t1 - base);
-        KvPlaces places;
-        places.look_up<D, F>(a.kv, a.prefix_table, (base + min(lane, some - 1)) * 32, n, 0, 0, kvh, bad);
-        load(places.get<F>(0));
-        commit(base, lds);
-        __syncthreads();
-        for (int i = 0; i < some; ++i) {
-            const int t = base + i;
-            const uint8_t *now = lds + (i & 1) * BUF;
-            load(places.get<F>(min(i + 1, some - 1)));
-            if (row0 < total) {
-                KvTile<DT, D, F> tile;
-                tile.keys_from(now, lane);
-                const uint8_t *scales = now + 2 * Stage::BYTES;
-                if constexpr (F == W4A4_KV_INT8) {
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        tile.ks[hf] = reinterpret_cast<const float4 *>(scales)[4 * hf + g];
-                        tile.vs[hf] = reinterpret_cast<const float4 *>(scales)[8 + 4 * hf + g];
-                    }
-                } else if constexpr (F == W4A4_KV_FP4) {
-                    const int vg = (S::VE * r < D ? S::VE * r : 0) / 32;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                        for (int l = 0; l < S::NL; ++l)
-                            tile.kb[hf][l] = scales[S::channel(l * S::NR, g) / 32 * 32 + 16 * hf + r];
-                        tile.vb[hf] = reinterpret_cast<const uint32_t *>(scales + D + vg * 32 + 16 * hf)[g];
-                    }
-                }
-                tile.values_from(now + Stage::BYTES, lane);
-                rows.template add<false>(tile, t * 32 <= n - 32,
-                                    [&](int e) { return t * 32 + 16 * (e / 4) + 4 * g + e % 4 < n; }, scale);
-            }
-            if (i + 1 < some) commit(t + 1, lds + ((i + 1) & 1) * BUF);
+            const int some = min(64, t1 - base);
+            KvPlaces places;
+            places.look_up<D, F>(a.kv, a.prefix_table, (base + min(lane, some - 1)) * 32, n, 0, 0, kvh, bad);
+            load(places.get<F>(0));
+            commit(base, lds);
             __syncthreads();
-        }
+            for (int i = 0; i < some; ++i) {
+                const int t = base + i;
+                const uint8_t *now = lds + (i & 1) * BUF;
+                load(places.get<F>(min(i + 1, some - 1)));
+                if (row0 < total) {
+                    KvTile<DT, D, F> tile;
+                    tile.keys_from(now, lane);
+                    const uint8_t *scales = now + 2 * Stage::BYTES;
+                    if constexpr (F == W4A4_KV_INT8) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            tile.ks[hf] = reinterpret_cast<const float4 *>(scales)[4 * hf + g];
+                            tile.vs[hf] = reinterpret_cast<const float4 *>(scales)[8 + 4 * hf + g];
+                        }
+                    } else if constexpr (F == W4A4_KV_FP4) {
+                        const int vg = (S::VE * r < D ? S::VE * r : 0) / 32;
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                            for (int l = 0; l < S::NL; ++l)
+                                tile.kb[hf][l] = scales[S::channel(l * S::NR, g) / 32 * 32 + 16 * hf + r];
+                            tile.vb[hf] = reinterpret_cast<const uint32_t *>(scales + D + vg * 32 + 16 * hf)[g];
+                        }
+                    }
+                    tile.values_from(now + Stage::BYTES, lane);
+                    rows.template add<false>(tile, t * 32 <= n - 32,
+                                        [&](int e) { return t * 32 + 16 * (e / 4) + 4 * g + e % 4 < n; }, scale);
+                }
+                if (i + 1 < some) commit(t + 1, lds + ((i + 1) & 1) * BUF);
+                __syncthreads();
+            }
         }
     }
 #pragma unroll
@@ -392,9 +392,10 @@ __device__ __forceinline__ void prefix_many(const AttnArgs &a, const int id, uin
     }
 }
 
-// The prefix for few rows: each wave loads its own tiles.
-template <int DT, int D, int F, int RT> __device__ __forceinline__ void prefix_few(const AttnArgs &a, const int id)
+// The prefix for few rows, fewer than four row tiles: each wave loads its own tiles of keys.
+template <int DT, int D, int F> __device__ __forceinline__ void prefix_few(const AttnArgs &a, const int id)
 {
+    constexpr int RT = 1;
     typedef KvShape<D, F> S;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -410,7 +411,7 @@ template <int DT, int D, int F, int RT> __device__ __forceinline__ void prefix_f
     if (row0 >= total) return;
     bool bad;
     const int T = prefix_tiles(a, bad), n = bad ? 0 : a.prefix_len[0];
-    const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+    const int per = tiles_per_part(T, a.prefix_splits, 1);
     const int t0 = split * per, t1 = min(T, t0 + per);
     if (t0 >= t1) return;
 
@@ -465,13 +466,14 @@ template <int DT, int D, int F, int RT> __device__ __forceinline__ void prefix_f
 }
 
 // The prefix and the sequences' own tokens in one launch: the one is bound by the matrix cores, the other by memory. The
-// prefix's workgroups come first, one or two for each CU, and the own tokens' fill in beside and behind them. RT 0: few rows.
+// prefix's workgroups come first, at most one for each CU where the row blocks allow it (prefix_plan), and
+// the own tokens' fill in beside and behind them. RT 0: few rows.
 template <int DT, int D, int F, int RT> __global__ __launch_bounds__(64 * ATTN_WAVES) void k_attn_shared(const AttnArgs a)
 {
     extern __shared__ float sm[];
     const int own = blockIdx.x - 8 * a.prefix_turns;
     if (own >= 0) own_tokens<DT, D, F>(a, own, sm);
-    else if constexpr (RT == 0) prefix_few<DT, D, F, 1>(a, blockIdx.x);
+    else if constexpr (RT == 0) prefix_few<DT, D, F>(a, blockIdx.x);
     else prefix_many<DT, D, F, RT>(a, blockIdx.x, reinterpret_cast<uint8_t *>(sm));
 }
 
@@ -492,7 +494,7 @@ template <int DT, int D> __global__ __launch_bounds__(256) void k_join(const Att
     int used_p = 0, used_s = 0;
     if (a.prefix_splits) {
         const int T = prefix_tiles(a, over);
-        const int per = tiles_per_part(T, a.prefix_splits, a.prefix_tiles);
+        const int per = tiles_per_part(T, a.prefix_splits, 1);
         used_p = (T + per - 1) / per;
     }
     const AttnTiles tl = attn_tiles(a.lens[b], a);
@@ -579,12 +581,12 @@ AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int si
     return p;
 }
 
-// How the prefix is split: at most one workgroup for each CU, those counted that only fill a turn of eight, since a CU
-// with two takes twice as long while others wait (2 key heads of 384 rows, 30011 int8 keys: 51.3 us with 240 workgroups,
-// 66.2 with 264). More than 4 row tiles go two to a wave: each key read from LDS serves both (64 sequences of 8 heads
-// a key head, 16384 keys: 56.2 us against 70.4 with one). More row blocks than an XCD has CUs are cut into runs, each on
-// one XCD (8 heads over 1 of 128, 16384 keys: 512 sequences, 32 blocks, 88 us; 513, 33 blocks, 152 in two runs of 17 and
-// 755 in one run, which leaves seven XCDs idle).
+// How the prefix is split: at most one workgroup for each CU as long as the heads' row blocks alone are no more than the
+// CUs, those counted that only fill a turn of eight, since a CU with two takes twice as long while others wait (2 key heads
+// of 384 rows, 30011 int8 keys: 51.3 us with 240 workgroups, 66.2 with 264). More than 4 row tiles go two to a wave: each
+// key read from LDS serves both (64 sequences of 8 heads a key head, 16384 keys: 56.2 us against 70.4 with one). More row
+// blocks than an XCD has CUs are cut into runs, each on one XCD (8 heads over 1 of 128, 16384 keys: 512 sequences, 32
+// blocks, 88 us; 513, 33 blocks, 152 in two runs of 17 and 755 in one run, which leaves seven XCDs idle).
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
 {
     PrefixPlan p;
@@ -599,7 +601,6 @@ PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix)
     const int wk = ATTN_WAVES / p.row_waves;
     const int64_t want = std::max<int64_t>(8 * (32 / p.row_blocks) / ((int64_t)kv_heads * p.row_runs), 1);  // on a run's keys
     p.splits = (int)std::min<int64_t>({want, (tiles + wk - 1) / wk, 128 / wk}) * wk;
-    p.tiles = 1;
     return p;
 }
 

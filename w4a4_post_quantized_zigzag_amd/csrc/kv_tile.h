@@ -136,7 +136,6 @@ template <int DT, int D, int F> struct KvTile {
     typedef KvShape<D, F> S;
     static constexpr int PDT = F == W4A4_KV_INT8 ? W4A4_BF16 : DT;  // type of the second product
     struct __attribute__((aligned(4))) KRun { uint32_t w[S::KW / 4]; };
-    struct __attribute__((aligned(S::VB < 4 ? 2 : 4))) VRun { uint16_t w[S::VB / 2]; };
     typedef typename std::conditional<S::VB == 2, uint16_t, DwordRun<(S::VB + 3) / 4>>::type VLoad;
     KRun k[2][S::NL];
     VLoad v[8];
@@ -454,8 +453,6 @@ template <int DT, int D, int F, int RT> struct AttnRows {
             for (int i = 0; i < S::VE; ++i) acc[t][i] = mma32<PDT>(v[i], lo[t], acc[t][i]);
 #pragma unroll
             for (int i = 0; i < S::VE; ++i) acc[t][i] = mma32<PDT>(v[i], hi[t], acc[t][i]);
-        }
-        if constexpr (RT > 1) {
         }
     }
 

@@ -273,7 +273,7 @@ struct AttnArgs {
     // parts of each (sequence, head) in stat and part are then prefix_splits of the prefix and `splits` of its own
     KvPages kv;
     const int32_t *prefix_table, *prefix_len;
-    int prefix_width, prefix_splits, prefix_tiles, prefix_row_waves, prefix_row_runs, prefix_row_blocks;
+    int prefix_width, prefix_splits, prefix_row_waves, prefix_row_runs, prefix_row_blocks;
     int prefix_turns, own_turns;  // set by the launcher
 };
 // rows as they are into the quantized cache, and back (k_kvq.hip)
@@ -293,9 +293,9 @@ struct AttnPlan {
 AttnPlan attn_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks);
 int launch_paged_attn(AttnArgs a, int dtype, int D, hipStream_t s);
 // How a shared prefix is cut: row tiles of 16 per wave, waves of a workgroup on different rows, runs of row blocks and
-// the blocks of a run, parts of the keys and the least tiles of a part.
+// the blocks of a run, parts of the keys.
 struct PrefixPlan {
-    int rt, row_waves, row_runs, row_blocks, splits, tiles;
+    int rt, row_waves, row_runs, row_blocks, splits;
 };
 AttnPlan kv_plan(int B, int heads, int kv_heads, int max_len, int window, int sinks, bool shared);
 PrefixPlan prefix_plan(int B, int heads, int kv_heads, int max_prefix);
