@@ -492,7 +492,9 @@ int w4a4_paged_attn_decode(const void *q, int dtype, int B, int heads, int kv_he
  * w4a4_paged_attn_decode_quant: w4a4_paged_attn_decode over such a cache: the values above in the same formula, sums in
  * fp32, nothing rounded before the end but the weights p, which go in as two 16-bit parts: 2^-17 of each is dropped over
  * int8 and for bf16; for fp16 over the other formats 2^-22 of each, and up to 2^-39 of the sequence's largest. Workspace:
- * w4a4_paged_attn_quant_workspace_bytes. What is not visible may hold anything, scales included.
+ * w4a4_paged_attn_quant_workspace_bytes. What is not visible may hold anything, scales included. The weights are relative
+ * to a maximum that may lag behind by 2^8, and a sequence's sum of weights times values has to stay in fp32's range: it
+ * does for bf16 values up to 2^88, and for all of fp16.
  *
  * w4a4_paged_attn_shared: the attention of one new token per sequence for a batch whose sequences all begin with the
  * same tokens. Sequence b sees the prefix_len[0] tokens of the pages in prefix_table[prefix_width], and after them the

@@ -129,3 +129,23 @@ def test_adapters_in_several_launches(M, R):
     for rows in (slice(0, 64), slice(M - 64, M)):
         none = ids[rows] < 0
         assert torch.equal(out[rows][none], Y[rows][none]) and not torch.equal(out[rows][~none], Y[rows][~none])
+
+
+@pytest.mark.parametrize("kind", ["none", "int8", "fp4"])
+@pytest.mark.parametrize("power", [88, -40])
+def test_values_far_from_one(power, kind):
+    """bf16 values up to 2^88 and far below one, behind scores that grow from tile to tile: a power of two on all values is
+    that power on the results, bit for bit."""
+    import torch
+    b = Batch([900, 33, 0, 2500], 8, 2, 128, 16, "bf16", kind, prefix=777, seed=9, qscale=6.0)
+    calls = [b.shared] + ([lambda: bd.paged_attn_decode_quant(b.q, b.cache, b.table, b.ld)] if kind != "none" else [])
+    want = [f() for f in calls]
+    b.check(want[0])
+    shift = power - int(np.ceil(np.log2(np.nanmax(np.abs(b.values[1])))))
+    if kind == "fp4":
+        b.cache[3].add_((b.cache[3] != 255).to(torch.uint8) * (shift % 256))
+    else:
+        b.cache[1 if kind == "none" else 3].mul_(2.0 ** shift)
+    for f, w in zip(calls, want):
+        got = f()
+        assert bool(got.isfinite().all()) and torch.equal(got.double(), w.double() * 2.0 ** shift)
